@@ -276,7 +276,7 @@ def _prep_sample(case, g):
     u = torch.rand(n, device=DEV, generator=g)
     return {"op": "sample", "logits": z, "u": u, "temperature": temp, "top_k": top_k, "top_p": top_p, "min_p": min_p,
             "token": torch.empty(n, dtype=torch.int32, device=DEV), "logprob": torch.empty(n, device=DEV),
-            "kept": torch.empty(n, dtype=torch.int32, device=DEV), "ws": None}
+            "kept": torch.empty(n, dtype=torch.int32, device=DEV)}
 
 
 # ----------------------------------------------------------------------------- one pass
@@ -369,8 +369,8 @@ def _plain_attn(s):
 
 
 def _own_sample(B, s):
-    s["ws"] = B.kvc_sample(logits=s["logits"], u=s["u"], temperature=s["temperature"], top_k=s["top_k"], top_p=s["top_p"],
-                           min_p=s["min_p"], token=s["token"], logprob=s["logprob"], kept=s["kept"], workspace=s["ws"])
+    B.kvc_sample(logits=s["logits"], u=s["u"], temperature=s["temperature"], top_k=s["top_k"], top_p=s["top_p"],
+                 min_p=s["min_p"], token=s["token"], logprob=s["logprob"], kept=s["kept"])
     return s["token"], s["logprob"], s["kept"]
 
 
