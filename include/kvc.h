@@ -553,9 +553,129 @@ typedef struct {
   float* H;
 } kvc_lmhead_entropy_args;
 
+/* ------------------------------------------------------------------------
+ * A batch that answers from one compressed prompt.  The prompt is compressed once
+ * (kvc_score .. kvc_merge) and its cache [L][Hkv][k_cap][d] is shared by every sequence;
+ * what a sequence generates lives in pages of its own.  A page holds `page` tokens of one
+ * (sequence, layer) row, because budgets differ by layer: K and V pools are
+ * [n_pages][Hkv][page][d] in any strides (kvc_kv with s_batch = elements between pages and
+ * s_layer unused), slot s is token s % page of page s / page.  The cited pages have
+ * no counterpart of this part: it is an interface addition of the library.  One decode step:
+ *   kvc_page_tables (the rows' new slots) -> kvc_page_append (their K and V) ->
+ *   kvc_prefix_decode_attn -> kvc_sample (the next token from the step's logits).
+ * ---------------------------------------------------------------------- */
+
+/* kvc_page_tables: page tables and slot maps from row lengths, on the device.
+ * Row r holds len[r] tokens in its first ceil(len[r] / page) table entries and is to hold
+ * len_new[r].  Pages it lacks are taken from the ring of free pages (at its head, in row
+ * order, ascending entries), pages it no longer needs join the ring (at its tail, in row
+ * order, ascending entries); pages given back in a call are not handed out in the same
+ * call.  Only entries [ceil(len / page), ceil(len_new / page)) of a table row are written.
+ *   slots       receives the slots of the new tokens len[r] <= t < len_new[r], row after row,
+ *               then -1 up to slots_cap (kvc_page_append skips them)
+ *   slot_start  receives each row's first index in slots and, last, their number
+ * All or nothing: if the free pages do not suffice, a length lies outside
+ * [0, max_pages * page], the new tokens exceed slots_cap (when slots is given) or the
+ * ring's state is not one of a ring, nothing but slots (all -1), slot_start (all 0),
+ * len_out (= len) and state_out (= state) is written, and the status word records it
+ * (KVC_ERR_DEVICE).  A page id outside the pool in a table or the ring is recorded too; it
+ * is not used (slots of it are -1). */
+typedef struct {
+  int rows;                /* table rows, e.g. batch * layers; 1 .. 2^20 */
+  int page;                /* tokens per page: 16, 32, 64, 128 or 256 */
+  int n_pages;             /* pages of the pool; n_pages * page < 2^31 */
+  int max_pages;           /* entries a table row can hold */
+  const int32_t* len;      /* [rows] */
+  const int32_t* len_new;  /* [rows] */
+  int32_t* table;          /* rows of table_s_row elements */
+  int64_t table_s_row;     /* >= max_pages */
+  int32_t* ring;           /* [n_pages] free page ids: ring[(head + i) % n_pages], i < count */
+  const int32_t* state;    /* [2]: head, count */
+  int32_t* state_out;      /* [2]: the state after the call; may be state */
+  int32_t* len_out;        /* optional [rows]: receives len_new; may be len */
+  int32_t* slots;          /* optional [slots_cap] */
+  int slots_cap;
+  int32_t* slot_start;     /* optional [rows + 1] */
+} kvc_page_tables_args;
+
+/* kvc_page_append: token t < T enters slot slots[t] of the K and V pools (every KV head).
+ * A negative slot is skipped; one past the pool is skipped and recorded in the status
+ * word.  Slots of one call should differ: of two tokens in one slot either may win, for each
+ * 16 bytes on its own. */
+typedef struct {
+  int T;                   /* >= 0 */
+  int page, n_pages;
+  kvc_kv k, v;             /* sources: token t, head g at t*s_tok + g*s_head (s_batch, s_layer unused) */
+  kvc_kv K, V;             /* pools, one dtype with k and v */
+  const int32_t* slots;    /* [T] */
+} kvc_page_append_args;
+
+/* kvc_prefix_decode_attn: decode attention of a batch that shares a prompt's cache.
+ *   o(b,l,h) = sum_i softmax_i(z) v_i over the prompt's rows i < len_prefix[l] of layer l,
+ *              z_i = q k_i * scale + alpha_c * log R_i   ([SelKV] Core component 2), and the
+ *              len[b][l] rows of the sequence's own cache, z_i = q k_i * scale
+ * The prompt's keys and values are read once for the batch, not once a sequence.  The own
+ * cache is paged (table != NULL: K and V are pools, table row (b, l) as kvc_page_tables
+ * fills it) or contiguous ([B][L][Hkv][>= max_len][d], as kvc_append fills it).  A row with
+ * no key at all gets o = 0 and lse = -infinity.  A length outside its bound is clamped to it,
+ * a page id outside the pool reads as rows of zeros (keys and values); both are recorded in
+ * the status word.  Rows behind a length may hold anything. */
+typedef struct {
+  int batch;
+  const void* q;           /* [B][L][Hq][d] contiguous */
+  kvc_dtype q_dtype;
+  kvc_kv K_prefix, V_prefix; /* [L][Hkv][>= max_len_prefix][d] (s_batch unused); ptr NULL: no prompt */
+  const int32_t* len_prefix; /* [L] device (kvc_select's k_out) */
+  int max_len_prefix;      /* host upper bound on every len_prefix[l] */
+  const float* R;          /* NULL: no bias; else R(l,g,i) = R[l*R_s_layer + g*R_s_head + i] */
+  int64_t R_s_layer, R_s_head;
+  float alpha_c;
+  float scale;             /* 0 selects 1/sqrt(head_dim) */
+  kvc_kv K, V;             /* the sequences' own rows; ptr NULL: none */
+  const int32_t* len;      /* [B][L] device */
+  int max_len;             /* host upper bound on every len[b][l] */
+  const int32_t* table;    /* NULL: contiguous; else entry j of row (b, l) at
+                              table[b*table_s_batch + l*table_s_layer + j], j < ceil(max_len / page) */
+  int64_t table_s_batch, table_s_layer;
+  int page, n_pages;
+  float* o;                /* [B][L][Hq][d] fp32 */
+  float* lse;              /* optional: natural-log sum-exp at lse[((b*L + l)*Hq + h) * lse_stride] */
+  int64_t lse_stride;      /* 0 or 1: contiguous */
+} kvc_prefix_decode_args;
+
+/* kvc_sample: the next token of every row from its logits and a given random number.
+ * With z the row's logits (NaN counts as -infinity), p_i ~ exp((z_i - max z) / temperature):
+ *   order   by logit downwards, equal logits by index upwards
+ *   top_k   only the first top_k tokens of that order stay              (<= 0: all)
+ *   top_p   of these, the shortest head of the order whose share of their mass is at least
+ *           top_p, never less than one token                            (>= 1 or NaN: all)
+ *   min_p   of these, tokens with p_i >= min_p * max p                  (<= 0 or NaN: all)
+ *   token   the smallest index i whose cumulative mass, kept tokens in index order, exceeds
+ *           u * the kept mass; u is clamped to [0, 1 - 2^-24], NaN counts as 0
+ * temperature <= 0 or NaN takes the first token of the order.  Logits of +infinity share the
+ * mass alone; a token of logit -infinity is never kept; a row that holds nothing else gets
+ * token -1, kept 0 and logprob -infinity.  Masses are summed to about 40 bits and more, in an
+ * order that does not depend on timing: equal calls give equal tokens. */
+typedef struct {
+  int n;                   /* rows */
+  int V;                   /* vocabulary, 1 .. 262144 */
+  const void* logits;      /* [n] rows, row_stride elements apart, any alignment of the dtype */
+  kvc_dtype dtype;
+  int64_t row_stride;      /* >= V */
+  const float* u;          /* [n] in [0, 1) */
+  const float* temperature;  /* [n], NULL: 1 */
+  const int32_t* top_k;    /* [n], NULL: off */
+  const float* top_p;      /* [n], NULL: off */
+  const float* min_p;      /* [n], NULL: off */
+  int32_t* token;          /* [n] */
+  float* logprob;          /* optional [n]: log of the token's share of the kept mass */
+  int32_t* kept;           /* optional [n]: tokens kept */
+} kvc_sample_args;
+
 /* Operation ids for kvc_workspace_size. */
 enum { KVC_OP_SCORE = 0, KVC_OP_SELECT = 1, KVC_OP_COMPACT = 2, KVC_OP_MERGE = 3,
-       KVC_OP_DECODE = 4, KVC_OP_RECOMPRESS = 5, KVC_OP_SPARSE_DECODE = 6, KVC_OP_LMHEAD_ENTROPY = 7 };
+       KVC_OP_DECODE = 4, KVC_OP_RECOMPRESS = 5, KVC_OP_SPARSE_DECODE = 6, KVC_OP_LMHEAD_ENTROPY = 7,
+       KVC_OP_PAGE_TABLES = 8, KVC_OP_PREFIX_DECODE = 9 };
 
 /* Bytes of workspace the operation needs for these arguments (args points to
  * the operation's argument struct).  0 is a valid answer. */
@@ -579,6 +699,11 @@ kvc_status kvc_recas_control(const kvc_model* m, const kvc_recas_control_args* a
 kvc_status kvc_sparse_decode(const kvc_model* m, const kvc_sparse_decode_args* a, void* ws, size_t ws_bytes,
                              kvc_stream_t stream);
 kvc_status kvc_lmhead_entropy(const kvc_lmhead_entropy_args* a, void* ws, size_t ws_bytes, kvc_stream_t stream);
+kvc_status kvc_page_tables(const kvc_page_tables_args* a, void* ws, size_t ws_bytes, kvc_stream_t stream);
+kvc_status kvc_page_append(const kvc_model* m, const kvc_page_append_args* a, kvc_stream_t stream);
+kvc_status kvc_prefix_decode_attn(const kvc_model* m, const kvc_prefix_decode_args* a, void* ws, size_t ws_bytes,
+                                  kvc_stream_t stream);
+kvc_status kvc_sample(const kvc_sample_args* a, kvc_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * kvc_decode_attn_noalloc: kvc_decode_attn for callers that cannot allocate.

@@ -22,7 +22,7 @@ SCORE_INFOKV, SCORE_VATP, SCORE_ATTN = 0, 1, 2
 SEL_PER_KV_HEAD, SEL_GQA_UNION = 0, 1
 BUDGET_UNIFORM, BUDGET_EXPLICIT, BUDGET_ADAPTIVE = 0, 1, 2
 (OP_SCORE, OP_SELECT, OP_COMPACT, OP_MERGE, OP_DECODE, OP_RECOMPRESS, OP_SPARSE_DECODE,
- OP_LMHEAD_ENTROPY) = range(8)
+ OP_LMHEAD_ENTROPY, OP_PAGE_TABLES, OP_PREFIX_DECODE) = range(10)
 STATUS_NAMES = {0: "KVC_OK", 1: "KVC_ERR_ARG", 2: "KVC_ERR_UNSUPPORTED", 3: "KVC_ERR_WORKSPACE",
                 4: "KVC_ERR_CUDA", 5: "KVC_ERR_TIMEOUT", 6: "KVC_ERR_DEVICE"}
 
@@ -30,7 +30,7 @@ EXPORTED = ["kvc_workspace_size", "kvc_score", "kvc_select", "kvc_compact", "kvc
             "kvc_rope_reposition", "kvc_decode_attn", "kvc_recompress", "kvc_append",
             "kvc_recas_calibrate", "kvc_recas_control", "kvc_sparse_decode", "kvc_lmhead_entropy",
             "kvc_check_status", "kvc_last_error", "kvc_version", "kvc_decode_attn_noalloc",
-            "kvc_launch_count"]
+            "kvc_launch_count", "kvc_page_tables", "kvc_page_append", "kvc_prefix_decode_attn", "kvc_sample"]
 
 
 class KvcError(RuntimeError):
@@ -140,6 +140,33 @@ class LmheadEntropyArgs(C.Structure):
                 ("H", C.c_void_p)]
 
 
+class PageTablesArgs(C.Structure):
+    _fields_ = [("rows", C.c_int), ("page", C.c_int), ("n_pages", C.c_int), ("max_pages", C.c_int),
+                ("len", C.c_void_p), ("len_new", C.c_void_p), ("table", C.c_void_p), ("table_s_row", C.c_int64),
+                ("ring", C.c_void_p), ("state", C.c_void_p), ("state_out", C.c_void_p), ("len_out", C.c_void_p),
+                ("slots", C.c_void_p), ("slots_cap", C.c_int), ("slot_start", C.c_void_p)]
+
+
+class PageAppendArgs(C.Structure):
+    _fields_ = [("T", C.c_int), ("page", C.c_int), ("n_pages", C.c_int), ("k", KV), ("v", KV), ("K", KV), ("V", KV),
+                ("slots", C.c_void_p)]
+
+
+class PrefixDecodeArgs(C.Structure):
+    _fields_ = [("batch", C.c_int), ("q", C.c_void_p), ("q_dtype", C.c_int), ("K_prefix", KV), ("V_prefix", KV),
+                ("len_prefix", C.c_void_p), ("max_len_prefix", C.c_int), ("R", C.c_void_p), ("R_s_layer", C.c_int64),
+                ("R_s_head", C.c_int64), ("alpha_c", C.c_float), ("scale", C.c_float), ("K", KV), ("V", KV),
+                ("len", C.c_void_p), ("max_len", C.c_int), ("table", C.c_void_p), ("table_s_batch", C.c_int64),
+                ("table_s_layer", C.c_int64), ("page", C.c_int), ("n_pages", C.c_int), ("o", C.c_void_p),
+                ("lse", C.c_void_p), ("lse_stride", C.c_int64)]
+
+
+class SampleArgs(C.Structure):
+    _fields_ = [("n", C.c_int), ("V", C.c_int), ("logits", C.c_void_p), ("dtype", C.c_int), ("row_stride", C.c_int64),
+                ("u", C.c_void_p), ("temperature", C.c_void_p), ("top_k", C.c_void_p), ("top_p", C.c_void_p),
+                ("min_p", C.c_void_p), ("token", C.c_void_p), ("logprob", C.c_void_p), ("kept", C.c_void_p)]
+
+
 RECAS_RING = 256
 # kvc_recas_cal as float64 words: sum_delta, sum_x, c, q, (count, head as two int32), ring
 RECAS_STATE_WORDS = 5 + RECAS_RING
@@ -198,6 +225,12 @@ def lib():
         L.kvc_sparse_decode.restype = C.c_int
         L.kvc_lmhead_entropy.argtypes = [C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]
         L.kvc_lmhead_entropy.restype = C.c_int
+        L.kvc_page_tables.argtypes = [C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]
+        L.kvc_page_append.argtypes = [C.c_void_p, C.c_void_p, C.c_void_p]
+        L.kvc_prefix_decode_attn.argtypes = [C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]
+        L.kvc_sample.argtypes = [C.c_void_p, C.c_void_p]
+        for name in ("kvc_page_tables", "kvc_page_append", "kvc_prefix_decode_attn", "kvc_sample"):
+            getattr(L, name).restype = C.c_int
         for name in ("kvc_recas_calibrate", "kvc_recas_control"):
             getattr(L, name).argtypes = [C.c_void_p, C.c_void_p, C.c_void_p]
             getattr(L, name).restype = C.c_int
@@ -661,6 +694,203 @@ def kvc_append(m: Model, *, k, v, K, V, lens, pos: int, side_pos=None, side_H=No
             raise ValueError("K2 and V2 must have the dtype of K")
         a.K2, a.V2, a.len2, a.cap2 = kv(K2), kv(V2), _i32(lens2, "lens2"), K2.shape[-2]
     _check(lib().kvc_append(C.byref(m), C.byref(a), _stream(stream)))
+
+
+# --------------------------------------------------------------------------- a batch on one prompt
+
+def _one_device(*tensors):
+    """Every tensor given lives on the current CUDA device (the library launches there)."""
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.device.index != dev):
+            raise ValueError(f"tensor on {t.device}: device tensors of the current device (cuda:{dev}) required")
+
+
+def _flat(t: Optional[torch.Tensor], name: str, dtype, n: int) -> Optional[int]:
+    """Address of a contiguous tensor of n elements."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with {n} elements")
+    return t.data_ptr()
+
+
+def _own_ws(op, m, args, workspace, device, stream):
+    """The workspace (None where none is needed); one allocated here is held for `stream`."""
+    need = workspace_size(op, m, args)
+    if workspace is not None:
+        if workspace.device != device or not workspace.is_contiguous() or workspace.element_size() * workspace.numel() < need:
+            raise ValueError(f"workspace must be contiguous device memory of {need} bytes")
+        return workspace, need
+    if need == 0:
+        return None, 0
+    workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    if stream is not None:
+        workspace.record_stream(stream)
+    return workspace, need
+
+
+def _pool(t: torch.Tensor, H: int, d: int, name: str) -> KV:
+    """KV descriptor of a page pool [n_pages][Hkv][page][d] in any strides with contiguous rows."""
+    if t.dim() != 4 or t.shape[1] != H or t.shape[3] != d or t.stride(3) != 1:
+        raise ValueError(f"{name} must be [n_pages][{H}][page][{d}] with contiguous rows")
+    sp, sh, st = t.stride()[:3]
+    if t.shape[0] == 1:
+        sp = t.shape[1] * t.shape[2] * d
+    if H == 1:
+        sh = t.shape[2] * d
+    return KV(t.data_ptr(), _dt(t), sp, 0, sh, st)
+
+
+def page_tables_args(*, lens, lens_new, table, ring, state, page: int, state_out=None, lens_out=None, slots=None,
+                     slot_start=None) -> PageTablesArgs:
+    """Argument struct of kvc_page_tables."""
+    _one_device(lens, lens_new, table, ring, state, state_out, lens_out, slots, slot_start)
+    rows = lens.numel()
+    tb = table.flatten(0, -2) if table.dim() > 2 and table.is_contiguous() else table
+    if tb.dtype != torch.int32 or tb.dim() != 2 or tb.shape[0] != rows or tb.stride(1) != 1:
+        raise ValueError("table must be int32 with one row of entries per length (more than two dimensions: contiguous)")
+    a = PageTablesArgs()
+    a.rows, a.page, a.n_pages, a.max_pages = rows, page, ring.numel(), tb.shape[1]
+    a.len, a.len_new = _flat(lens, "lens", torch.int32, rows), _flat(lens_new, "lens_new", torch.int32, rows)
+    a.table, a.table_s_row = tb.data_ptr(), tb.stride(0) if rows > 1 else tb.shape[1]
+    a.ring, a.state = _flat(ring, "ring", torch.int32, ring.numel()), _flat(state, "state", torch.int32, 2)
+    a.state_out = a.state if state_out is None else _flat(state_out, "state_out", torch.int32, 2)
+    a.len_out = _flat(lens_out, "lens_out", torch.int32, rows)
+    if slots is not None:
+        a.slots, a.slots_cap = _flat(slots, "slots", torch.int32, slots.numel()), slots.numel()
+    a.slot_start = _flat(slot_start, "slot_start", torch.int32, rows + 1)
+    return a
+
+
+def kvc_page_tables(*, workspace=None, stream=None, **kw):
+    """Page tables and slot maps from row lengths (see kvc.h): every row of `table` (one per
+    length, e.g. [B][L][max_pages] for lens [B][L]) grows or shrinks from lens to lens_new tokens,
+    with pages from and to the ring of free ones; state [2] = (head, count) is updated in place
+    unless state_out is given, lens_out (may be lens) receives lens_new, slots the new tokens'
+    slots, slot_start [rows + 1] where each row's begin.  Returns the workspace (None out of place)."""
+    a = page_tables_args(**kw)
+    ws, need = _own_ws(OP_PAGE_TABLES, None, a, workspace, kw["lens"].device, stream)
+    _check(lib().kvc_page_tables(C.byref(a), ws.data_ptr() if ws is not None else None, need, _stream(stream)))
+    return ws
+
+
+def kvc_page_append(m: Model, *, k, v, K, V, slots, stream=None):
+    """Token t's rows k[t], v[t] ([T][Hkv][d], any strides with contiguous rows) into slot slots[t]
+    of the pools K, V [n_pages][Hkv][page][d]; negative slots are skipped."""
+    _one_device(k, v, K, V, slots)
+    H, d = m.n_kv_heads, m.head_dim
+    a = PageAppendArgs()
+    if k.dim() != 3 or k.shape != v.shape or k.shape[1] != H or k.shape[2] != d or k.stride(2) != 1 or v.stride(2) != 1:
+        raise ValueError(f"k and v must be [T][{H}][{d}] with contiguous rows")
+    if K.shape != V.shape:
+        raise ValueError("K and V must have one shape")
+    T = k.shape[0]
+    a.T, a.page, a.n_pages = T, K.shape[2], K.shape[0]
+
+    def src(t):
+        return KV(t.data_ptr(), _dt(t), 0, 0, t.stride(1) if H > 1 else d, t.stride(0) if T > 1 else H * d)
+
+    if T == 0:
+        return
+    a.k, a.v, a.K, a.V = src(k), src(v), _pool(K, H, d, "K"), _pool(V, H, d, "V")
+    a.slots = _flat(slots, "slots", torch.int32, T)
+    _check(lib().kvc_page_append(C.byref(m), C.byref(a), _stream(stream)))
+
+
+def _strides_of(t: torch.Tensor, shape, d: int, name: str):
+    """Strides of a cache tensor whose leading sizes must be `shape` (tokens free), rows contiguous."""
+    if t.dim() != len(shape) + 2 or tuple(t.shape[:-2]) != tuple(shape) or t.shape[-1] != d or t.stride(-1) != 1:
+        raise ValueError(f"{name} must be {''.join(f'[{x}]' for x in shape)}[tokens][{d}] with contiguous rows")
+    st = list(t.stride()[:-1])
+    for i in range(len(st) - 1, -1, -1):      # a dimension of one element gets the stride its neighbour implies
+        if t.shape[i] == 1:
+            st[i] = d if i == len(st) - 1 else st[i + 1] * t.shape[i + 1]
+    return st
+
+
+def prefix_decode_args(m: Model, *, q, o, K_prefix=None, V_prefix=None, lens_prefix=None, max_len_prefix: int = 0,
+                       R=None, alpha_c: float = 1.0, scale: float = 0.0, K=None, V=None, lens=None, max_len: int = 0,
+                       table=None, lse=None) -> PrefixDecodeArgs:
+    """Argument struct of kvc_prefix_decode_attn."""
+    _one_device(q, o, K_prefix, V_prefix, lens_prefix, R, K, V, lens, table, lse)
+    L, Hq, H, d = m.n_layers, m.n_q_heads, m.n_kv_heads, m.head_dim
+    if q.dim() != 4 or tuple(q.shape[1:]) != (L, Hq, d) or not q.is_contiguous():
+        raise ValueError(f"q must be contiguous [B][{L}][{Hq}][{d}]")
+    a = PrefixDecodeArgs()
+    B_ = q.shape[0]
+    a.batch, a.q, a.q_dtype = B_, q.data_ptr(), _dt(q)
+    a.o = _flat(o, "o", torch.float32, q.numel())
+    a.alpha_c, a.scale = alpha_c, scale
+    if K_prefix is not None:
+        sk, sv = _strides_of(K_prefix, (L, H), d, "K_prefix"), _strides_of(V_prefix, (L, H), d, "V_prefix")
+        if max_len_prefix > min(K_prefix.shape[2], V_prefix.shape[2]):
+            raise ValueError("max_len_prefix above the prompt cache's rows")
+        a.K_prefix = KV(K_prefix.data_ptr(), _dt(K_prefix), 0, *sk)
+        a.V_prefix = KV(V_prefix.data_ptr(), _dt(V_prefix), 0, *sv)
+        a.len_prefix, a.max_len_prefix = _flat(lens_prefix, "lens_prefix", torch.int32, L), max_len_prefix
+        if R is not None:
+            if R.dtype != torch.float32 or R.dim() != 3 or tuple(R.shape[:2]) != (L, H) or R.shape[2] < max_len_prefix \
+                    or R.stride(2) != 1:
+                raise ValueError(f"R must be fp32 [{L}][{H}][>= max_len_prefix] with contiguous rows")
+            a.R, a.R_s_layer, a.R_s_head = R.data_ptr(), R.stride(0), R.stride(1)
+    elif R is not None:
+        raise ValueError("R belongs to a prompt")
+    if K is not None:
+        if table is None:
+            sk, sv = _strides_of(K, (B_, L, H), d, "K"), _strides_of(V, (B_, L, H), d, "V")
+            if max_len > min(K.shape[3], V.shape[3]):
+                raise ValueError("max_len above the cache's rows")
+            a.K, a.V = KV(K.data_ptr(), _dt(K), *sk), KV(V.data_ptr(), _dt(V), *sv)
+        else:
+            if K.shape != V.shape:
+                raise ValueError("K and V must have one shape")
+            a.K, a.V, a.page, a.n_pages = _pool(K, H, d, "K"), _pool(V, H, d, "V"), K.shape[2], K.shape[0]
+            if table.dtype != torch.int32 or table.dim() != 3 or tuple(table.shape[:2]) != (B_, L) \
+                    or table.stride(2) != 1 or table.shape[2] * a.page < max_len:
+                raise ValueError(f"table must be int32 [{B_}][{L}][>= max_len / page] with contiguous rows")
+            a.table, a.table_s_batch, a.table_s_layer = table.data_ptr(), table.stride(0), table.stride(1)
+        a.len, a.max_len = _flat(lens, "lens", torch.int32, B_ * L), max_len
+    if lse is not None:
+        if tuple(lse.shape) != (B_, L, Hq):
+            raise ValueError(f"lse must be [{B_}][{L}][{Hq}]")
+        a.lse, a.lse_stride = _lse(lse)
+    return a
+
+
+def kvc_prefix_decode_attn(m: Model, *, workspace=None, stream=None, **kw):
+    """Decode attention of a batch that shares a prompt's cache (see kvc.h): q [B][L][Hq][d] over
+    K_prefix, V_prefix [L][Hkv][>= max_len_prefix][d] (lens_prefix [L], optional R) and each
+    sequence's own rows, in pages (K, V [n_pages][Hkv][page][d], table [B][L][entries]) or
+    contiguous (K, V [B][L][Hkv][cap][d]), lens [B][L] -> o (fp32), optional lse.  Returns the
+    workspace; without one given, one is allocated."""
+    a = prefix_decode_args(m, **kw)
+    ws, need = _own_ws(OP_PREFIX_DECODE, m, a, workspace, kw["q"].device, stream)
+    _check(lib().kvc_prefix_decode_attn(C.byref(m), C.byref(a), ws.data_ptr(), ws.element_size() * ws.numel(),
+                                        _stream(stream)))
+    return ws
+
+
+def kvc_sample(*, logits, u, token, temperature=None, top_k=None, top_p=None, min_p=None, logprob=None, kept=None,
+               stream=None):
+    """The next token [n] int32 of every row of logits [n][V] (bf16 / fp32, rows any distance apart)
+    from u [n] in [0, 1): temperature, top_k, top_p and min_p per row, each optional (see kvc.h);
+    optional logprob [n] and the number of tokens kept [n]."""
+    _one_device(logits, u, token, temperature, top_k, top_p, min_p, logprob, kept)
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be [n][V] with contiguous rows")
+    n, V = logits.shape
+    f32, i32 = torch.float32, torch.int32
+    a = SampleArgs()
+    a.n, a.V, a.logits, a.dtype = n, V, logits.data_ptr(), _dt(logits)
+    a.row_stride = logits.stride(0) if n > 1 else V
+    a.u, a.temperature = _flat(u, "u", f32, n), _flat(temperature, "temperature", f32, n)
+    a.top_k, a.top_p = _flat(top_k, "top_k", i32, n), _flat(top_p, "top_p", f32, n)
+    a.min_p, a.token = _flat(min_p, "min_p", f32, n), _flat(token, "token", i32, n)
+    a.logprob, a.kept = _flat(logprob, "logprob", f32, n), _flat(kept, "kept", i32, n)
+    _check(lib().kvc_sample(C.byref(a), _stream(stream)))
 
 
 def kvc_check_status(stream=None) -> int:

@@ -1073,6 +1073,207 @@ static kvc_status run_append(const kvc_model* m, const kvc_append_args* a, cudaS
   return KVC_OK;
 }
 
+// ----------------------------------------------------------------- pages
+static int page_shift(int page) {
+  switch (page) {
+    case 16: return 4;
+    case 32: return 5;
+    case 64: return 6;
+    case 128: return 7;
+    case 256: return 8;
+  }
+  return -1;
+}
+
+static kvc_status check_pool(int page, int n_pages) {
+  if (page_shift(page) < 0) return fail(KVC_ERR_UNSUPPORTED, "page %d (supported: 16, 32, 64, 128, 256)", page);
+  if (n_pages < 1 || (int64_t)n_pages * page > INT_MAX)
+    return fail(KVC_ERR_ARG, "n_pages must be >= 1 and n_pages * page below 2^31");
+  return KVC_OK;
+}
+
+static bool overlap(const void* a, size_t an, const void* b, size_t bn) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return a && b && x < y + bn && y < x + an;
+}
+
+static kvc_status check_page_tables(const kvc_page_tables_args* a) {
+  if (!a) return fail(KVC_ERR_ARG, "args is NULL");
+  kvc_status s = check_pool(a->page, a->n_pages);
+  if (s) return s;
+  if (a->rows < 1 || a->rows > (1 << 20)) return fail(KVC_ERR_ARG, "rows must be in [1, 2^20]");
+  if (a->max_pages < 1 || a->table_s_row < a->max_pages)
+    return fail(KVC_ERR_ARG, "max_pages must be >= 1 and table_s_row at least max_pages");
+  if (!a->len || !a->len_new || !a->table || !a->ring || !a->state || !a->state_out)
+    return fail(KVC_ERR_ARG, "len, len_new, table, ring, state and state_out are required");
+  if (a->slots && a->slots_cap < 0) return fail(KVC_ERR_ARG, "slots_cap must be >= 0");
+  const size_t nb = (size_t)a->rows * 4;
+  if ((a->len_out != a->len && overlap(a->len_out, nb, a->len, nb)) ||
+      (a->len_out != a->len_new && overlap(a->len_out, nb, a->len_new, nb)))
+    return fail(KVC_ERR_ARG, "len_out must be len, len_new or apart from both");
+  if (a->state_out != a->state && overlap(a->state_out, 8, a->state, 8))
+    return fail(KVC_ERR_ARG, "state_out must be state or apart from it");
+  return KVC_OK;
+}
+
+// In place (lengths or state written over their inputs) the verdict goes through the workspace.
+static size_t page_tables_ws(const kvc_page_tables_args* a) {
+  const bool in_place = a->state_out == a->state || (a->len_out && (a->len_out == a->len || a->len_out == a->len_new));
+  return in_place ? 256 : 0;
+}
+
+static kvc_status run_page_tables(const kvc_page_tables_args* a, void* ws, size_t ws_bytes, cudaStream_t st) {
+  kvc_status s = check_page_tables(a);
+  if (s) return s;
+  const size_t need = page_tables_ws(a);
+  if (need && (!ws || ws_bytes < need)) return fail(KVC_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
+  if (need && (uintptr_t)ws % 4) return fail(KVC_ERR_ARG, "workspace not 4-byte aligned");
+  PageTablesParams p{};
+  p.rows = a->rows; p.shift = page_shift(a->page); p.n_pages = a->n_pages; p.max_pages = a->max_pages;
+  p.len = a->len; p.len_new = a->len_new; p.table = a->table; p.table_row = a->table_s_row;
+  p.ring = a->ring; p.state = a->state; p.state_out = a->state_out; p.len_out = a->len_out;
+  p.slots = a->slots; p.slots_cap = a->slots ? a->slots_cap : 0; p.slot_start = a->slot_start;
+  p.commit = need ? (int32_t*)ws : nullptr;
+  p.status = status_ptr();
+  cudaError_t e = launch_page_tables(p, st);
+  if (e) return cuda_fail(e, "page_tables");
+  return KVC_OK;
+}
+
+static kvc_status run_page_append(const kvc_model* m, const kvc_page_append_args* a, cudaStream_t st) {
+  kvc_status s = check_model(m);
+  if (s) return s;
+  if (!a) return fail(KVC_ERR_ARG, "args is NULL");
+  if ((s = check_pool(a->page, a->n_pages))) return s;
+  if (a->T < 0) return fail(KVC_ERR_ARG, "T must be >= 0");
+  const int d = m->head_dim;
+  if ((s = check_kv(a->k, "k", d, true)) || (s = check_kv(a->v, "v", d, true)) || (s = check_kv(a->K, "K", d, true)) ||
+      (s = check_kv(a->V, "V", d, true)))
+    return s;
+  if (a->k.dtype != a->K.dtype || a->v.dtype != a->K.dtype || a->V.dtype != a->K.dtype)
+    return fail(KVC_ERR_ARG, "k, v, K and V must have one dtype");
+  if (!a->slots) return fail(KVC_ERR_ARG, "slots is required");
+  if (a->T == 0) return KVC_OK;
+  PageAppendParams p{};
+  p.T = a->T; p.Hkv = m->n_kv_heads; p.vr = (int)(d * esize(a->K.dtype) / 16);
+  if ((int64_t)p.T * p.Hkv * p.vr > (1LL << 38)) return fail(KVC_ERR_UNSUPPORTED, "too many rows in one call");
+  p.shift = page_shift(a->page); p.n_pages = a->n_pages;
+  p.k = (const char*)a->k.ptr; p.kst = b2(a->k, a->k.s_tok); p.ksh = b2(a->k, a->k.s_head);
+  p.v = (const char*)a->v.ptr; p.vst = b2(a->v, a->v.s_tok); p.vsh = b2(a->v, a->v.s_head);
+  p.K = (char*)a->K.ptr; p.Ksp = b2(a->K, a->K.s_batch); p.Ksh = b2(a->K, a->K.s_head); p.Kst = b2(a->K, a->K.s_tok);
+  p.V = (char*)a->V.ptr; p.Vsp = b2(a->V, a->V.s_batch); p.Vsh = b2(a->V, a->V.s_head); p.Vst = b2(a->V, a->V.s_tok);
+  p.slots = a->slots;
+  p.status = status_ptr();
+  cudaError_t e = launch_page_append(p, st);
+  if (e) return cuda_fail(e, "page_append");
+  return KVC_OK;
+}
+
+// ----------------------------------------------------------------- shared-prompt decode
+static kvc_status check_prefix(const kvc_model* m, const kvc_prefix_decode_args* a) {
+  kvc_status s = check_model(m);
+  if (s) return s;
+  if (!a) return fail(KVC_ERR_ARG, "args is NULL");
+  const int d = m->head_dim;
+  if (m->n_q_heads / m->n_kv_heads > 8) return fail(KVC_ERR_UNSUPPORTED, "more than 8 query heads per KV head");
+  if (a->batch < 1) return fail(KVC_ERR_ARG, "batch must be >= 1");
+  if (!a->q || !a->o) return fail(KVC_ERR_ARG, "q and o are required");
+  if (!dtype_ok(a->q_dtype)) return fail(KVC_ERR_ARG, "q_dtype invalid");
+  if ((uintptr_t)a->q % 16 || (uintptr_t)a->o % 16) return fail(KVC_ERR_ARG, "q / o not 16-byte aligned");
+  if (!(a->scale >= 0.f) || std::isinf(a->scale)) return fail(KVC_ERR_ARG, "scale must be finite and >= 0");
+  if (a->lse_stride < 0) return fail(KVC_ERR_ARG, "lse_stride must be >= 0");
+  if (!a->K_prefix.ptr && !a->K.ptr) return fail(KVC_ERR_ARG, "neither a prompt nor own rows");
+  if ((int64_t)a->batch * m->n_layers * m->n_q_heads > INT_MAX / 32)
+    return fail(KVC_ERR_UNSUPPORTED, "batch * layers * query heads above 2^26");
+  if (a->K_prefix.ptr) {
+    kvc_kv k = a->K_prefix, v = a->V_prefix;
+    k.s_batch = v.s_batch = 0;
+    if ((s = check_kv(k, "K_prefix", d, true)) || (s = check_kv(v, "V_prefix", d, true))) return s;
+    if (k.dtype != v.dtype) return fail(KVC_ERR_ARG, "K_prefix and V_prefix dtypes differ");
+    if (!a->len_prefix) return fail(KVC_ERR_ARG, "len_prefix is required with a prompt");
+    if (a->max_len_prefix < 1) return fail(KVC_ERR_ARG, "max_len_prefix must be >= 1");
+    if (a->R && !std::isfinite(a->alpha_c)) return fail(KVC_ERR_ARG, "alpha_c must be finite");
+  } else if (a->R) {
+    return fail(KVC_ERR_ARG, "R belongs to a prompt");
+  }
+  if (a->K.ptr) {
+    kvc_kv k = a->K, v = a->V;
+    if (a->table) k.s_layer = v.s_layer = 0;
+    if ((s = check_kv(k, "K", d, true)) || (s = check_kv(v, "V", d, true))) return s;
+    if (k.dtype != v.dtype) return fail(KVC_ERR_ARG, "K and V dtypes differ");
+    if (a->K_prefix.ptr && k.dtype != a->K_prefix.dtype) return fail(KVC_ERR_ARG, "K and K_prefix dtypes differ");
+    if (!a->len) return fail(KVC_ERR_ARG, "len is required with own rows");
+    if (a->max_len < 1) return fail(KVC_ERR_ARG, "max_len must be >= 1");
+    if (a->table) {
+      if ((s = check_pool(a->page, a->n_pages))) return s;
+      if (a->table_s_batch < 0 || a->table_s_layer < 0) return fail(KVC_ERR_ARG, "table strides must be >= 0");
+    }
+  } else if (a->table) {
+    return fail(KVC_ERR_ARG, "table without K and V");
+  }
+  return KVC_OK;
+}
+
+static PrefixParams prefix_params(const kvc_model* m, const kvc_prefix_decode_args* a) {
+  PrefixParams p{};
+  const int d = m->head_dim;
+  p.B = a->batch; p.L = m->n_layers; p.Hq = m->n_q_heads; p.Hkv = m->n_kv_heads; p.G = p.Hq / p.Hkv; p.d = d;
+  p.q = a->q; p.qbf16 = a->q_dtype == KVC_BF16;
+  p.kbf16 = (a->K_prefix.ptr ? a->K_prefix.dtype : a->K.dtype) == KVC_BF16;
+  p.qscale = (a->scale > 0.f ? a->scale : 1.f / sqrtf((float)d)) * 1.4426950408889634f;
+  if (a->K_prefix.ptr) {
+    const kvc_kv &K = a->K_prefix, &V = a->V_prefix;
+    p.Kp = (const char*)K.ptr; p.Kpl = b2(K, K.s_layer); p.Kph = b2(K, K.s_head); p.Kpt = b2(K, K.s_tok);
+    p.Vp = (const char*)V.ptr; p.Vpl = b2(V, V.s_layer); p.Vph = b2(V, V.s_head); p.Vpt = b2(V, V.s_tok);
+    p.len_p = a->len_prefix; p.max_p = a->max_len_prefix;
+    p.R = a->R; p.Rsl = a->R_s_layer; p.Rsh = a->R_s_head; p.alpha_c = a->alpha_c;
+  }
+  if (a->K.ptr) {
+    const kvc_kv &K = a->K, &V = a->V;
+    p.K = (const char*)K.ptr; p.Ksb = b2(K, K.s_batch); p.Ksl = b2(K, K.s_layer); p.Ksh = b2(K, K.s_head); p.Kst = b2(K, K.s_tok);
+    p.V = (const char*)V.ptr; p.Vsb = b2(V, V.s_batch); p.Vsl = b2(V, V.s_layer); p.Vsh = b2(V, V.s_head); p.Vst = b2(V, V.s_tok);
+    p.len = a->len; p.max_len = a->max_len;
+    if (a->table) {
+      p.table = a->table; p.tsb = a->table_s_batch; p.tsl = a->table_s_layer;
+      p.shift = page_shift(a->page); p.n_pages = a->n_pages;
+    }
+  }
+  p.status = status_ptr();
+  p.o = a->o; p.lse = a->lse; p.lse_stride = a->lse_stride > 0 ? a->lse_stride : 1;
+  return p;
+}
+
+static kvc_status run_prefix(const kvc_model* m, const kvc_prefix_decode_args* a, void* ws, size_t ws_bytes,
+                             cudaStream_t st) {
+  kvc_status s = check_prefix(m, a);
+  if (s) return s;
+  PrefixParams p = prefix_params(m, a);
+  const size_t need = plan_prefix(p, ws);
+  if (!ws || ws_bytes < need) return fail(KVC_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
+  if ((uintptr_t)ws % 16) return fail(KVC_ERR_ARG, "workspace not 16-byte aligned");
+  cudaError_t e = launch_prefix(p, st);
+  if (e) return cuda_fail(e, "prefix_decode_attn");
+  return KVC_OK;
+}
+
+// ----------------------------------------------------------------- sampling
+static kvc_status run_sample(const kvc_sample_args* a, cudaStream_t st) {
+  if (!a) return fail(KVC_ERR_ARG, "args is NULL");
+  if (a->n < 1) return fail(KVC_ERR_ARG, "n must be >= 1");
+  if (a->V < 1 || a->V > 262144) return fail(KVC_ERR_UNSUPPORTED, "V must be in [1, 262144]");
+  if (!dtype_ok(a->dtype)) return fail(KVC_ERR_ARG, "dtype invalid");
+  if (!a->logits || !a->u || !a->token) return fail(KVC_ERR_ARG, "logits, u and token are required");
+  if ((uintptr_t)a->logits % esize(a->dtype)) return fail(KVC_ERR_ARG, "logits not aligned to their dtype");
+  if (a->n > 1 && a->row_stride < a->V) return fail(KVC_ERR_ARG, "row_stride smaller than V");
+  SampleParams p{};
+  p.n = a->n; p.V = a->V; p.bf16 = a->dtype == KVC_BF16; p.logits = a->logits; p.row_stride = a->row_stride;
+  p.u = a->u; p.temperature = a->temperature; p.top_k = a->top_k; p.top_p = a->top_p; p.min_p = a->min_p;
+  p.token = a->token; p.logprob = a->logprob; p.kept = a->kept;
+  cudaError_t e = launch_sample(p, st);
+  if (e) return cuda_fail(e, "sample");
+  return KVC_OK;
+}
+
 }  // namespace kvc
 
 // ===================================================================== C ABI
@@ -1123,6 +1324,19 @@ kvc_status kvc_workspace_size(int op, const kvc_model* m, const void* args, size
       auto a = (const kvc_lmhead_entropy_args*)args;
       if ((s = check_lmhead(a))) return s;
       *bytes = plan_lmhead(a->n, a->Dh, a->V, a->k, num_sms()).bytes;
+      return KVC_OK;
+    }
+    case KVC_OP_PAGE_TABLES: {
+      auto a = (const kvc_page_tables_args*)args;
+      if ((s = check_page_tables(a))) return s;
+      *bytes = page_tables_ws(a);
+      return KVC_OK;
+    }
+    case KVC_OP_PREFIX_DECODE: {
+      auto a = (const kvc_prefix_decode_args*)args;
+      if ((s = check_prefix(m, a))) return s;
+      PrefixParams p = prefix_params(m, a);
+      *bytes = plan_prefix(p, nullptr);
       return KVC_OK;
     }
   }
@@ -1184,6 +1398,21 @@ kvc_status kvc_sparse_decode(const kvc_model* m, const kvc_sparse_decode_args* a
 kvc_status kvc_lmhead_entropy(const kvc_lmhead_entropy_args* a, void* ws, size_t ws_bytes, kvc_stream_t stream) {
   return run_lmhead(a, ws, ws_bytes, (cudaStream_t)stream);
 }
+
+kvc_status kvc_page_tables(const kvc_page_tables_args* a, void* ws, size_t ws_bytes, kvc_stream_t stream) {
+  return run_page_tables(a, ws, ws_bytes, (cudaStream_t)stream);
+}
+
+kvc_status kvc_page_append(const kvc_model* m, const kvc_page_append_args* a, kvc_stream_t stream) {
+  return run_page_append(m, a, (cudaStream_t)stream);
+}
+
+kvc_status kvc_prefix_decode_attn(const kvc_model* m, const kvc_prefix_decode_args* a, void* ws, size_t ws_bytes,
+                                  kvc_stream_t stream) {
+  return run_prefix(m, a, ws, ws_bytes, (cudaStream_t)stream);
+}
+
+kvc_status kvc_sample(const kvc_sample_args* a, kvc_stream_t stream) { return run_sample(a, (cudaStream_t)stream); }
 
 kvc_status kvc_check_status(kvc_stream_t stream, uint32_t* host_code) {
   unsigned* p = status_ptr();

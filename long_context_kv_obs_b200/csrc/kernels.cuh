@@ -207,4 +207,75 @@ bool decode_tma_supported(const DecodeParams& p, bool bf16, bool probe);
 bool decode_mma_supported(const DecodeParams& p, bool bf16, bool probe);
 cudaError_t launch_decode_mma(const DecodeParams& p, bool probe, cudaStream_t st);
 
+// Page tables and slot maps (include/kvc.h: kvc_page_tables).
+struct PageTablesParams {
+  int rows, shift, n_pages, max_pages;      // page = 1 << shift tokens
+  const int32_t* len; const int32_t* len_new;
+  int32_t* table; int64_t table_row;
+  int32_t* ring;
+  const int32_t* state; int32_t* state_out;
+  int32_t* len_out; int32_t* slots; int slots_cap; int32_t* slot_start;
+  int32_t* commit;                          // [3] verdict, head, count for page_commit_kernel; NULL: out of place
+  int rows_per_cta;                         // set by the launcher
+  unsigned* status;
+};
+cudaError_t launch_page_tables(const PageTablesParams& p, cudaStream_t st);
+
+struct PageAppendParams {
+  int T, Hkv, vr, shift, n_pages;           // vr = 16-byte vectors per row
+  const char* k; int64_t kst, ksh;          // byte strides
+  const char* v; int64_t vst, vsh;
+  char* K; int64_t Ksp, Ksh, Kst;
+  char* V; int64_t Vsp, Vsh, Vst;
+  const int32_t* slots;
+  unsigned* status;
+};
+cudaError_t launch_page_append(const PageAppendParams& p, cudaStream_t st);
+
+// Decode attention over a shared prompt and the sequences' own rows (prefix.cu).  Partial
+// results are records of one query row over one stretch of keys: ml = (max in log2 units, sum),
+// o[d] unnormalised.  Records lie in groups of `rows` consecutive query rows.
+struct PartialBuf {
+  float2* ml;                               // [groups * rows]
+  float* o;                                 // [groups * rows][d]
+};
+struct PrefixParams {
+  int B, L, Hq, Hkv, G, d;
+  const void* q; int qbf16, kbf16;
+  // the prompt (Kp == nullptr: none); byte strides
+  const char* Kp; int64_t Kpl, Kph, Kpt;
+  const char* Vp; int64_t Vpl, Vph, Vpt;
+  const int32_t* len_p; int max_p;
+  const float* R; int64_t Rsl, Rsh;
+  float alpha_c, qscale;                    // qscale = scale * log2(e)
+  // own rows (K == nullptr: none); table != nullptr: Ksb is the page stride and Ksl is unused
+  const char* K; int64_t Ksb, Ksl, Ksh, Kst;
+  const char* V; int64_t Vsb, Vsl, Vsh, Vst;
+  const int32_t* len; int max_len;
+  const int32_t* table; int64_t tsb, tsl; int shift, n_pages;
+  unsigned* status;
+  float* o; float* lse; int64_t lse_stride;
+  // how the prompt's keys are cut: tc: work of all (layer, KV head, row block) items laid end to
+  // end in 128-key tiles and cut into equal runs, one a CTA; else nsp splits of spl keys an item
+  int tc, mt, mp, grid;                     // mt: 1 or 2 query tiles of 128 rows a CTA; mp: row blocks
+  int nsp, spl, rgp;                        // generic: splits, keys a split, groups of 8 query rows
+  int nso, slo;                             // own rows: splits and keys a split
+  PartialBuf pp, po;
+};
+bool prefix_tc_supported(const PrefixParams& p);
+cudaError_t launch_prefix_tc(const PrefixParams& p, cudaStream_t st);
+bool prefix_own_mma_supported(const PrefixParams& p);
+cudaError_t launch_prefix_own_mma(const PrefixParams& p, cudaStream_t st);
+size_t plan_prefix(PrefixParams& p, void* ws);   // cuts the work, places the partials; bytes needed
+cudaError_t launch_prefix(const PrefixParams& p, cudaStream_t st);
+
+// Token sampling (sample.cu).
+struct SampleParams {
+  int n, V, bf16;
+  const void* logits; int64_t row_stride;   // elements
+  const float* u; const float* temperature; const int32_t* top_k; const float* top_p; const float* min_p;
+  int32_t* token; float* logprob; int32_t* kept;
+};
+cudaError_t launch_sample(const SampleParams& p, cudaStream_t st);
+
 }  // namespace kvc

@@ -1,0 +1,346 @@
+// Decode attention of a batch over a shared prompt and each sequence's own rows: how the work is
+// cut, the general kernel, and the merge of the partial results.
+//
+//   o(b,l,h) = sum_i 2^(z_i - M) v_i / sum_i 2^(z_i - M),  z in log2 units, over the prompt's keys
+//   (z_i = q k_i * qscale + alpha_c log2 R_i) and the sequence's own (no bias).
+// Any cut of the keys into stretches gives partial (m, sum, o) records that combine exactly:
+// M = max m, each record scaled by 2^(m - M).  The prompt's stretches are worked on for all rows
+// of the batch at once (prefix_tc.cu: bf16, tensor cores; here: fp32 caches or queries, groups of 8
+// query rows), the own ones row by row (prefix_own.cu, or here).
+#include <cuda_runtime.h>
+
+#include "kernels.cuh"
+#include "tc_sm100.cuh"
+
+namespace kvc {
+
+constexpr float PF_LN2 = 0.6931471805599453f;
+constexpr int PG_THREADS = 128;
+constexpr int PG_ROWS = 8;                      // query rows a CTA
+
+// Four consecutive elements of a row.
+__device__ __forceinline__ void ld4(const char* p, int bf16, float (&f)[4]) {
+  if (bf16) {
+    const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+    f[0] = bf_lo(u.x); f[1] = bf_hi(u.x); f[2] = bf_lo(u.y); f[3] = bf_hi(u.y);
+  } else {
+    const float4 u = __ldg(reinterpret_cast<const float4*>(p));
+    f[0] = u.x; f[1] = u.y; f[2] = u.z; f[3] = u.w;
+  }
+}
+
+// General form: one CTA a (group of up to 8 query rows, stretch of keys).  D / 4 lanes share a key,
+// four dimensions each; the logits are summed over them by shuffles, the softmax runs online
+// per key group, and the CTA's groups are merged in shared memory.  The lanes of a key hold all
+// of its logits, so no wider exchange is needed.  OWN: the group is the G heads of a
+// (sequence, layer, KV head) row over its own keys; else 8 of the B * G rows of (layer, KV head)
+// over the prompt's.
+template <int D, bool OWN>
+__global__ void __launch_bounds__(PG_THREADS) prefix_generic_kernel(const __grid_constant__ PrefixParams p) {
+  constexpr int LPK = D / 4, KPW = 32 / LPK, NG = (PG_THREADS / 32) * KPW;   // lanes a key, keys a warp, key groups
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int part = lane % LPK, grp = warp * KPW + lane / LPK;
+  const int item = blockIdx.x, split = blockIdx.y;
+  int g, l, b = 0, n, R0 = 0, nr;
+  const char *Kb, *Vb;
+  int64_t kst, vst;
+  const int32_t* trow = nullptr;
+  const float* Rr = nullptr;
+  if (OWN) {
+    g = item % p.Hkv;
+    l = item / p.Hkv % p.L;
+    b = item / (p.Hkv * p.L);
+    const int n0 = p.len[b * p.L + l];
+    n = n0 < 0 ? 0 : min(n0, p.max_len);
+    if (n != n0 && split == 0 && threadIdx.x == 0) flag(p.status, ST_BOUNDS);
+    nr = p.G;
+    if (p.table) trow = p.table + b * p.tsb + l * p.tsl;
+    Kb = p.K + g * p.Ksh + (p.table ? 0 : b * p.Ksb + l * p.Ksl);
+    Vb = p.V + g * p.Vsh + (p.table ? 0 : b * p.Vsb + l * p.Vsl);
+    kst = p.Kst;
+    vst = p.Vst;
+  } else {
+    const int rg = item % p.rgp;
+    g = item / p.rgp % p.Hkv;
+    l = item / (p.rgp * p.Hkv);
+    const int n0 = p.len_p[l];
+    n = n0 < 0 ? 0 : min(n0, p.max_p);
+    if (n != n0 && split == 0 && threadIdx.x == 0) flag(p.status, ST_BOUNDS);
+    R0 = rg * PG_ROWS;
+    nr = min(PG_ROWS, p.B * p.G - R0);
+    Kb = p.Kp + l * p.Kpl + g * p.Kph;
+    Vb = p.Vp + l * p.Vpl + g * p.Vph;
+    kst = p.Kpt;
+    vst = p.Vpt;
+    if (p.R) Rr = p.R + l * p.Rsl + g * p.Rsh;
+  }
+  const int sl = OWN ? p.slo : p.spl, ns = OWN ? p.nso : p.nsp;
+  const int s0 = split * sl, s1 = min(n, s0 + sl);
+  const PartialBuf& out = OWN ? p.po : p.pp;
+  const int64_t rec0 = ((int64_t)item * ns + split) * (OWN ? p.G : PG_ROWS);
+  if (s0 >= s1) {
+    if ((int)threadIdx.x < nr) out.ml[rec0 + threadIdx.x] = make_float2(-INFINITY, 0.f);
+    return;
+  }
+  float q[PG_ROWS][4], acc[PG_ROWS][4], m[PG_ROWS], ls[PG_ROWS];
+#pragma unroll
+  for (int r = 0; r < PG_ROWS; ++r) {
+    m[r] = -INFINITY;
+    ls[r] = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) q[r][e] = acc[r][e] = 0.f;
+    if (r < nr) {
+      const int bb = OWN ? b : (R0 + r) / p.G, gg = OWN ? r : (R0 + r) % p.G;
+      const int64_t off = (((int64_t)bb * p.L + l) * p.Hq + g * p.G + gg) * D + part * 4;
+      ld4(reinterpret_cast<const char*>(p.q) + off * (p.qbf16 ? 2 : 4), p.qbf16, q[r]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) q[r][e] *= p.qscale;
+    }
+  }
+  const int esz = p.kbf16 ? 2 : 4;
+  for (int i0 = s0; i0 < s1; i0 += NG) {
+    const int i = i0 + grp;
+    bool valid = i < s1;
+    float kf[4] = {0.f, 0.f, 0.f, 0.f}, vf[4] = {0.f, 0.f, 0.f, 0.f};
+    if (valid) {
+      const char *ka, *va;
+      bool in = true;
+      if (OWN && trow) {
+        const int pg = __ldg(trow + (i >> p.shift)), off = i & ((1 << p.shift) - 1);
+        in = (unsigned)pg < (unsigned)p.n_pages;
+        if (!in) flag(p.status, ST_BOUNDS);
+        ka = Kb + (int64_t)pg * p.Ksb + off * kst;
+        va = Vb + (int64_t)pg * p.Vsb + off * vst;
+      } else {
+        ka = Kb + (int64_t)i * kst;
+        va = Vb + (int64_t)i * vst;
+      }
+      if (in) {
+        ld4(ka + part * 4 * esz, p.kbf16, kf);
+        ld4(va + part * 4 * esz, p.kbf16, vf);
+      }
+    }
+    float z[PG_ROWS];
+#pragma unroll
+    for (int r = 0; r < PG_ROWS; ++r) {
+      z[r] = q[r][0] * kf[0];
+#pragma unroll
+      for (int e = 1; e < 4; ++e) z[r] = fmaf(q[r][e], kf[e], z[r]);
+    }
+#pragma unroll
+    for (int o = LPK / 2; o > 0; o >>= 1)
+#pragma unroll
+      for (int r = 0; r < PG_ROWS; ++r) z[r] += __shfl_xor_sync(FULL, z[r], o);
+    const float bias = Rr && valid ? p.alpha_c * log2f(__ldg(Rr + i)) : 0.f;
+#pragma unroll
+    for (int r = 0; r < PG_ROWS; ++r) {
+      const float x = valid ? z[r] + bias : -INFINITY;
+      if (x > m[r] + 8.f) {
+        const float corr = exp2f(m[r] - x);
+        m[r] = x;
+        ls[r] *= corr;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[r][e] *= corr;
+      }
+      const float w = x == -INFINITY ? 0.f : exp2f(x - m[r]);
+      ls[r] += w;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[r][e] = fmaf(w, vf[e], acc[r][e]);
+    }
+  }
+  // merge the CTA's key groups
+  __shared__ float sm_o[NG][PG_ROWS][D];
+  __shared__ float2 sm_ml[NG][PG_ROWS];
+#pragma unroll
+  for (int r = 0; r < PG_ROWS; ++r) {
+    if (part == 0) sm_ml[grp][r] = make_float2(m[r], ls[r]);
+    *reinterpret_cast<float4*>(&sm_o[grp][r][part * 4]) = make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]);
+  }
+  __syncthreads();
+  for (int t = threadIdx.x; t < nr * D; t += PG_THREADS) {
+    const int r = t / D, e = t % D;
+    float M = -INFINITY, v = 0.f, s = 0.f;
+#pragma unroll
+    for (int k = 0; k < NG; ++k) M = fmaxf(M, sm_ml[k][r].x);
+#pragma unroll
+    for (int k = 0; k < NG; ++k) {
+      const float sc = M == -INFINITY ? 0.f : exp2f(sm_ml[k][r].x - M);
+      v += sm_o[k][r][e] * sc;
+      s += sm_ml[k][r].y * sc;
+    }
+    out.o[(rec0 + r) * D + e] = v;
+    if (e == 0) out.ml[rec0 + r] = make_float2(M, s);
+  }
+}
+
+// One warp a (sequence, layer, query head): merge its records, prompt first, in a fixed order.
+// Records without weight (nothing seen) are not read.
+template <int D>
+__global__ void __launch_bounds__(256) prefix_combine_kernel(const __grid_constant__ PrefixParams p) {
+  constexpr int EPL = D / 32;
+  const int wid = (int)((blockIdx.x * 256 + threadIdx.x) >> 5), lane = threadIdx.x & 31;
+  if (wid >= p.B * p.L * p.Hq) return;
+  const int h = wid % p.Hq, bl = wid / p.Hq, l = bl % p.L, b = bl / p.L;
+  const int g = h / p.G, gg = h - g * p.G;
+  int np = 0;                                   // prompt records, `pstep` apart from prec
+  int64_t prec = 0, pstep = 0;
+  if (p.Kp && p.tc) {
+    // the runs that touch this row's item (see prefix_tc.cu)
+    const int per = p.Hkv * p.mp;
+    int before = 0, all = 0, T = 0;
+    for (int x = lane; x < p.L; x += 32) {
+      const int n0 = p.len_p[x], n = n0 < 0 ? 0 : min(n0, p.max_p), t = (n + 127) / 128;
+      all += t * per;
+      if (x < l) before += t * per;
+      if (x == l) T = t;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      before += __shfl_xor_sync(FULL, before, o);
+      all += __shfl_xor_sync(FULL, all, o);
+      T += __shfl_xor_sync(FULL, T, o);
+    }
+    if (T > 0) {
+      const int W = max(1, (all + p.grid - 1) / p.grid);
+      const int r = b * p.G + gg, blk = p.mt * 128, mp = r / blk, rr = r - mp * blk;
+      const int it = g * p.mp + mp, start = before + it * T, c0 = start / W, c1 = (start + T - 1) / W;
+      const int64_t item = (int64_t)l * per + it;
+      // mt 1: both warpgroups' records of a run hold the row; mt 2: one of them
+      np = (c1 - c0 + 1) * (p.mt == 1 ? 2 : 1);
+      pstep = p.mt == 1 ? 128 : 256;
+      prec = 2 * (item + c0) * 128 + rr;        // mt 2: the second group of 128 rows follows the first
+    }
+  } else if (p.Kp) {
+    const int r = b * p.G + gg;
+    np = p.nsp;
+    pstep = PG_ROWS;
+    prec = (((int64_t)l * p.Hkv + g) * p.rgp + r / PG_ROWS) * p.nsp * PG_ROWS + r % PG_ROWS;
+  }
+  const int no = p.K ? p.nso : 0;
+  const int64_t orec = ((int64_t)bl * p.Hkv + g) * p.nso * p.G + gg;
+  const int nall = np + no;
+  float M = -INFINITY;
+  for (int i = lane; i < nall; i += 32) {
+    const float2 x = i < np ? p.pp.ml[prec + i * pstep] : p.po.ml[orec + (int64_t)(i - np) * p.G];
+    M = fmaxf(M, x.x);
+  }
+  M = warp_max(M);
+  float acc[EPL], lsum = 0.f;
+#pragma unroll
+  for (int e = 0; e < EPL; ++e) acc[e] = 0.f;
+  for (int i0 = 0; i0 < nall; i0 += 32) {
+    const int i = i0 + lane;
+    float w = 0.f, s = 0.f;
+    if (i < nall) {
+      const float2 x = i < np ? p.pp.ml[prec + i * pstep] : p.po.ml[orec + (int64_t)(i - np) * p.G];
+      w = x.x == -INFINITY ? 0.f : tc::ex2(x.x - M);
+      s = w * x.y;
+    }
+    lsum += warp_sum(s);
+    const int nn = min(32, nall - i0);
+    for (int j = 0; j < nn; ++j) {
+      const float wj = __shfl_sync(FULL, w, j);
+      if (wj == 0.f) continue;
+      const int k = i0 + j;
+      const float* r = k < np ? p.pp.o + (prec + k * pstep) * D : p.po.o + (orec + (int64_t)(k - np) * p.G) * D;
+      float v[EPL];
+      if constexpr (EPL == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(r + lane * 4);
+        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(r + lane * 2);
+        v[0] = x.x; v[1] = x.y;
+      }
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) acc[e] = fmaf(v[e], wj, acc[e]);
+    }
+  }
+  const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
+  float* o = p.o + (int64_t)wid * D + lane * EPL;
+#pragma unroll
+  for (int e = 0; e < EPL; ++e) o[e] = acc[e] * inv;
+  if (p.lse && lane == 0) p.lse[(int64_t)wid * p.lse_stride] = lsum > 0.f ? (M + log2f(lsum)) * PF_LN2 : -INFINITY;
+}
+
+static size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+size_t plan_prefix(PrefixParams& p, void* ws) {
+  const int sms = num_sms();
+  size_t off = 0;
+  auto place = [&](PartialBuf& b, int64_t recs) {
+    b.ml = ws ? reinterpret_cast<float2*>((char*)ws + off) : nullptr;
+    off += up256((size_t)recs * sizeof(float2));
+    b.o = ws ? reinterpret_cast<float*>((char*)ws + off) : nullptr;
+    off += up256((size_t)recs * p.d * sizeof(float));
+  };
+  if (p.Kp) {
+    const int rows = p.B * p.G;
+    p.mt = rows <= 128 ? 1 : 2;
+    p.mp = (rows + p.mt * 128 - 1) / (p.mt * 128);
+    p.grid = sms;
+    p.tc = prefix_tc_supported(p);
+    p.rgp = (rows + PG_ROWS - 1) / PG_ROWS;
+    if (p.tc) {
+      // one group pair a run and item it touches: items + runs bound them
+      place(p.pp, ((int64_t)p.L * p.Hkv * p.mp + p.grid) * 2 * 128);
+    } else {
+      // enough CTAs for four waves, stretches of at least 64 keys
+      const int64_t items = (int64_t)p.L * p.Hkv * p.rgp;
+      int64_t ns = (sms * 4 * 4 + items - 1) / items;
+      const int most = (p.max_p + 63) / 64;
+      if (ns > most) ns = most;
+      if (ns < 1) ns = 1;
+      p.spl = (int)((p.max_p + ns - 1) / ns);
+      p.nsp = (p.max_p + p.spl - 1) / p.spl;
+      place(p.pp, items * p.nsp * PG_ROWS);
+    }
+  }
+  if (p.K) {
+    // items of at least 128 keys, about 12 a persistent CTA (two an SM), so that their round robin
+    // leaves little imbalance
+    const int64_t rows = (int64_t)p.B * p.L * p.Hkv;
+    int64_t ns = ((int64_t)sms * 2 * 12 + rows - 1) / rows;
+    const int most = (p.max_len + 127) / 128;
+    if (ns > most) ns = most;
+    if (ns < 1) ns = 1;
+    // (whole 64-key stages: a stage starts on a page's first token or a multiple of 64 inside it)
+    p.slo = (int)(((p.max_len + ns - 1) / ns + 63) / 64 * 64);
+    p.nso = (p.max_len + p.slo - 1) / p.slo;
+    place(p.po, rows * p.nso * p.G);
+  }
+  return off;
+}
+
+cudaError_t launch_prefix(const PrefixParams& p, cudaStream_t st) {
+  cudaError_t e;
+  if (p.Kp) {
+    if (p.tc) {
+      if ((e = launch_prefix_tc(p, st)) != cudaSuccess) return e;
+    } else {
+      const dim3 grid(p.L * p.Hkv * p.rgp, p.nsp);
+      if (p.d == 128) prefix_generic_kernel<128, false><<<grid, PG_THREADS, 0, st>>>(p);
+      else prefix_generic_kernel<64, false><<<grid, PG_THREADS, 0, st>>>(p);
+      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+      count_launch();
+    }
+  }
+  if (p.K) {
+    if (prefix_own_mma_supported(p)) {
+      if ((e = launch_prefix_own_mma(p, st)) != cudaSuccess) return e;
+    } else {
+      const dim3 grid(p.B * p.L * p.Hkv, p.nso);
+      if (p.d == 128) prefix_generic_kernel<128, true><<<grid, PG_THREADS, 0, st>>>(p);
+      else prefix_generic_kernel<64, true><<<grid, PG_THREADS, 0, st>>>(p);
+      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+      count_launch();
+    }
+  }
+  const int64_t warps = (int64_t)p.B * p.L * p.Hq;
+  const unsigned blocks = (unsigned)((warps + 7) / 8);
+  if (p.d == 128) prefix_combine_kernel<128><<<blocks, 256, 0, st>>>(p);
+  else prefix_combine_kernel<64><<<blocks, 256, 0, st>>>(p);
+  if ((e = cudaGetLastError()) == cudaSuccess) count_launch();
+  return e;
+}
+
+}  // namespace kvc

@@ -1,0 +1,352 @@
+// Decode attention of every sequence over its own rows, in pages or contiguous, on mma.sync.
+//
+// A (sequence, layer, KV head) row has G <= 8 query rows against len[b][l] keys of its own, so each
+// key is used G times and the pass is bound by HBM: 512 bytes a key (bf16, d = 128).  The query
+// rows fill half of the 16 rows of an m16n8k16 A operand; the tensor pipe has room for that
+// (a 128-row tcgen05 tile would be 94 % padding here):
+//   S = Q K^T   B = K rows by ldmatrix;   O += P V   P as a bf16 pair hi + lo (about 16 bits, so the
+//   fp32 output keeps its accuracy), B = V rows by ldmatrix.trans; the softmax runs online.
+//
+// A producer warp fills a ring of 64-key stages by TMA (128B swizzle); four consumer warps take 16
+// keys of a stage each, with a running state of their own, and are merged in shared memory at the
+// end of an item, a stretch of at most slo keys of one row.  Persistent CTAs, two an SM; the producer
+// runs ahead across items, so short rows (a few hundred keys) still keep the ring full.
+// Pages: a stage is 64 / page boxes of `page` tokens (or a part of one page), each at the place its
+// table entry says.  The producer's lanes hold 32 entries of the row's table at a time and each
+// issues one box.  A page id outside the pool becomes a coordinate past the map, whose box reads
+// as zeros.  Boxes wholly behind the row's end are not loaded.
+#include <cudaTypedefs.h>
+
+#include "kernels.cuh"
+#include "mma_sync.cuh"
+#include "tc_sm100.cuh"
+
+namespace kvc {
+using namespace tc;
+
+constexpr int PO_KEYS = 64;                     // keys a stage, 16 a consumer warp
+constexpr int PO_CW = 4;
+constexpr int PO_THREADS = 32 * (1 + PO_CW);
+constexpr int PO_ATOM = PO_KEYS * 128;          // 64 rows x 64 bf16 (8 KB)
+constexpr int PO_PER_SM = 2;
+template <int D> constexpr int po_stage() { return 2 * (D / 64) * PO_ATOM; }
+
+struct PoArgs {
+  PrefixParams p;
+  int nitems, nst, bt;                          // bt: tokens of a box
+};
+
+template <int D>
+__global__ void __launch_bounds__(PO_THREADS, PO_PER_SM)
+prefix_own_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
+                  const __grid_constant__ PoArgs a) {
+  constexpr int NA = D / 64, STAGE = po_stage<D>(), REC = D + 2;
+  const PrefixParams& p = a.p;
+  const int NST = a.nst;
+  extern __shared__ __align__(1024) uint8_t po_raw[];
+  uint8_t* ring = po_raw;
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + (size_t)NST * STAGE);
+  uint64_t* empty = full + NST;
+  int* abort_flag = reinterpret_cast<int*>(empty + NST);
+  float* dsm = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(abort_flag) + 16);   // [CW][G][REC]
+  volatile int* abort = abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], PO_CW);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_map(&mapK);
+    prefetch_map(&mapV);
+  }
+  __syncthreads();
+  auto row_len = [&](int bl) {
+    const int n = p.len[bl];
+    return n < 0 ? 0 : min(n, p.max_len);
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    const bool paged = p.table != nullptr;
+    const int bt = a.bt, nb = PO_KEYS / bt;     // boxes a stage (per K / V atom)
+    uint32_t chunk = 0;
+    bool ok = true;
+    for (int item = blockIdx.x; ok && item < a.nitems; item += gridDim.x) {
+      const int row = item / p.nso, split = item - row * p.nso;
+      const int bl = row / p.Hkv, g = row - bl * p.Hkv, b = bl / p.L, l = bl - b * p.L;
+      const int n = row_len(bl);
+      const int s0 = split * p.slo, s1 = min(n, s0 + p.slo);
+      const int32_t* trow = paged ? p.table + b * p.tsb + l * p.tsl : nullptr;
+      int ent = 0, ent0 = -1;                   // entries ent0 .. ent0 + 31 of the table, one a lane
+      for (int i0 = s0; i0 < s1; i0 += PO_KEYS, ++chunk) {
+        const int s = chunk % NST;
+        const int tok = i0 + lane * bt;         // this lane's box, lane < nb
+        const bool box = lane < nb && tok < s1;
+        int pg = 0, off = 0;
+        if (paged) {
+          const int first = i0 >> p.shift;      // the stage's entries: at most 4 from here
+          if (ent0 < 0 || first + 3 >= ent0 + 32) {
+            ent0 = first;
+            const int e = ent0 + lane, last = (n - 1) >> p.shift;
+            ent = e <= last ? __ldg(trow + e) : 0;
+            if ((unsigned)ent >= (unsigned)p.n_pages) {
+              flag(p.status, ST_BOUNDS);
+              ent = p.n_pages;                  // past the map: reads as zeros
+            }
+          }
+          pg = __shfl_sync(FULL, ent, min(31, ((box ? tok : i0) >> p.shift) - ent0));
+          off = tok & ((1 << p.shift) - 1);
+        }
+        const unsigned boxes = __ballot_sync(FULL, box);
+        if (lane == 0) {
+          ok = mbar_wait(&empty[s], ((chunk / NST) & 1) ^ 1, abort, p.status);
+          if (ok) mbar_expect_tx(&full[s], (uint32_t)__popc(boxes) * bt * 128 * 2 * NA);
+        }
+        ok = __shfl_sync(FULL, (int)ok, 0) != 0;
+        if (!ok) break;
+        if (box) {
+          uint8_t* st = ring + (size_t)s * STAGE + (size_t)lane * bt * 128;
+          const int c1 = paged ? off : tok, c3 = paged ? pg : l, c4 = paged ? 0 : b;
+#pragma unroll
+          for (int x = 0; x < NA; ++x) {
+            tma_load_5d(st + x * PO_ATOM, &mapK, x * 64, c1, g, c3, c4, &full[s]);
+            tma_load_5d(st + (NA + x) * PO_ATOM, &mapV, x * 64, c1, g, c3, c4, &full[s]);
+          }
+        }
+      }
+    }
+    if (*abort && lane == 0) {                  // copies in flight end before shared memory is given up
+      int none = 0;
+      const uint32_t issued = chunk;
+      for (uint32_t j = issued > (uint32_t)NST ? issued - NST : 0; j < issued; ++j)
+        mbar_wait(&full[j % NST], (j / NST) & 1, &none, p.status);
+    }
+    return;
+  }
+  // -------------------------------------------------------------- consumers
+  const int cw = warp - 1;
+  const int gid = lane >> 2, tig = lane & 3;    // accumulator row (query head) and column pair
+  const int G = p.G;
+  uint32_t chunk = 0;
+  for (int item = blockIdx.x; item < a.nitems; item += gridDim.x) {
+    const int row = item / p.nso, split = item - row * p.nso;
+    const int bl = row / p.Hkv, g = row - bl * p.Hkv;
+    const int n = row_len(bl);
+    const int s0 = split * p.slo, s1 = min(n, s0 + p.slo);
+    if (cw == 0 && lane == 0 && split == 0 && n != p.len[bl]) flag(p.status, ST_BOUNDS);
+    const int64_t rec0 = ((int64_t)row * p.nso + split) * G;
+    if (s0 >= s1) {                             // nothing here: records of no weight
+      if (cw == 0 && lane < G) p.po.ml[rec0 + lane] = make_float2(-INFINITY, 0.f);
+      continue;
+    }
+    uint32_t qa[D / 16][2];
+    {
+      const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(p.q) + ((int64_t)bl * p.Hq + g * G + gid) * D;
+#pragma unroll
+      for (int kc = 0; kc < D / 16; ++kc) {
+        qa[kc][0] = gid < G ? __ldg(reinterpret_cast<const uint32_t*>(q + kc * 16 + 2 * tig)) : 0u;
+        qa[kc][1] = gid < G ? __ldg(reinterpret_cast<const uint32_t*>(q + kc * 16 + 8 + 2 * tig)) : 0u;
+      }
+    }
+    float O[D / 8][4];
+#pragma unroll
+    for (int t = 0; t < D / 8; ++t) O[t][0] = O[t][1] = O[t][2] = O[t][3] = 0.f;
+    float m = -INFINITY, lsum = 0.f;
+    for (int i0 = s0; i0 < s1; i0 += PO_KEYS, ++chunk) {
+      const int s = chunk % NST;
+      const bool ok = !*abort && mbar_wait(&full[s], (chunk / NST) & 1, abort, p.status);
+      if (!__all_sync(FULL, ok)) continue;
+      const int r0 = cw * 16, nk = min(PO_KEYS, s1 - i0) - r0;   // this warp's keys, valid ones of them
+      uint8_t* st = ring + (size_t)s * STAGE;
+      const uint32_t kb = smem_u32(st), vb = kb + NA * PO_ATOM;
+      if (nk > 0) {
+        if (nk < 16) {
+          // rows past the end may hold anything: zero V there (P is 0 for them, but 0 * NaN is not)
+          for (int i = nk * (D / 8) + lane; i < 16 * (D / 8); i += 32) {
+            const int r = r0 + i / (D / 8), ch = i % (D / 8);
+            *reinterpret_cast<uint4*>(st + (NA + (ch >> 3)) * PO_ATOM + r * 128 + (ch & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+        }
+        float S[2][4];
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          S[nt][0] = S[nt][1] = S[nt][2] = S[nt][3] = 0.f;
+          const int r = r0 + nt * 8 + (lane & 7);
+#pragma unroll
+          for (int kc2 = 0; kc2 < D / 32; ++kc2) {
+            const int d0 = kc2 * 32 + (lane >> 3) * 8;
+            uint32_t b0, b1, b2, b3;
+            ldsm_x4(kb + (d0 >> 6) * PO_ATOM + sw_off(r, (d0 & 63) >> 3), b0, b1, b2, b3);
+            mma_rows8(S[nt], qa[2 * kc2][0], qa[2 * kc2][1], b0, b1);
+            mma_rows8(S[nt], qa[2 * kc2 + 1][0], qa[2 * kc2 + 1][1], b2, b3);
+          }
+        }
+        float x[2][2], mx = -INFINITY;
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int key = nt * 8 + 2 * tig + j;
+            x[nt][j] = key < nk ? S[nt][j] * p.qscale : -INFINITY;
+            mx = fmaxf(mx, x[nt][j]);
+          }
+        mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 2));
+        if (mx > m + 8.f) {
+          const float corr = ex2(m - mx);
+          lsum *= corr;
+#pragma unroll
+          for (int t = 0; t < D / 8; ++t) {
+            O[t][0] *= corr;
+            O[t][1] *= corr;
+          }
+          m = mx;
+        }
+        float pr[2][2];
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            pr[nt][j] = x[nt][j] == -INFINITY ? 0.f : ex2(x[nt][j] - m);
+            lsum += pr[nt][j];
+          }
+        const uint32_t h0 = pack_bf16(pr[0][0], pr[0][1]), h2 = pack_bf16(pr[1][0], pr[1][1]);
+        const uint32_t l0 = pack_bf16(pr[0][0] - bf_lo(h0), pr[0][1] - bf_hi(h0));
+        const uint32_t l2 = pack_bf16(pr[1][0] - bf_lo(h2), pr[1][1] - bf_hi(h2));
+        const int r = r0 + ((lane >> 3) & 1) * 8 + (lane & 7);
+#pragma unroll
+        for (int dt2 = 0; dt2 < D / 16; ++dt2) {
+          const int d0 = dt2 * 16 + (lane >> 4) * 8;
+          uint32_t b0, b1, b2, b3;
+          ldsm_x4_t(vb + (d0 >> 6) * PO_ATOM + sw_off(r, (d0 & 63) >> 3), b0, b1, b2, b3);
+          mma_rows8(O[2 * dt2], h0, h2, b0, b1);
+          mma_rows8(O[2 * dt2], l0, l2, b0, b1);
+          mma_rows8(O[2 * dt2 + 1], h0, h2, b2, b3);
+          mma_rows8(O[2 * dt2 + 1], l0, l2, b2, b3);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[s]);
+    }
+    lsum += __shfl_xor_sync(FULL, lsum, 1);
+    lsum += __shfl_xor_sync(FULL, lsum, 2);
+    if (gid < G) {
+      float* r = dsm + ((size_t)cw * G + gid) * REC;
+      if (tig == 0) {
+        r[D] = m;
+        r[D + 1] = lsum;
+      }
+#pragma unroll
+      for (int t = 0; t < D / 8; ++t) {
+        r[t * 8 + 2 * tig] = O[t][0];
+        r[t * 8 + 2 * tig + 1] = O[t][1];
+      }
+    }
+    asm volatile("bar.sync 1, %0;" ::"n"(PO_CW * 32) : "memory");
+    for (int t = threadIdx.x - 32; t < G * D; t += PO_CW * 32) {
+      const int gg = t / D, e = t % D;
+      float M = -INFINITY, v = 0.f, l = 0.f;
+#pragma unroll
+      for (int w = 0; w < PO_CW; ++w) M = fmaxf(M, dsm[((size_t)w * G + gg) * REC + D]);
+#pragma unroll
+      for (int w = 0; w < PO_CW; ++w) {
+        const float* r = dsm + ((size_t)w * G + gg) * REC;
+        const float sc = M == -INFINITY ? 0.f : ex2(r[D] - M);
+        v += r[e] * sc;
+        l += r[D + 1] * sc;
+      }
+      p.po.o[(rec0 + gg) * D + e] = v;
+      if (e == 0) p.po.ml[rec0 + gg] = make_float2(M, l);
+    }
+    asm volatile("bar.sync 1, %0;" ::"n"(PO_CW * 32) : "memory");
+  }
+}
+
+// ---------------------------------------------------------------- host side
+static PFN_cuTensorMapEncodeTiled_v12000 po_encode() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      ptr = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  }();
+  return fn;
+}
+
+static int po_box(const PrefixParams& p) {
+  const int page = 1 << p.shift;
+  return p.table && page < PO_KEYS ? page : PO_KEYS;
+}
+
+// 5-D map: (dim, token, KV head, layer, sequence), or (dim, token of the page, KV head, page, 1).
+static bool po_map(CUtensorMap* m, const char* base, int64_t sb, int64_t sl, int64_t sh, int64_t st,
+                   const PrefixParams& p) {
+  auto enc = po_encode();
+  if (!enc) return false;
+  const bool paged = p.table != nullptr;
+  cuuint64_t dims[5] = {(cuuint64_t)p.d, (cuuint64_t)(paged ? 1 << p.shift : p.max_len), (cuuint64_t)p.Hkv,
+                        (cuuint64_t)(paged ? p.n_pages : p.L), (cuuint64_t)(paged ? 1 : p.B)};
+  int64_t s[4] = {st, sh, paged ? sb : sl, sb};
+  if (dims[1] == 1) s[0] = p.d * 2;
+  for (int i = 1; i < 4; ++i)
+    if (dims[i + 1] == 1) s[i] = s[i - 1];
+  for (int i = 0; i < 4; ++i)
+    if (s[i] <= 0 || s[i] % 16 || s[i] >= (1LL << 40)) return false;
+  cuuint64_t strides[4] = {(cuuint64_t)s[0], (cuuint64_t)s[1], (cuuint64_t)s[2], (cuuint64_t)s[3]};
+  cuuint32_t box[5] = {64, (cuuint32_t)po_box(p), 1, 1, 1};
+  cuuint32_t el[5] = {1, 1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<char*>(base), dims, strides, box, el,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool prefix_own_mma_supported(const PrefixParams& p) {
+  if (!p.qbf16 || !p.kbf16 || (p.d != 64 && p.d != 128) || p.G > 8 || (uintptr_t)p.q % 16) return false;
+  CUtensorMap a, b;
+  return po_map(&a, p.K, p.Ksb, p.Ksl, p.Ksh, p.Kst, p) && po_map(&b, p.V, p.Vsb, p.Vsl, p.Vsh, p.Vst, p);
+}
+
+template <int D>
+static cudaError_t launch_po(const PrefixParams& p, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t st) {
+  PoArgs a{};
+  a.p = p;
+  a.nitems = p.B * p.L * p.Hkv * p.nso;
+  a.bt = po_box(p);
+  int dev = 0, smem_sm = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&smem_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev);
+  // two CTAs an SM, as many stages (at most 6) as fit beside the merge records (1 KB a CTA is the runtime's)
+  const size_t fixed = 16 + (size_t)PO_CW * p.G * (D + 2) * 4;
+  const long long room = (long long)smem_sm / PO_PER_SM - 1024 - (long long)fixed;
+  a.nst = (int)(room / (po_stage<D>() + 16));
+  if (a.nst > 6) a.nst = 6;
+  if (a.nst < 2) return cudaErrorInvalidConfiguration;
+  const size_t smem = fixed + (size_t)a.nst * (po_stage<D>() + 16);
+  auto kern = prefix_own_kernel<D>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  int grid = PO_PER_SM * num_sms();
+  if (grid > a.nitems) grid = a.nitems;
+  kern<<<grid, PO_THREADS, smem, st>>>(mk, mv, a);
+  e = cudaGetLastError();
+  if (e == cudaSuccess) count_launch();
+  return e;
+}
+
+cudaError_t launch_prefix_own_mma(const PrefixParams& p, cudaStream_t st) {
+  CUtensorMap mk, mv;
+  if (!po_map(&mk, p.K, p.Ksb, p.Ksl, p.Ksh, p.Kst, p) || !po_map(&mv, p.V, p.Vsb, p.Vsl, p.Vsh, p.Vst, p))
+    return cudaErrorInvalidValue;
+  return p.d == 128 ? launch_po<128>(p, mk, mv, st) : launch_po<64>(p, mk, mv, st);
+}
+
+}  // namespace kvc

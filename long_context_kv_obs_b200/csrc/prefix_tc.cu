@@ -1,0 +1,516 @@
+// Decode attention of a batch over a shared prompt on the 5th-generation tensor cores.
+//
+// For every layer l and KV head g the B * G query rows of the batch face the same len_prefix[l]
+// keys:  S = Q K^T,  P = 2^(S * qscale + alpha_c log2 R - m),  O = P V, with a running maximum m
+// and sum a row.  Every key and value is read once for the whole batch: 512 bytes (bf16,
+// d = 128) serve B * G rows, so the arithmetic per byte grows with the batch, and up to about 128 rows
+// (one M = 128 tile) the pass is bound by HBM, above it by the products.
+//
+// P is carried as a bf16 pair hi + lo (two products with V), about 16 bits of it, so that the
+// fp32 output keeps fp32-level accuracy: with hi alone its error would be 2^-9 a weight.
+//
+// Work: tiles of 128 keys.  All items (l, g, row block) laid end to end are cut into equal runs of
+// tiles, one run a CTA, one CTA an SM (lengths differ by layer; a run may cover the end of
+// one item and the start of the next).  A partial record (m, sum, O) leaves for every item a
+// run touches; the item's runs are consecutive, so the combine kernel finds them by arithmetic.
+// MT = 1 (B * G <= 128): the two softmax warpgroups take the even and the odd tiles of a run, each
+// with its own running state.  MT = 2: both take every tile, with 128 query rows each, so K and V
+// are fetched once for 256 rows.
+//
+// Roles: warps 0-3 and 4-7 are the softmax warpgroups (a thread owns a query row, its TMEM lane),
+// warp 8 loads K and V (TMA, 128B swizzle, separate rings), warp 9 issues the products.  TMEM: a
+// warpgroup has 128 columns of S, overwritten by its P, and 128 of O.  Every wait is an mbarrier
+// with a time limit, those among the softmax warps too, so an abort strands no warp.  While one warpgroup
+// works on its S the tensor cores run the other's products.
+#include <cudaTypedefs.h>
+
+#include "kernels.cuh"
+#include "tc_sm100.cuh"
+
+namespace kvc {
+using namespace tc;
+
+constexpr int PX_KEYS = 128;                    // keys a tile
+constexpr int PX_THREADS = 320;
+constexpr int PX_ATOM = PX_KEYS * 128;          // 128 rows x 64 bf16, 128B-swizzled (16 KB)
+constexpr int PX_MAXL = 128;                    // layers whose tile sums fit the shared array
+template <int D> constexpr int px_tile() { return (D / 64) * PX_ATOM; }
+template <int D, int MT> constexpr int px_nk() { return D == 64 ? 4 : (MT == 1 ? 3 : 2); }
+template <int D, int MT> constexpr int px_nv() { return D == 64 ? 4 : 3; }
+struct PxCtl {
+  uint64_t fullK[4], emptyK[4], fullV[4], emptyV[4];
+  uint64_t s_ready[2], p_ready[2], o_ready[2], b_ready[2], q_ready, q_free, drain;
+  uint32_t tmem;
+  int abort;
+  float bias[2][2][PX_KEYS];                    // [warpgroup][buffer]
+  int cum[PX_MAXL + 1];                         // tiles of the layers before
+};
+template <int D, int MT> constexpr size_t px_smem() {
+  return (size_t)MT * px_tile<D>() + (size_t)(px_nk<D, MT>() + px_nv<D, MT>()) * px_tile<D>() + sizeof(PxCtl);
+}
+
+__device__ __forceinline__ int px_len(const PrefixParams& p, int l) {
+  const int n = p.len_p[l];
+  return n < 0 ? 0 : n > p.max_p ? p.max_p : n;
+}
+
+// A run's next piece: tiles [t0, t0 + n) of item (l, g, mp).
+struct PxSeg {
+  int l, g, mp, t0, n, item;
+};
+struct PxRun {
+  int cur, end, l;
+  __device__ __forceinline__ bool next(const PrefixParams& p, const int* cum, PxSeg& s) {
+    if (cur >= end) return false;
+    while (cur >= cum[l + 1]) ++l;
+    const int per = p.Hkv * p.mp, T = (cum[l + 1] - cum[l]) / per;
+    const int x = cur - cum[l], it = x / T;
+    s.l = l;
+    s.g = it / p.mp;
+    s.mp = it % p.mp;
+    s.t0 = x % T;
+    s.n = min(T - s.t0, end - cur);
+    s.item = l * per + it;
+    cur += s.n;
+    return true;
+  }
+};
+
+// Maximum of 32 products (biased, in log2 units, when HAS_R), of which the first n count.
+template <bool HAS_R>
+__device__ __forceinline__ void px_max(const uint32_t (&r)[32], const float* bias, float qscale, int n, float (&mx)[4]) {
+#pragma unroll
+  for (int k = 0; k < 32; ++k) {
+    float x = __uint_as_float(r[k]);
+    if (HAS_R) x = fmaf(x, qscale, bias[k]);
+    if (n < 32) x = k < n ? x : -INFINITY;
+    mx[k & 3] = fmaxf(mx[k & 3], x);
+  }
+}
+
+template <int D, int MT, bool HAS_R>
+__global__ void __launch_bounds__(PX_THREADS, 1)
+prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
+                 const __grid_constant__ PrefixParams p) {
+  constexpr int TILE = px_tile<D>(), NK = px_nk<D, MT>(), NV = px_nv<D, MT>(), NA = D / 64;
+  extern __shared__ __align__(1024) uint8_t px_raw[];
+  uint8_t* Qs = px_raw;
+  uint8_t* Ks = Qs + MT * TILE;
+  uint8_t* Vs = Ks + NK * TILE;
+  PxCtl* c = reinterpret_cast<PxCtl*>(Vs + NV * TILE);
+  volatile int* abort = &c->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&c->fullK[i], 1);
+      mbar_init(&c->emptyK[i], 1);
+      mbar_init(&c->fullV[i], 1);
+      mbar_init(&c->emptyV[i], 1);
+    }
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(&c->s_ready[w], 1);
+      mbar_init(&c->p_ready[w], 4);
+      mbar_init(&c->o_ready[w], 1);
+      mbar_init(&c->b_ready[w], 4);
+    }
+    mbar_init(&c->q_ready, 8);
+    mbar_init(&c->q_free, 8);
+    mbar_init(&c->drain, 1);
+    c->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) tmem_alloc(&c->tmem, 512);
+  if (warp == 8) {
+    if (lane == 0) {
+      prefetch_map(&mapK);
+      prefetch_map(&mapV);
+    }
+    // tiles of the layers before each layer
+    int run = 0;
+    for (int l0 = 0; l0 < p.L; l0 += 32) {
+      const int l = l0 + lane;
+      int t = 0;
+      if (l < p.L) {
+        t = (px_len(p, l) + PX_KEYS - 1) / PX_KEYS * p.Hkv * p.mp;
+        if (blockIdx.x == 0 && px_len(p, l) != p.len_p[l]) flag(p.status, ST_BOUNDS);
+      }
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(FULL, t, o);
+        if (lane >= o) t += x;
+      }
+      if (l < p.L) c->cum[l + 1] = run + t;
+      run += __shfl_sync(FULL, t, 31);
+    }
+    if (lane == 0) c->cum[0] = 0;
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = c->tmem;
+  const int total = c->cum[p.L];
+  const int W = max(1, (total + (int)gridDim.x - 1) / (int)gridDim.x);
+  PxRun run;
+  run.cur = (int)min((long long)blockIdx.x * W, (long long)total);
+  run.end = min(total, run.cur + W);
+  run.l = 0;
+  PxSeg sg;
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ loads
+    if (lane == 0) {
+      uint32_t tc = 0, issued_k = 0, issued_v = 0;
+      while (run.next(p, c->cum, sg)) {
+        for (int i = 0; i < sg.n; ++i, ++tc) {
+          const int key0 = (sg.t0 + i) * PX_KEYS;
+          const int ks = tc % NK, vs = tc % NV;
+          if (!mbar_wait(&c->emptyK[ks], ((tc / NK) & 1) ^ 1, abort, p.status)) goto load_done;
+          mbar_expect_tx(&c->fullK[ks], TILE);
+#pragma unroll
+          for (int a = 0; a < NA; ++a)
+            tma_load_4d(Ks + ks * TILE + a * PX_ATOM, &mapK, a * 64, key0, sg.g, sg.l, &c->fullK[ks]);
+          ++issued_k;
+          if (!mbar_wait(&c->emptyV[vs], ((tc / NV) & 1) ^ 1, abort, p.status)) goto load_done;
+          mbar_expect_tx(&c->fullV[vs], TILE);
+#pragma unroll
+          for (int a = 0; a < NA; ++a)
+            tma_load_4d(Vs + vs * TILE + a * PX_ATOM, &mapV, a * 64, key0, sg.g, sg.l, &c->fullV[vs]);
+          ++issued_v;
+        }
+      }
+    load_done:
+      if (*abort) {                             // copies in flight end before shared memory is given up
+        int none = 0;
+        for (uint32_t j = issued_k > NK ? issued_k - NK : 0; j < issued_k; ++j)
+          mbar_wait(&c->fullK[j % NK], (j / NK) & 1, &none, p.status);
+        for (uint32_t j = issued_v > NV ? issued_v - NV : 0; j < issued_v; ++j)
+          mbar_wait(&c->fullV[j % NV], (j / NV) & 1, &none, p.status);
+      }
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ products
+    if (lane == 0) {
+      constexpr uint32_t idS = idesc_bf16(128, PX_KEYS);
+      constexpr uint32_t idO = idesc_bf16(128, D) | IDESC_B_MN;
+      uint32_t tc = 0, nseg = 0, pv[2] = {0, 0};   // tiles, pieces and P V products so far
+      bool ok = true;
+      while (ok && run.next(p, c->cum, sg)) {
+        ok = mbar_wait(&c->q_ready, nseg & 1, abort, p.status);
+        ++nseg;
+        const int U = MT * sg.n;                  // steps: (tile, warpgroup)
+        auto issue_s = [&](int u) {
+          const int w = u & 1, i = MT == 2 ? u >> 1 : u;
+          const uint32_t t = tc + i, ks = t % NK;
+          if (MT == 1 || w == 0) {
+            if (!mbar_wait(&c->fullK[ks], (t / NK) & 1, abort, p.status)) return false;
+          }
+          fence_after();
+          const uint8_t* q = Qs + (MT == 2 ? w : 0) * TILE;
+          const uint64_t da = sw128_desc(q), db = sw128_desc(Ks + ks * TILE);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint64_t off = (uint64_t)((k >> 2) * (PX_ATOM >> 4) + (k & 3) * 2);
+            mma_bf16(tmem + w * 128, da + off, db + off, idS, k > 0);
+          }
+          mma_commit(&c->s_ready[w]);
+          if (MT == 1 || w == 1) mma_commit(&c->emptyK[ks]);
+          return true;
+        };
+        for (int u = 0; u < 2 && u < U && ok; ++u) ok = issue_s(u);
+        for (int u = 0; u < U && ok; ++u) {
+          const int w = u & 1, i = MT == 2 ? u >> 1 : u;
+          const uint32_t t = tc + i, vs = t % NV;
+          ok = mbar_wait(&c->fullV[vs], (t / NV) & 1, abort, p.status) &&
+               mbar_wait(&c->p_ready[w], pv[w] & 1, abort, p.status);
+          if (!ok) break;
+          fence_after();
+          const uint64_t dv = sw128_desc_mn(Vs + vs * TILE, PX_ATOM);
+          const uint32_t ta = tmem + w * 128, to = tmem + 256 + w * 128;
+          const bool fresh = MT == 2 ? i == 0 : u < 2;   // the warpgroup's first tile of this piece
+#pragma unroll
+          for (int k = 0; k < PX_KEYS / 16; ++k) {
+            // keys 16 k ..: P hi in 8 columns, P lo 16 columns further; V rows 16 k ..
+            const uint32_t a = ta + (k >> 1) * 32 + (k & 1) * 8;
+            const uint64_t b = dv + (uint64_t)(k * 16 * 128 >> 4);
+            mma_bf16_ts(to, a, b, idO, !(fresh && k == 0));
+            mma_bf16_ts(to, a + 16, b, idO, 1);
+          }
+          mma_commit(&c->o_ready[w]);
+          if (MT == 1 || w == 1) mma_commit(&c->emptyV[vs]);
+          if (u + 2 < U) {
+            // the next S of this warpgroup overwrites the P that these products read
+            ok = mbar_wait(&c->o_ready[w], pv[w] & 1, abort, p.status) && issue_s(u + 2);
+          }
+          ++pv[w];
+        }
+        tc += sg.n;
+      }
+      // every arrive issued above has landed before shared memory is given up
+      int none = 0;
+      mma_commit(&c->drain);
+      mbar_wait(&c->drain, 0, &none, p.status);
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int w = warp >> 2, row = (warp & 3) * 32 + lane;   // row = TMEM lane
+    const uint32_t tS = tmem + w * 128 + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t tO = tS + 256;
+    const int rows = p.B * p.G;
+    const int wt = threadIdx.x & 127;
+    uint32_t steps = 0, tc = 0, nseg = 0;
+    bool ok = true;
+    while (ok && run.next(p, c->cum, sg)) {
+      const int len = px_len(p, sg.l);
+      const int r0 = sg.mp * (MT * 128);
+      // Q of the piece: all S products of the piece before are done (both warpgroups waited for theirs)
+      if (nseg > 0) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c->q_free);
+        ok = mbar_wait(&c->q_free, (nseg - 1) & 1, abort, p.status);
+        if (!__all_sync(FULL, ok)) break;
+      }
+      ++nseg;
+      {
+        constexpr int CH = D / 8;                // 16-byte chunks a row
+        const int qr = MT == 2 ? threadIdx.x : wt;
+        const int R = r0 + qr;
+        const int c0 = MT == 2 ? 0 : w * (CH / 2), c1 = MT == 2 ? CH : c0 + CH / 2;
+        const int b = R / p.G, gg = R - b * p.G;
+        const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(p.q) +
+                                 (((int64_t)b * p.L + sg.l) * p.Hq + sg.g * p.G + gg) * D;
+        uint8_t* dst = Qs + (MT == 2 ? (qr >> 7) * TILE : 0) + (qr & 127) * 128;
+#pragma unroll
+        for (int ch = c0; ch < c1; ++ch) {
+          const uint4 v = R < rows ? ldg16(q + ch * 8) : make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(dst + (ch >> 3) * PX_ATOM + (((ch & 7) ^ (qr & 7)) << 4)) = v;
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c->q_ready);
+      }
+      const int Rw = r0 + (MT == 2 ? w * 128 : 0) + (warp & 3) * 32;   // the warp's first query row
+      const bool live = Rw < rows;
+      float m = -INFINITY, lsum = 0.f;
+      const float* Rr = HAS_R ? p.R + sg.l * p.Rsl + sg.g * p.Rsh : nullptr;
+      const int i0 = MT == 1 ? w : 0, di = MT == 1 ? 2 : 1;
+      float rnext = 1.f;
+      if (HAS_R && i0 < sg.n) {
+        const int k = (sg.t0 + i0) * PX_KEYS + wt;
+        rnext = k < len ? __ldg(Rr + k) : 1.f;
+      }
+      int mine = 0;
+      for (int i = i0; i < sg.n; i += di, ++mine) {
+        const int key0 = (sg.t0 + i) * PX_KEYS, nk = min(PX_KEYS, len - key0);
+        const float* bias = c->bias[w][mine & 1];
+        if (HAS_R) {
+          c->bias[w][mine & 1][wt] = p.alpha_c * log2f(rnext);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&c->b_ready[w]);
+          ok = mbar_wait(&c->b_ready[w], steps & 1, abort, p.status);
+          if (!__all_sync(FULL, ok)) {
+            ok = false;
+            break;
+          }
+          const int k = key0 + di * PX_KEYS + wt;
+          rnext = i + di < sg.n && k < len ? __ldg(Rr + k) : 1.f;
+        }
+        ok = mbar_wait(&c->s_ready[w], steps & 1, abort, p.status);
+        if (!__all_sync(FULL, ok)) {
+          ok = false;
+          break;
+        }
+        fence_after();
+        if (nk < PX_KEYS && (MT == 1 || w == 0)) {
+          // rows past the length may hold anything and 0 * NaN is NaN: zero them in V
+          const uint32_t t = tc + i, vs = t % NV;
+          ok = mbar_wait(&c->fullV[vs], (t / NV) & 1, abort, p.status);
+          if (!__all_sync(FULL, ok)) {
+            ok = false;
+            break;
+          }
+          for (int x = nk * (D / 8) + wt; x < PX_KEYS * (D / 8); x += 128) {
+            const int r = x / (D / 8), ch = x % (D / 8);
+            *reinterpret_cast<uint4*>(Vs + vs * TILE + (ch >> 3) * PX_ATOM + r * 128 + ((ch & 7) << 4)) =
+                make_uint4(0, 0, 0, 0);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        if (live) {
+          // the row's maximum, then P, both from TMEM: holding the 128 products in registers spilled
+          float mt;
+          {
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int q4 = 0; q4 < 4; q4 += 2) {
+              uint32_t ra[32], rb[32];
+              tmem_ld32_raw(tS + q4 * 32, ra);
+              tmem_ld32_raw(tS + q4 * 32 + 32, rb);
+              tmem_wait_ld32(ra);
+              tmem_wait_ld32(rb);
+              px_max<HAS_R>(ra, bias + q4 * 32, p.qscale, nk - q4 * 32, mx);
+              px_max<HAS_R>(rb, bias + q4 * 32 + 32, p.qscale, nk - q4 * 32 - 32, mx);
+            }
+            mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          }
+          if (!HAS_R) mt *= p.qscale;           // qscale > 0: the maximum of the products
+          // the running maximum moves only when it grows by more than 2^8: sums and O stay within
+          // fp32 range and most tiles rescale nothing
+          const bool grow = mt > m + 8.f;
+          if (__any_sync(FULL, grow)) {
+            const float corr = grow ? ex2(m - mt) : 1.f;   // 0 while nothing was seen
+            if (grow) m = mt;
+            lsum *= corr;
+            if (mine > 0) {
+#pragma unroll
+              for (int q4 = 0; q4 < D / 32; ++q4) {
+                uint32_t o[32];
+                tmem_ld32_raw(tO + q4 * 32, o);
+                tmem_wait_ld32(o);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * corr);
+                tmem_st32(tO + q4 * 32, o);
+              }
+            }
+          }
+          const float mref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4) {
+            uint32_t x[32], u[32];
+            tmem_ld32_raw(tS + q4 * 32, x);
+            tmem_wait_ld32(x);
+            float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+              float a = __uint_as_float(x[k]), b = __uint_as_float(x[k + 1]);
+              if (HAS_R) {
+                const float2 bb = *reinterpret_cast<const float2*>(bias + q4 * 32 + k);
+                a = ex2(fmaf(a, p.qscale, bb.x - mref));
+                b = ex2(fmaf(b, p.qscale, bb.y - mref));
+              } else {
+                a = ex2(fmaf(a, p.qscale, -mref));
+                b = ex2(fmaf(b, p.qscale, -mref));
+              }
+              if (nk < PX_KEYS) {
+                a = q4 * 32 + k < nk ? a : 0.f;
+                b = q4 * 32 + k + 1 < nk ? b : 0.f;
+              }
+              s0 += a;
+              s1 += b;
+              const uint32_t hi = pack_bf16x2(a, b);
+              u[k >> 1] = hi;
+              u[16 + (k >> 1)] = pack_bf16x2(a - bf_lo(hi), b - bf_hi(hi));
+            }
+            lsum += s0 + s1;
+            tmem_st32(tS + q4 * 32, u);
+          }
+          tmem_wait_st();
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c->p_ready[w]);
+        ++steps;
+      }
+      if (!ok) break;
+      tc += sg.n;
+      // the piece's record of this warpgroup
+      const int64_t group = 2 * (int64_t)(sg.item + blockIdx.x) + w;
+      const int64_t rec = group * 128 + row;
+      if (mine > 0) {
+        ok = mbar_wait(&c->o_ready[w], (steps - 1) & 1, abort, p.status);
+        if (!__all_sync(FULL, ok)) {
+          ok = false;
+          break;
+        }
+        fence_after();
+        if (live) {
+          p.pp.ml[rec] = make_float2(m, lsum);
+#pragma unroll
+          for (int q4 = 0; q4 < D / 32; ++q4) {
+            uint32_t o[32];
+            tmem_ld32_raw(tO + q4 * 32, o);
+            tmem_wait_ld32(o);
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+              *reinterpret_cast<uint4*>(p.pp.o + rec * D + q4 * 32 + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+          }
+        }
+        fence_before();
+      } else if (live) {
+        p.pp.ml[rec] = make_float2(-INFINITY, 0.f);
+      }
+    }
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------- host side
+static PFN_cuTensorMapEncodeTiled_v12000 px_encode() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      ptr = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  }();
+  return fn;
+}
+
+// 4-D map (dim, token, KV head, layer) with 64 x 128-token boxes, 128B swizzle.  A dimension of
+// extent 1 gets the stride its inner neighbour implies (any legal value works).
+static bool px_map(CUtensorMap* m, const char* base, int64_t sl, int64_t sh, int64_t st, const PrefixParams& p) {
+  auto enc = px_encode();
+  if (!enc) return false;
+  cuuint64_t dims[4] = {(cuuint64_t)p.d, (cuuint64_t)p.max_p, (cuuint64_t)p.Hkv, (cuuint64_t)p.L};
+  int64_t s[3] = {st, sh, sl};
+  if (dims[1] == 1) s[0] = p.d * 2;
+  for (int i = 1; i < 3; ++i)
+    if (dims[i + 1] == 1) s[i] = s[i - 1] * (int64_t)dims[i];
+  for (int i = 0; i < 3; ++i)
+    if (s[i] <= 0 || s[i] % 16 || s[i] >= (1LL << 40)) return false;
+  cuuint64_t strides[3] = {(cuuint64_t)s[0], (cuuint64_t)s[1], (cuuint64_t)s[2]};
+  cuuint32_t box[4] = {64, PX_KEYS, 1, 1};
+  cuuint32_t el[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<char*>(base), dims, strides, box, el,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// bf16 queries and keys, at most 128 layers, and cache layouts a TMA map can describe.
+bool prefix_tc_supported(const PrefixParams& p) {
+  if (!p.qbf16 || !p.kbf16 || (p.d != 64 && p.d != 128) || p.L > PX_MAXL) return false;
+  if ((uintptr_t)p.q % 16) return false;
+  CUtensorMap a, b;
+  return px_map(&a, p.Kp, p.Kpl, p.Kph, p.Kpt, p) && px_map(&b, p.Vp, p.Vpl, p.Vph, p.Vpt, p);
+}
+
+template <int D, int MT, bool HAS_R>
+static cudaError_t launch_px(const PrefixParams& p, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t st) {
+  auto kern = prefix_tc_kernel<D, MT, HAS_R>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)px_smem<D, MT>());
+  if (e != cudaSuccess) return e;
+  kern<<<p.grid, PX_THREADS, px_smem<D, MT>(), st>>>(mk, mv, p);
+  e = cudaGetLastError();
+  if (e == cudaSuccess) count_launch();
+  return e;
+}
+
+cudaError_t launch_prefix_tc(const PrefixParams& p, cudaStream_t st) {
+  CUtensorMap mk, mv;
+  if (!px_map(&mk, p.Kp, p.Kpl, p.Kph, p.Kpt, p) || !px_map(&mv, p.Vp, p.Vpl, p.Vph, p.Vpt, p))
+    return cudaErrorInvalidValue;
+#define KVC_PX(DV, MTV) return p.R ? launch_px<DV, MTV, true>(p, mk, mv, st) : launch_px<DV, MTV, false>(p, mk, mv, st)
+  if (p.d == 128) {
+    if (p.mt == 1) KVC_PX(128, 1);
+    KVC_PX(128, 2);
+  }
+  if (p.mt == 1) KVC_PX(64, 1);
+  KVC_PX(64, 2);
+#undef KVC_PX
+}
+
+}  // namespace kvc

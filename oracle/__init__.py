@@ -29,5 +29,7 @@ Modules:
   recas      - O11 dropped attention mass and the 2 * V_max * delta bound
   pipeline   - prefill compression and decode-time periodic recompression
                (O12) composed from the steps above
+  serving    - page tables and slot maps, the append into pages, decode attention over a shared
+               prompt and token sampling (interface additions of the library)
 """
-from . import infokv, selkv, recas, pipeline  # noqa: F401
+from . import infokv, selkv, recas, pipeline, serving  # noqa: F401

@@ -1,0 +1,322 @@
+"""GPU: decode attention over a shared prompt and each sequence's own rows against the fp64 oracle.
+
+Tolerance, per output element, from the arithmetic (u = 2^-24):
+* a logit is an fp32 dot product of d exact products, possibly truncated while it is accumulated:
+  |dz| <= gamma_d scale sum |q k| with the unit roundoff doubled, plus 3 u |z| for the scale's
+  product and the difference to the maximum, plus 2^-20 alpha_c for the fp32 log2 of R;
+* exp2 adds 2^-22; the running rescales one rounding each (2^-22 together, at most one in 2^8);
+* a weight kept as a bf16 pair carries 2^-8 of 2^-8 = 2^-16;
+* sums over n keys in fp32: gamma_n with the roundoff doubled.
+With w the exact weights, |do| <= E sum w |v - o| + gamma_n sum w |v| for a relative weight error of E
+(first order; E is below 2^-12 here, its square is covered by doubling), and |dlse| <= max |dz| + 2^-20 + gamma_n.
+"""
+import numpy as np
+import pytest
+import torch
+
+from long_context_kv_obs_b200 import binding as B
+from oracle import serving
+from tests.helpers import np64
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+U = 2.0 ** -24
+
+
+def gamma(n, u=2 * U):
+    return n * u / (1 - n * u)
+
+
+def i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device=DEV)
+
+
+class Case:
+    """Inputs of one call; rows behind every length hold NaN, unused table entries are negative."""
+
+    def __init__(self, B_, L, Hkv, G, d, P, own, page=16, dt=torch.bfloat16, qdt=None, merged=False, layout="head", seed=0,
+                 lens_p=None, lens=None, qs=1.0, prompt=True, has_own=True):
+        g = torch.Generator(device=DEV).manual_seed(seed)
+        rng = np.random.default_rng(seed)
+        self.m = B.model(L, Hkv * G, Hkv, d)
+        self.dims = (B_, L, Hkv, G, d)
+        self.P, self.page = P, page
+        self.q = (qs * torch.randn(B_, L, Hkv * G, d, device=DEV, generator=g)).to(qdt or dt)
+        self.prompt, self.has_own = prompt, has_own
+        self.lens_p = lens_p if lens_p is not None else [P] + [int(x) for x in rng.integers(max(0, P // 2), P + 1, L - 1)]
+        self.lens = np.asarray(lens if lens is not None else rng.integers(0, own + 1, (B_, L)))
+        self.max_len = max(1, own)
+        self.R = None
+        if prompt:
+            buf = torch.randn(2, L, Hkv, P + 3, d, device=DEV, generator=g).to(dt)
+            self.Kp, self.Vp = buf[0, :, :, :P], buf[1, :, :, :P]
+            self.Kp[:, :, 0] *= 3
+            for l in range(L):
+                self.Kp[l, :, self.lens_p[l]:] = float("nan")
+                self.Vp[l, :, self.lens_p[l]:] = float("nan")
+            if merged:
+                self.R = 1 + 3 * torch.rand(L, Hkv, P, device=DEV, generator=g)
+        if has_own:
+            if page:
+                pg = -(-self.lens // page)
+                held = int(pg.sum())
+                n_pages = held + 2
+                ids = rng.permutation(n_pages)
+                width = -(-self.max_len // page) + 1
+                table = rng.integers(-5, 0, (B_, L, width))
+                k = 0
+                for b in range(B_):
+                    for l in range(L):
+                        table[b, l, :pg[b, l]] = ids[k:k + pg[b, l]]
+                        k += pg[b, l]
+                self.table = i32(table)
+                shape = (n_pages, Hkv, page, d) if layout == "head" else (n_pages, page, Hkv, d)
+                K, V = [torch.randn(*shape, device=DEV, generator=g).to(dt) for _ in range(2)]
+                self.K, self.V = (K, V) if layout == "head" else (K.transpose(1, 2), V.transpose(1, 2))
+                spare = [int(x) for x in ids[held:]]
+                self.K[spare], self.V[spare] = float("nan"), float("nan")
+                for b in range(B_):
+                    for l in range(L):
+                        n = int(self.lens[b, l])
+                        if n % page:
+                            last = int(table[b, l, n // page])
+                            self.K[last, :, n % page:], self.V[last, :, n % page:] = float("nan"), float("nan")
+            else:
+                self.table = None
+                self.K, self.V = [torch.randn(B_, L, Hkv, self.max_len + 2, d, device=DEV, generator=g).to(dt)
+                                  for _ in range(2)]
+                for b in range(B_):
+                    for l in range(L):
+                        n = int(self.lens[b, l])
+                        self.K[b, l, :, n:], self.V[b, l, :, n:] = float("nan"), float("nan")
+        self.o = torch.full((B_, L, Hkv * G, d), float("nan"), device=DEV)
+        self.lse = torch.full((B_, L, Hkv * G), float("nan"), device=DEV)
+
+    def kw(self):
+        kw = dict(q=self.q, o=self.o, lse=self.lse)
+        if self.prompt:
+            kw.update(K_prefix=self.Kp, V_prefix=self.Vp, lens_prefix=i32(self.lens_p), max_len_prefix=self.P, R=self.R)
+        if self.has_own:
+            kw.update(K=self.K, V=self.V, table=self.table, lens=i32(self.lens), max_len=self.max_len)
+        return kw
+
+    def run(self, **more):
+        return B.kvc_prefix_decode_attn(self.m, **{**self.kw(), **more})
+
+    def own_rows(self, b, l, g):
+        if not self.has_own:
+            return np.zeros((0, self.dims[4])), np.zeros((0, self.dims[4]))
+        n = int(self.lens[b, l])
+        if self.table is None:
+            return np64(self.K[b, l, g, :n]), np64(self.V[b, l, g, :n])
+        t = self.table[b, l, :-(-n // self.page)].long()
+        return [np64(x[t][:, g].reshape(-1, self.dims[4])[:n]) for x in (self.K, self.V)]
+
+    def check(self, alpha_c=1.0, scale=None, pair=True):
+        B_, L, Hkv, G, d = self.dims
+        o, lse, q = np64(self.o), np64(self.lse), np64(self.q)
+        assert np.isfinite(o).all()
+        sc = d ** -0.5 if scale is None else scale
+        for l in range(L):
+            P = self.lens_p[l] if self.prompt else 0
+            for g in range(Hkv):
+                kp = np64(self.Kp[l, g, :P]) if P else np.zeros((0, d))
+                vp = np64(self.Vp[l, g, :P]) if P else np.zeros((0, d))
+                R = np64(self.R[l, g, :P]) if self.R is not None else None
+                for b in range(B_):
+                    ko, vo = self.own_rows(b, l, g)
+                    qq = q[b, l, g * G:(g + 1) * G]
+                    ro, rl, w = serving.prefix_attention(qq, kp, vp, ko, vo, R, alpha_c, sc)
+                    n = w.shape[1]
+                    go, gl = o[b, l, g * G:(g + 1) * G], lse[b, l, g * G:(g + 1) * G]
+                    if n == 0:
+                        assert (go == 0).all() and (gl == -np.inf).all()
+                        continue
+                    kk, vv = np.concatenate([kp, ko]), np.concatenate([vp, vo])
+                    dz = (gamma(d) * sc * (np.abs(qq) @ np.abs(kk).T) + 3 * U * sc * np.abs(qq @ kk.T)).max(axis=1)
+                    dz = dz + 3 * U * 40 + (2.0 ** -20 * abs(alpha_c) if R is not None else 0)
+                    E = 2 * dz + 2.0 ** -21 + (2.0 ** -16 if pair else 0)
+                    spread = np.stack([(w[h][:, None] * np.abs(vv - ro[h])).sum(0) for h in range(G)])
+                    lim = 2 * E[:, None] * spread + gamma(n + 64) * (w @ np.abs(vv)) + 1e-30
+                    err = np.abs(go - ro)
+                    assert (err <= lim).all(), (b, l, g, float((err / lim).max()))
+                    assert (np.abs(gl - rl) <= dz + 2.0 ** -20 + gamma(n + 64) + 2 * U * np.abs(rl)).all(), (b, l, g)
+
+
+BF, FP = torch.bfloat16, torch.float32
+SHAPES = [
+    # B, L, Hkv, G, d, P, own, page
+    (1, 1, 1, 1, 128, 1, 1, 16),
+    (2, 2, 2, 4, 128, 129, 33, 16),
+    (3, 3, 2, 7, 128, 500, 70, 32),
+    (8, 2, 4, 7, 128, 777, 130, 64),
+    (16, 1, 8, 4, 128, 1100, 65, 128),
+    (33, 2, 2, 4, 128, 300, 64, 256),       # 132 rows: one query row block and four rows
+    (64, 1, 1, 4, 128, 1000, 200, 16),      # 256 rows
+    (40, 1, 2, 8, 64, 385, 20, 16),         # 320 rows: two row blocks
+    (5, 3, 3, 5, 64, 640, 100, 32),
+    (150, 1, 1, 2, 128, 257, 17, 16),
+]
+
+
+@pytest.mark.parametrize("merged", [False, True])
+@pytest.mark.parametrize("B_,L,Hkv,G,d,P,own,page", SHAPES)
+def test_bf16_matches_the_oracle(B_, L, Hkv, G, d, P, own, page, merged):
+    c = Case(B_, L, Hkv, G, d, P, own, page, merged=merged, seed=P + own)
+    c.run()
+    assert B.kvc_check_status() == 0
+    c.check()
+
+
+@pytest.mark.parametrize("dt,qdt", [(FP, FP), (BF, FP), (FP, BF)])
+@pytest.mark.parametrize("B_,L,Hkv,G,d,P,own,page", [SHAPES[i] for i in (0, 1, 2, 4, 7, 8)])
+def test_fp32_caches_or_queries_match_the_oracle(B_, L, Hkv, G, d, P, own, page, dt, qdt):
+    c = Case(B_, L, Hkv, G, d, P, own, page, dt=dt, qdt=qdt, merged=True, seed=P + own + 1)
+    c.run()
+    assert B.kvc_check_status() == 0
+    c.check(pair=False)
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
+@pytest.mark.parametrize("B_,L,Hkv,G,d,P,own,page", [SHAPES[i] for i in (1, 3, 8)])
+def test_contiguous_own_rows(B_, L, Hkv, G, d, P, own, page, dt):
+    c = Case(B_, L, Hkv, G, d, P, own, 0, dt=dt, seed=3)
+    c.run()
+    assert B.kvc_check_status() == 0
+    c.check()
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
+def test_tokens_first_in_a_page_and_only_one_side(dt):
+    c = Case(4, 2, 3, 4, 128, 200, 90, 32, dt=dt, layout="token", seed=4)
+    c.run()
+    c.check()
+    c = Case(4, 2, 3, 4, 128, 200, 90, 32, dt=dt, seed=5, prompt=False)
+    c.run()
+    c.check()
+    c = Case(4, 2, 3, 4, 128, 200, 90, 32, dt=dt, seed=6, has_own=False)
+    c.run()
+    c.check()
+    assert B.kvc_check_status() == 0
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
+def test_empty_rows_and_edges(dt):
+    """No prompt in a layer, no own rows in a sequence, neither, one key, lengths at tile borders."""
+    lens = [[0, 0, 0, 0, 0], [1, 1, 1, 1, 1], [64, 63, 65, 128, 0], [16, 15, 17, 0, 200]]
+    c = Case(4, 5, 2, 4, 128, 256, 200, 16, dt=dt, seed=7, lens_p=[0, 1, 128, 127, 256], lens=lens, merged=True)
+    c.run()
+    assert B.kvc_check_status() == 0
+    c.check()
+    c = Case(4, 5, 2, 4, 128, 256, 200, 16, dt=dt, seed=8, lens_p=[0] * 5, lens=lens)
+    c.run()
+    c.check()
+    c = Case(2, 2, 1, 4, 64, 100, 50, 16, dt=dt, seed=9, lens_p=[0, 0], lens=[[0, 0], [0, 0]])
+    c.run()
+    c.check()
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
+def test_large_logits_rescale_and_scale_argument(dt):
+    """Logits in the hundreds: the running maximum moves often; a scale and an alpha_c of one's own."""
+    c = Case(9, 1, 2, 4, 128, 900, 100, 16, dt=dt, seed=10, qs=12.0, merged=True)
+    c.run()
+    c.check()
+    c.run(scale=0.25, alpha_c=-0.5)
+    c.check(scale=0.25, alpha_c=-0.5)
+    # keys that grow along the sequence: every tile moves the maximum
+    c.Kp.mul_(torch.linspace(0.01, 2, 900, device=DEV)[:, None].to(dt))
+    c.run()
+    c.check()
+
+
+def test_lengths_and_pages_out_of_bounds_are_clamped_and_recorded():
+    c = Case(3, 2, 2, 4, 128, 200, 60, 16, seed=11, lens_p=[200, 200], lens=np.full((3, 2), 60))
+    kw = c.kw()
+    c.check_ = None
+    B.kvc_prefix_decode_attn(c.m, **{**kw, "lens_prefix": i32([4000, 200])})
+    with pytest.raises(B.KvcError):
+        B.kvc_check_status()
+    c.check()
+    B.kvc_prefix_decode_attn(c.m, **{**kw, "lens": i32([[60, 60], [60, 9000], [60, 60]])})
+    with pytest.raises(B.KvcError):
+        B.kvc_check_status()
+    c.check()
+    # a page id outside the pool reads as rows of zeros
+    t = c.table.clone()
+    t[1, 0, 1] = c.K.shape[0] + 3
+    t[2, 1, 0] = -4
+    B.kvc_prefix_decode_attn(c.m, **{**kw, "table": t})
+    with pytest.raises(B.KvcError):
+        B.kvc_check_status()
+    K = torch.cat([c.K, torch.zeros_like(c.K[:1])])
+    V = torch.cat([c.V, torch.zeros_like(c.V[:1])])
+    t[1, 0, 1] = t[2, 1, 0] = c.K.shape[0]
+    c.K, c.V, c.table = K, V, t
+    c.check()
+
+
+def test_equal_calls_are_bit_identical_and_graphs_replay():
+    c = Case(20, 3, 2, 4, 128, 2000, 150, 16, seed=12, merged=True)
+    ws = c.run()
+    first = (c.o.clone(), c.lse.clone())
+    for _ in range(3):
+        c.o.fill_(float("nan"))
+        ws.fill_(0xff)
+        c.run(workspace=ws)
+        assert torch.equal(c.o, first[0]) and torch.equal(c.lse, first[1])
+    # two graphs with workspaces of their own, replayed on two streams at once
+    other = Case(20, 3, 2, 4, 128, 2000, 150, 16, seed=13)
+    graphs = []
+    for x, w in ((c, ws), (other, torch.empty_like(ws))):
+        x.run(workspace=w)
+        kw = x.kw()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            B.kvc_prefix_decode_attn(x.m, workspace=w, **kw)
+        graphs.append((g, kw, w))
+    want = other.o.clone()
+    c.o.zero_()
+    other.o.zero_()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        with torch.cuda.stream(s1):
+            graphs[0][0].replay()
+        with torch.cuda.stream(s2):
+            graphs[1][0].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(c.o, first[0]) and torch.equal(other.o, want)
+    assert B.kvc_check_status() == 0
+
+
+def test_lse_ring_slot_and_another_stream():
+    c = Case(6, 2, 2, 4, 128, 300, 40, 16, seed=14)
+    ring = torch.zeros(6, 2, 8, 5, device=DEV)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    c.run(lse=ring[..., 3], stream=s)
+    s.synchronize()
+    c.lse = ring[..., 3].contiguous()
+    c.check()
+    ring[..., 3] = 0
+    assert int(torch.count_nonzero(ring)) == 0
+
+
+def test_refusals_launch_nothing():
+    c = Case(2, 1, 2, 4, 128, 64, 40, 16, seed=15)
+    kw = c.kw()
+    ws = c.run()
+    before = B.kvc_launch_count()
+    bad = [dict(workspace=ws[:64]), dict(K=None, V=None, table=None, K_prefix=None, V_prefix=None, R=None), dict(scale=-1.0),
+           dict(scale=float("nan")), dict(lens=i32([[1]])), dict(max_len_prefix=65), dict(max_len=400), dict(o=c.o[:1]),
+           dict(q=c.q.cpu()), dict(table=c.table[:1]), dict(K=c.K.float()), dict(V_prefix=c.Vp.float()),
+           dict(K_prefix=c.Kp[:, :1]), dict(table=c.table.long())]
+    for change in bad:
+        with pytest.raises((ValueError, TypeError, B.KvcError)):
+            B.kvc_prefix_decode_attn(c.m, **{**kw, **change})
+    with pytest.raises(B.KvcError):
+        B.kvc_prefix_decode_attn(B.model(1, 18, 2, 128), q=torch.zeros(2, 1, 18, 128, device=DEV, dtype=BF),
+                                 o=torch.zeros(2, 1, 18, 128, device=DEV), K_prefix=c.Kp, V_prefix=c.Vp,
+                                 lens_prefix=i32([64]), max_len_prefix=64)
+    assert B.kvc_launch_count() == before
