@@ -7,7 +7,10 @@
 // (one M = 128 tile) the pass is bound by HBM, above it by the products.
 //
 // P is carried as a bf16 pair hi + lo (two products with V), about 16 bits of it, so that the
-// fp32 output keeps fp32-level accuracy: with hi alone its error would be 2^-9 a weight.
+// fp32 output keeps fp32-level accuracy: with hi alone its error would be up to 2^-8 a weight.
+// The accumulator in TMEM truncates: left to run over a whole prompt (13107 keys, 1640 products) O
+// came out 3.4e-5 too small.  So a tile's P V starts afresh and the softmax warps add it to O in
+// registers, rounding to nearest.
 //
 // Work: tiles of 128 keys.  All items (l, g, row block) laid end to end are cut into equal runs of
 // tiles, one run a CTA, one CTA an SM (lengths differ by layer; a run may cover the end of
@@ -31,7 +34,7 @@ namespace kvc {
 using namespace tc;
 
 constexpr int PX_KEYS = 128;                    // keys a tile
-constexpr int PX_THREADS = 320;
+constexpr int PX_THREADS = 384;                 // warps 10 and 11 only complete the third warpgroup
 constexpr int PX_ATOM = PX_KEYS * 128;          // 128 rows x 64 bf16, 128B-swizzled (16 KB)
 constexpr int PX_MAXL = 128;                    // layers whose tile sums fit the shared array
 template <int D> constexpr int px_tile() { return (D / 64) * PX_ATOM; }
@@ -76,16 +79,33 @@ struct PxRun {
   }
 };
 
-// Maximum of 32 products (biased, in log2 units, when HAS_R), of which the first n count.
+// Maximum of 32 products, biased and in log2 units when HAS_R.
 template <bool HAS_R>
-__device__ __forceinline__ void px_max(const uint32_t (&r)[32], const float* bias, float qscale, int n, float (&mx)[4]) {
+__device__ __forceinline__ float px_max(const uint32_t (&r)[32], const float* bias, float qscale, float mx) {
+  float m0 = mx, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
 #pragma unroll
-  for (int k = 0; k < 32; ++k) {
-    float x = __uint_as_float(r[k]);
-    if (HAS_R) x = fmaf(x, qscale, bias[k]);
-    if (n < 32) x = k < n ? x : -INFINITY;
-    mx[k & 3] = fmaxf(mx[k & 3], x);
+  for (int k = 0; k < 32; k += 8) {
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; e += 4) {
+      const float4 bb = HAS_R ? *reinterpret_cast<const float4*>(bias + k + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+      x[e] = __uint_as_float(r[k + e]);
+      x[e + 1] = __uint_as_float(r[k + e + 1]);
+      x[e + 2] = __uint_as_float(r[k + e + 2]);
+      x[e + 3] = __uint_as_float(r[k + e + 3]);
+      if (HAS_R) {
+        x[e] = fmaf(x[e], qscale, bb.x);
+        x[e + 1] = fmaf(x[e + 1], qscale, bb.y);
+        x[e + 2] = fmaf(x[e + 2], qscale, bb.z);
+        x[e + 3] = fmaf(x[e + 3], qscale, bb.w);
+      }
+    }
+    m0 = fmaxf(m0, fmaxf(x[0], x[1]));
+    m1 = fmaxf(m1, fmaxf(x[2], x[3]));
+    m2 = fmaxf(m2, fmaxf(x[4], x[5]));
+    m3 = fmaxf(m3, fmaxf(x[6], x[7]));
   }
+  return fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
 }
 
 template <int D, int MT, bool HAS_R>
@@ -157,7 +177,10 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
   run.l = 0;
   PxSeg sg;
 
-  if (warp == 8) {
+  // registers: 3 x 168 a thread at launch = 2 x 232 + 40
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp == 8) {
     // ------------------------------------------------------------ loads
     if (lane == 0) {
       uint32_t tc = 0, issued_k = 0, issued_v = 0;
@@ -208,8 +231,8 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
           fence_after();
           const uint8_t* q = Qs + (MT == 2 ? w : 0) * TILE;
           const uint64_t da = sw128_desc(q), db = sw128_desc(Ks + ks * TILE);
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
+#pragma unroll 1
+          for (int k = 0; k < D / 16; ++k) {    // (rolled: this warp has few registers)
             const uint64_t off = (uint64_t)((k >> 2) * (PX_ATOM >> 4) + (k & 3) * 2);
             mma_bf16(tmem + w * 128, da + off, db + off, idS, k > 0);
           }
@@ -227,15 +250,14 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
           fence_after();
           const uint64_t dv = sw128_desc_mn(Vs + vs * TILE, PX_ATOM);
           const uint32_t ta = tmem + w * 128, to = tmem + 256 + w * 128;
-          const bool fresh = MT == 2 ? i == 0 : u < 2;   // the warpgroup's first tile of this piece
-#pragma unroll
-          for (int k = 0; k < PX_KEYS / 16; ++k) {
-            // keys 16 k ..: P hi in 8 columns, P lo 16 columns further; V rows 16 k ..
-            const uint32_t a = ta + (k >> 1) * 32 + (k & 1) * 8;
-            const uint64_t b = dv + (uint64_t)(k * 16 * 128 >> 4);
-            mma_bf16_ts(to, a, b, idO, !(fresh && k == 0));
-            mma_bf16_ts(to, a + 16, b, idO, 1);
-          }
+          // P lo first: the tensor core truncates its fp32 accumulator at every product, and the lo
+          // parts leave it small, so 8 roundings a tile count, not 16 (see the head of the file)
+#pragma unroll 1
+          for (int k = 0; k < PX_KEYS / 16; ++k)
+            mma_bf16_ts(to, ta + k * 16 + 8, dv + (uint64_t)(k * 16 * 128 >> 4), idO, k > 0);
+#pragma unroll 1
+          for (int k = 0; k < PX_KEYS / 16; ++k)
+            mma_bf16_ts(to, ta + k * 16, dv + (uint64_t)(k * 16 * 128 >> 4), idO, 1);
           mma_commit(&c->o_ready[w]);
           if (MT == 1 || w == 1) mma_commit(&c->emptyV[vs]);
           if (u + 2 < U) {
@@ -251,7 +273,9 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
       mma_commit(&c->drain);
       mbar_wait(&c->drain, 0, &none, p.status);
     }
+    }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     // ------------------------------------------------------------ softmax
     const int w = warp >> 2, row = (warp & 3) * 32 + lane;   // row = TMEM lane
     const uint32_t tS = tmem + w * 128 + ((uint32_t)((warp & 3) * 32) << 16);
@@ -300,6 +324,9 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
         rnext = k < len ? __ldg(Rr + k) : 1.f;
       }
       int mine = 0;
+      float acc[D];                             // O of the row
+#pragma unroll
+      for (int k = 0; k < D; ++k) acc[k] = 0.f;
       for (int i = i0; i < sg.n; i += di, ++mine) {
         const int key0 = (sg.t0 + i) * PX_KEYS, nk = min(PX_KEYS, len - key0);
         const float* bias = c->bias[w][mine & 1];
@@ -337,73 +364,84 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
         if (live) {
-          // the row's maximum, then P, both from TMEM: holding the 128 products in registers spilled
-          float mt;
-          {
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          if (nk < PX_KEYS) {
+            // products of keys past the length: -infinity, before anything reads them
+#pragma unroll 1
+            for (int q4 = nk >> 5; q4 < 4; ++q4) {
+              uint32_t x[32];
+              tmem_ld32_raw(tS + q4 * 32, x);
+              tmem_wait_ld32(x);
 #pragma unroll
-            for (int q4 = 0; q4 < 4; q4 += 2) {
-              uint32_t ra[32], rb[32];
-              tmem_ld32_raw(tS + q4 * 32, ra);
-              tmem_ld32_raw(tS + q4 * 32 + 32, rb);
-              tmem_wait_ld32(ra);
-              tmem_wait_ld32(rb);
-              px_max<HAS_R>(ra, bias + q4 * 32, p.qscale, nk - q4 * 32, mx);
-              px_max<HAS_R>(rb, bias + q4 * 32 + 32, p.qscale, nk - q4 * 32 - 32, mx);
+              for (int k = 0; k < 32; ++k) x[k] = q4 * 32 + k < nk ? x[k] : 0xff800000u;
+              tmem_st32(tS + q4 * 32, x);
             }
-            mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            tmem_wait_st();
+          }
+          float mt = -INFINITY;
+#pragma unroll
+          for (int q4 = 0; q4 < 4; q4 += 2) {
+            uint32_t ra[32], rb[32];
+            tmem_ld32_raw(tS + q4 * 32, ra);
+            tmem_ld32_raw(tS + q4 * 32 + 32, rb);
+            tmem_wait_ld32(ra);
+            tmem_wait_ld32(rb);
+            mt = px_max<HAS_R>(ra, bias + q4 * 32, p.qscale, mt);
+            mt = px_max<HAS_R>(rb, bias + q4 * 32 + 32, p.qscale, mt);
           }
           if (!HAS_R) mt *= p.qscale;           // qscale > 0: the maximum of the products
           // the running maximum moves only when it grows by more than 2^8: sums and O stay within
           // fp32 range and most tiles rescale nothing
           const bool grow = mt > m + 8.f;
-          if (__any_sync(FULL, grow)) {
-            const float corr = grow ? ex2(m - mt) : 1.f;   // 0 while nothing was seen
-            if (grow) m = mt;
-            lsum *= corr;
-            if (mine > 0) {
-#pragma unroll
-              for (int q4 = 0; q4 < D / 32; ++q4) {
-                uint32_t o[32];
-                tmem_ld32_raw(tO + q4 * 32, o);
-                tmem_wait_ld32(o);
-#pragma unroll
-                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * corr);
-                tmem_st32(tO + q4 * 32, o);
-              }
-            }
-          }
+          const bool rescale = __any_sync(FULL, grow);
+          const float corr = grow ? ex2(m - mt) : 1.f;   // 0 while nothing was seen
+          if (grow) m = mt;
+          lsum *= corr;
           const float mref = m == -INFINITY ? 0.f : m;
+          const uint64_t qs2 = pk2(p.qscale, p.qscale), nm2 = pk2(-mref, -mref), neg1 = pk2(-1.f, -1.f);
+          uint64_t sum2 = 0;
 #pragma unroll
           for (int q4 = 0; q4 < 4; ++q4) {
-            uint32_t x[32], u[32];
-            tmem_ld32_raw(tS + q4 * 32, x);
-            tmem_wait_ld32(x);
-            float s0 = 0.f, s1 = 0.f;
+            // 32 dimensions of the tile before's P V (done: S waited for it), then 32 keys' products
+            if (q4 < D / 32 && mine > 0) {
 #pragma unroll
-            for (int k = 0; k < 32; k += 2) {
-              float a = __uint_as_float(x[k]), b = __uint_as_float(x[k + 1]);
-              if (HAS_R) {
-                const float2 bb = *reinterpret_cast<const float2*>(bias + q4 * 32 + k);
-                a = ex2(fmaf(a, p.qscale, bb.x - mref));
-                b = ex2(fmaf(b, p.qscale, bb.y - mref));
-              } else {
-                a = ex2(fmaf(a, p.qscale, -mref));
-                b = ex2(fmaf(b, p.qscale, -mref));
+              for (int h = 0; h < 2; ++h) {
+                uint32_t t[16];
+                tmem_ld16_raw(tO + q4 * 32 + h * 16, t);
+                tmem_wait_ld16(t);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) acc[q4 * 32 + h * 16 + k] += __uint_as_float(t[k]);
               }
-              if (nk < PX_KEYS) {
-                a = q4 * 32 + k < nk ? a : 0.f;
-                b = q4 * 32 + k + 1 < nk ? b : 0.f;
+              if (rescale) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) acc[q4 * 32 + k] *= corr;
               }
-              s0 += a;
-              s1 += b;
-              const uint32_t hi = pack_bf16x2(a, b);
-              u[k >> 1] = hi;
-              u[16 + (k >> 1)] = pack_bf16x2(a - bf_lo(hi), b - bf_hi(hi));
             }
-            lsum += s0 + s1;
-            tmem_st32(tS + q4 * 32, u);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t x[16], u[16];
+              tmem_ld16_raw(tS + q4 * 32 + h * 16, x);
+              tmem_wait_ld16(x);
+#pragma unroll
+              for (int k = 0; k < 16; k += 2) {
+                uint64_t off = nm2;
+                if (HAS_R) {
+                  const float2 bb = *reinterpret_cast<const float2*>(bias + q4 * 32 + h * 16 + k);
+                  off = add2(pk2(bb.x, bb.y), nm2);
+                }
+                const float2 y = upk2(fma2(pk2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), qs2, off));
+                const float a = ex2(y.x), b = ex2(y.y);
+                const uint64_t ab = pk2(a, b);
+                sum2 = add2(sum2, ab);
+                const uint32_t hi = pack_bf16x2(a, b);
+                const float2 lo = upk2(fma2(pk2(bf_lo(hi), bf_hi(hi)), neg1, ab));
+                u[k >> 1] = hi;
+                u[8 + (k >> 1)] = pack_bf16x2(lo.x, lo.y);
+              }
+              tmem_st16(tS + q4 * 32 + h * 16, u);
+            }
           }
+          const float2 s2 = upk2(sum2);
+          lsum += s2.x + s2.y;
           tmem_wait_st();
         }
         fence_before();
@@ -427,12 +465,16 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
           p.pp.ml[rec] = make_float2(m, lsum);
 #pragma unroll
           for (int q4 = 0; q4 < D / 32; ++q4) {
-            uint32_t o[32];
-            tmem_ld32_raw(tO + q4 * 32, o);
-            tmem_wait_ld32(o);
+            uint32_t t[32];
+            tmem_ld32_raw(tO + q4 * 32, t);
+            tmem_wait_ld32(t);
 #pragma unroll
-            for (int k = 0; k < 32; k += 4)
-              *reinterpret_cast<uint4*>(p.pp.o + rec * D + q4 * 32 + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+            for (int k = 0; k < 32; k += 4) {
+              const float* x = acc + q4 * 32 + k;
+              *reinterpret_cast<float4*>(p.pp.o + rec * D + q4 * 32 + k) =
+                  make_float4(x[0] + __uint_as_float(t[k]), x[1] + __uint_as_float(t[k + 1]),
+                              x[2] + __uint_as_float(t[k + 2]), x[3] + __uint_as_float(t[k + 3]));
+            }
           }
         }
         fence_before();
