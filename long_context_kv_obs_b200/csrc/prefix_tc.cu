@@ -27,6 +27,8 @@
 // works on its S the tensor cores run the other's products.
 #include <cudaTypedefs.h>
 
+#include <type_traits>
+
 #include "kernels.cuh"
 #include "tc_sm100.cuh"
 
@@ -213,66 +215,79 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------ products
-    if (lane == 0) {
+    // The whole warp runs the loop and one lane issues: addresses that are known to be the same in
+    // all lanes live in uniform registers, where the products' descriptors are wanted (issued by a
+    // lone thread each product took 80 to 150 cycles to issue for 53 of work).
       constexpr uint32_t idS = idesc_bf16(128, PX_KEYS);
       constexpr uint32_t idO = idesc_bf16(128, D) | IDESC_B_MN;
+      const uint32_t tm = __shfl_sync(FULL, tmem, 0);
+      const uint32_t q0 = __shfl_sync(FULL, smem_u32(Qs), 0), k0 = q0 + MT * TILE, v0 = k0 + NK * TILE;
       uint32_t tc = 0, nseg = 0, pv[2] = {0, 0};   // tiles, pieces and P V products so far
       bool ok = true;
       while (ok && run.next(p, c->cum, sg)) {
         ok = mbar_wait(&c->q_ready, nseg & 1, abort, p.status);
+        ok = __all_sync(FULL, ok);
         ++nseg;
-        const int U = MT * sg.n;                  // steps: (tile, warpgroup)
-        auto issue_s = [&](int u) {
-          const int w = u & 1, i = MT == 2 ? u >> 1 : u;
-          const uint32_t t = tc + i, ks = t % NK;
+        const int n = __shfl_sync(FULL, sg.n, 0), U = MT * n;   // steps: (tile, warpgroup)
+        auto issue_s = [&](int u, auto wc) {
+          constexpr int w = decltype(wc)::value;
+          const uint32_t t = tc + (MT == 2 ? u >> 1 : u), ks = t % NK;
           if (MT == 1 || w == 0) {
-            if (!mbar_wait(&c->fullK[ks], (t / NK) & 1, abort, p.status)) return false;
+            if (!__all_sync(FULL, mbar_wait(&c->fullK[ks], (t / NK) & 1, abort, p.status))) return false;
           }
           fence_after();
-          const uint8_t* q = Qs + (MT == 2 ? w : 0) * TILE;
-          const uint64_t da = sw128_desc(q), db = sw128_desc(Ks + ks * TILE);
-#pragma unroll 1
-          for (int k = 0; k < D / 16; ++k) {    // (rolled: this warp has few registers)
-            const uint64_t off = (uint64_t)((k >> 2) * (PX_ATOM >> 4) + (k & 3) * 2);
-            mma_bf16(tmem + w * 128, da + off, db + off, idS, k > 0);
+          const uint64_t da = sw128_desc_at(q0 + (MT == 2 ? w : 0) * TILE, 16);
+          const uint64_t db = sw128_desc_at(k0 + ks * TILE, 16);
+          if (elect_one()) {
+            if constexpr (D == 128) mma_bf16_k128(tm + w * 128, da, db, PX_ATOM >> 4, PX_ATOM >> 4, idS);
+            else mma_bf16_k64(tm + w * 128, da, db, idS);
+            mma_commit(&c->s_ready[w]);
+            if (MT == 1 || w == 1) mma_commit(&c->emptyK[ks]);
           }
-          mma_commit(&c->s_ready[w]);
-          if (MT == 1 || w == 1) mma_commit(&c->emptyK[ks]);
+          __syncwarp();
           return true;
         };
-        for (int u = 0; u < 2 && u < U && ok; ++u) ok = issue_s(u);
-        for (int u = 0; u < U && ok; ++u) {
-          const int w = u & 1, i = MT == 2 ? u >> 1 : u;
-          const uint32_t t = tc + i, vs = t % NV;
-          ok = mbar_wait(&c->fullV[vs], (t / NV) & 1, abort, p.status) &&
-               mbar_wait(&c->p_ready[w], pv[w] & 1, abort, p.status);
-          if (!ok) break;
+        auto step = [&](int u, auto wc) {
+          constexpr int w = decltype(wc)::value;
+          const uint32_t t = tc + (MT == 2 ? u >> 1 : u), vs = t % NV;
+          if (!__all_sync(FULL, mbar_wait(&c->fullV[vs], (t / NV) & 1, abort, p.status) &&
+                                    mbar_wait(&c->p_ready[w], pv[w] & 1, abort, p.status)))
+            return false;
           fence_after();
-          const uint64_t dv = sw128_desc_mn(Vs + vs * TILE, PX_ATOM);
-          const uint32_t ta = tmem + w * 128, to = tmem + 256 + w * 128;
-          // P lo first: the tensor core truncates its fp32 accumulator at every product, and the lo
-          // parts leave it small, so 8 roundings a tile count, not 16 (see the head of the file)
-#pragma unroll 1
-          for (int k = 0; k < PX_KEYS / 16; ++k)
-            mma_bf16_ts(to, ta + k * 16 + 8, dv + (uint64_t)(k * 16 * 128 >> 4), idO, k > 0);
-#pragma unroll 1
-          for (int k = 0; k < PX_KEYS / 16; ++k)
-            mma_bf16_ts(to, ta + k * 16, dv + (uint64_t)(k * 16 * 128 >> 4), idO, 1);
-          mma_commit(&c->o_ready[w]);
-          if (MT == 1 || w == 1) mma_commit(&c->emptyV[vs]);
+          const uint64_t dv = sw128_desc_at(v0 + vs * TILE, PX_ATOM);
+          const uint32_t ta = tm + w * 128, to = tm + 256 + w * 128;
+          if (elect_one()) {
+            // P lo first: the tensor core truncates its fp32 accumulator at every product, and the lo
+            // parts leave it small, so 8 roundings a tile count, not 16 (see the head of the file)
+            mma_bf16_ts_k128(to, ta + 8, dv, idO, 0);
+            mma_bf16_ts_k128(to, ta, dv, idO, 1);
+            mma_commit(&c->o_ready[w]);
+            if (MT == 1 || w == 1) mma_commit(&c->emptyV[vs]);
+          }
+          __syncwarp();
+          bool good = true;
           if (u + 2 < U) {
             // the next S of this warpgroup overwrites the P that these products read
-            ok = mbar_wait(&c->o_ready[w], pv[w] & 1, abort, p.status) && issue_s(u + 2);
+            good = __all_sync(FULL, mbar_wait(&c->o_ready[w], pv[w] & 1, abort, p.status)) && issue_s(u + 2, wc);
           }
           ++pv[w];
+          return good;
+        };
+        constexpr std::integral_constant<int, 0> W0{};
+        constexpr std::integral_constant<int, 1> W1{};
+        if (ok) ok = issue_s(0, W0);
+        if (ok && U > 1) ok = issue_s(1, W1);
+        for (int u = 0; u < U && ok; u += 2) {
+          ok = step(u, W0);
+          if (ok && u + 1 < U) ok = step(u + 1, W1);
         }
-        tc += sg.n;
+        tc += n;
       }
       // every arrive issued above has landed before shared memory is given up
       int none = 0;
-      mma_commit(&c->drain);
+      if (elect_one()) mma_commit(&c->drain);
+      __syncwarp();
       mbar_wait(&c->drain, 0, &none, p.status);
-    }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
@@ -377,16 +392,25 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
             }
             tmem_wait_st();
           }
+          // TMEM loads run one chunk ahead of the arithmetic (a wait covers all loads before it)
           float mt = -INFINITY;
-#pragma unroll
-          for (int q4 = 0; q4 < 4; q4 += 2) {
+          uint32_t xa[16], xb[16], t[16];
+          {
             uint32_t ra[32], rb[32];
-            tmem_ld32_raw(tS + q4 * 32, ra);
-            tmem_ld32_raw(tS + q4 * 32 + 32, rb);
+            tmem_ld32_raw(tS, ra);
             tmem_wait_ld32(ra);
+            tmem_ld32_raw(tS + 32, rb);
+            mt = px_max<HAS_R>(ra, bias, p.qscale, mt);
             tmem_wait_ld32(rb);
-            mt = px_max<HAS_R>(ra, bias + q4 * 32, p.qscale, mt);
-            mt = px_max<HAS_R>(rb, bias + q4 * 32 + 32, p.qscale, mt);
+            tmem_ld32_raw(tS + 64, ra);
+            mt = px_max<HAS_R>(rb, bias + 32, p.qscale, mt);
+            tmem_wait_ld32(ra);
+            tmem_ld32_raw(tS + 96, rb);
+            mt = px_max<HAS_R>(ra, bias + 64, p.qscale, mt);
+            tmem_wait_ld32(rb);
+            tmem_ld16_raw(tS, xa);
+            if (mine > 0) tmem_ld16_raw(tO, t);
+            mt = px_max<HAS_R>(rb, bias + 96, p.qscale, mt);
           }
           if (!HAS_R) mt *= p.qscale;           // qscale > 0: the maximum of the products
           // the running maximum moves only when it grows by more than 2^8: sums and O stay within
@@ -399,46 +423,46 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
           const float mref = m == -INFINITY ? 0.f : m;
           const uint64_t qs2 = pk2(p.qscale, p.qscale), nm2 = pk2(-mref, -mref), neg1 = pk2(-1.f, -1.f);
           uint64_t sum2 = 0;
-#pragma unroll
-          for (int q4 = 0; q4 < 4; ++q4) {
-            // 32 dimensions of the tile before's P V (done: S waited for it), then 32 keys' products
-            if (q4 < D / 32 && mine > 0) {
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                uint32_t t[16];
-                tmem_ld16_raw(tO + q4 * 32 + h * 16, t);
+          // chunk q: 16 dimensions of the tile before's P V (done: S waited for it) into O, and the P
+          // of 16 keys from x, while the loads of chunk q + 1 go to xn and t
+          auto chunk = [&](int q, uint32_t (&x)[16], uint32_t (&xn)[16]) {
+            tmem_wait_ld16(x);
+            if (q < D / 16) {
+              if (mine > 0) {
                 tmem_wait_ld16(t);
 #pragma unroll
-                for (int k = 0; k < 16; ++k) acc[q4 * 32 + h * 16 + k] += __uint_as_float(t[k]);
-              }
-              if (rescale) {
+                for (int k = 0; k < 16; ++k) acc[q * 16 + k] += __uint_as_float(t[k]);
+                if (rescale) {
 #pragma unroll
-                for (int k = 0; k < 32; ++k) acc[q4 * 32 + k] *= corr;
-              }
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t x[16], u[16];
-              tmem_ld16_raw(tS + q4 * 32 + h * 16, x);
-              tmem_wait_ld16(x);
-#pragma unroll
-              for (int k = 0; k < 16; k += 2) {
-                uint64_t off = nm2;
-                if (HAS_R) {
-                  const float2 bb = *reinterpret_cast<const float2*>(bias + q4 * 32 + h * 16 + k);
-                  off = add2(pk2(bb.x, bb.y), nm2);
+                  for (int k = 0; k < 16; ++k) acc[q * 16 + k] *= corr;
                 }
-                const float2 y = upk2(fma2(pk2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), qs2, off));
-                const float a = ex2(y.x), b = ex2(y.y);
-                const uint64_t ab = pk2(a, b);
-                sum2 = add2(sum2, ab);
-                const uint32_t hi = pack_bf16x2(a, b);
-                const float2 lo = upk2(fma2(pk2(bf_lo(hi), bf_hi(hi)), neg1, ab));
-                u[k >> 1] = hi;
-                u[8 + (k >> 1)] = pack_bf16x2(lo.x, lo.y);
+                if (q + 1 < D / 16) tmem_ld16_raw(tO + q * 16 + 16, t);
               }
-              tmem_st16(tS + q4 * 32 + h * 16, u);
             }
+            if (q + 1 < PX_KEYS / 16) tmem_ld16_raw(tS + q * 16 + 16, xn);
+            uint32_t u[16];
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+              uint64_t off = nm2;
+              if (HAS_R) {
+                const float2 bb = *reinterpret_cast<const float2*>(bias + q * 16 + k);
+                off = add2(pk2(bb.x, bb.y), nm2);
+              }
+              const float2 y = upk2(fma2(pk2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), qs2, off));
+              const float a = ex2(y.x), b = ex2(y.y);
+              const uint64_t ab = pk2(a, b);
+              sum2 = add2(sum2, ab);
+              const uint32_t hi = pack_bf16x2(a, b);
+              const float2 lo = upk2(fma2(pk2(bf_lo(hi), bf_hi(hi)), neg1, ab));
+              u[k >> 1] = hi;
+              u[8 + (k >> 1)] = pack_bf16x2(lo.x, lo.y);
+            }
+            tmem_st16(tS + q * 16, u);
+          };
+#pragma unroll
+          for (int q = 0; q < PX_KEYS / 16; q += 2) {
+            chunk(q, xa, xb);
+            chunk(q + 1, xb, xa);
           }
           const float2 s2 = upk2(sum2);
           lsum += s2.x + s2.y;

@@ -137,6 +137,13 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok));
+  return ok != 0;
+}
+
 // ------------------------------------------------------------------ tcgen05
 __device__ __forceinline__ void tmem_alloc(uint32_t* holder, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(holder)),
@@ -188,14 +195,41 @@ __device__ __forceinline__ void mma_bf16_k128(uint32_t d_tmem, uint64_t a0, uint
       "l"(b[1]), "l"(b[2]), "l"(b[3]), "l"(b[4]), "l"(b[5]), "l"(b[6]), "l"(b[7]), "r"(idesc)
       : "memory");
 }
-// D[tmem] (+)= A[tmem] * B[smem]^T: A's rows are TMEM lanes, two bf16 of the K dimension in a
-// 32-bit column (K = 16 takes 8 columns).
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t accumulate) {
+// The same over K = 64 (four steps inside one atom).
+__device__ __forceinline__ void mma_bf16_k64(uint32_t d_tmem, uint64_t a0, uint64_t b0, uint32_t idesc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p0, p1;\n .reg .b64 a1, a2, a3, b1, b2, b3;\n"
+      " setp.ne.b32 p0, %3, %3;\n setp.eq.b32 p1, %3, %3;\n"
+      " add.s64 a1, %1, 2;\n add.s64 a2, %1, 4;\n add.s64 a3, %1, 6;\n"
+      " add.s64 b1, %2, 2;\n add.s64 b2, %2, 4;\n add.s64 b3, %2, 6;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, p1;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, p1;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, p1;\n}\n" ::"r"(d_tmem),
+      "l"(a0), "l"(b0), "r"(idesc)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem]^T over K = 128 (eight K = 16 steps) in one asm block.  A's rows are
+// TMEM lanes, two bf16 of the K dimension in a 32-bit column; step k's 8 columns start at
+// a0 + 16 k.  B is M/N-major: a step is 16 rows of 128 bytes.  first 0: the first step overwrites D.
+__device__ __forceinline__ void mma_bf16_ts_k128(uint32_t d_tmem, uint32_t a0, uint64_t b0, uint32_t idesc,
+                                                 uint32_t first) {
+  asm volatile(
+      "{\n .reg .pred p0, p1;\n .reg .b64 b1, b2, b3, b4, b5, b6, b7;\n .reg .b32 a1, a2, a3, a4, a5, a6, a7;\n"
+      " setp.ne.b32 p0, %4, 0;\n setp.eq.b32 p1, %3, %3;\n"
+      " add.u32 a1, %1, 16;\n add.u32 a2, %1, 32;\n add.u32 a3, %1, 48;\n add.u32 a4, %1, 64;\n"
+      " add.u32 a5, %1, 80;\n add.u32 a6, %1, 96;\n add.u32 a7, %1, 112;\n"
+      " add.s64 b1, %2, 128;\n add.s64 b2, %2, 256;\n add.s64 b3, %2, 384;\n add.s64 b4, %2, 512;\n"
+      " add.s64 b5, %2, 640;\n add.s64 b6, %2, 768;\n add.s64 b7, %2, 896;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, p1;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, p1;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, p1;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [a4], b4, %3, p1;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [a5], b5, %3, p1;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [a6], b6, %3, p1;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [a7], b7, %3, p1;\n}\n" ::"r"(d_tmem),
+      "r"(a0), "l"(b0), "r"(idesc), "r"(first)
       : "memory");
 }
 // Arrive on `bar` once every tcgen05 operation issued so far by this thread has completed.
@@ -309,12 +343,11 @@ __device__ __forceinline__ uint64_t sw128_desc(const void* smem) {
   const uint64_t a = smem_u32(smem);
   return ((a & 0x3FFFFull) >> 4) | (1ull << 16) | ((1024ull >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
-// The same for an operand whose M / N dimension runs along the rows' 128 bytes (64 elements to an
-// atom row, one row a K index, 8-row groups 1024 B apart): group_bytes from one 64-element
-// group to the next.
-__device__ __forceinline__ uint64_t sw128_desc_mn(const void* smem, uint32_t group_bytes) {
-  const uint64_t a = smem_u32(smem);
-  return ((a & 0x3FFFFull) >> 4) | ((uint64_t)(group_bytes >> 4) << 16) | ((1024ull >> 4) << 32) | (1ull << 46) |
+// The same from a shared-memory address, for either operand form.  An operand whose M / N dimension
+// runs along the rows' 128 bytes (64 elements to an atom row, one row a K index, 8-row groups
+// 1024 B apart) gives the bytes from one 64-element group to the next; K-major operands give 16.
+__device__ __forceinline__ uint64_t sw128_desc_at(uint32_t addr, uint32_t group_bytes) {
+  return ((addr & 0x3FFFFull) >> 4) | ((uint64_t)(group_bytes >> 4) << 16) | ((1024ull >> 4) << 32) | (1ull << 46) |
          (2ull << 61);
 }
 constexpr uint32_t IDESC_B_MN = 1u << 16;     // instruction descriptor: B is M/N-major
