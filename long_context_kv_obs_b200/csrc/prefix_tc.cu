@@ -110,6 +110,24 @@ __device__ __forceinline__ float px_max(const uint32_t (&r)[32], const float* bi
   return fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
 }
 
+// acc += the row's D columns of O in TMEM.
+template <int D>
+__device__ __forceinline__ void px_add_o(uint32_t tO, float (&acc)[D]) {
+  uint32_t a[32], b[32];
+  tmem_ld32_raw(tO, a);
+#pragma unroll
+  for (int q = 0; q < D / 32; q += 2) {
+    tmem_wait_ld32(a);
+    tmem_ld32_raw(tO + q * 32 + 32, b);
+#pragma unroll
+    for (int k = 0; k < 32; ++k) acc[q * 32 + k] += __uint_as_float(a[k]);
+    tmem_wait_ld32(b);
+    if (q + 2 < D / 32) tmem_ld32_raw(tO + q * 32 + 64, a);
+#pragma unroll
+    for (int k = 0; k < 32; ++k) acc[q * 32 + 32 + k] += __uint_as_float(b[k]);
+  }
+}
+
 template <int D, int MT, bool HAS_R>
 __global__ void __launch_bounds__(PX_THREADS, 1)
 prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
@@ -357,6 +375,16 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
           const int k = key0 + di * PX_KEYS + wt;
           rnext = i + di < sg.n && k < len ? __ldg(Rr + k) : 1.f;
         }
+        if (mine > 0) {
+          // the tile before's P V, while the tensor cores work on this tile's S
+          ok = mbar_wait(&c->o_ready[w], (steps - 1) & 1, abort, p.status);
+          if (!__all_sync(FULL, ok)) {
+            ok = false;
+            break;
+          }
+          fence_after();
+          if (live) px_add_o<D>(tO, acc);
+        }
         ok = mbar_wait(&c->s_ready[w], steps & 1, abort, p.status);
         if (!__all_sync(FULL, ok)) {
           ok = false;
@@ -394,7 +422,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
           }
           // TMEM loads run one chunk ahead of the arithmetic (a wait covers all loads before it)
           float mt = -INFINITY;
-          uint32_t xa[16], xb[16], t[16];
+          uint32_t xa[16], xb[16], ua[16], ub[16];
           {
             uint32_t ra[32], rb[32];
             tmem_ld32_raw(tS, ra);
@@ -409,7 +437,6 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
             mt = px_max<HAS_R>(ra, bias + 64, p.qscale, mt);
             tmem_wait_ld32(rb);
             tmem_ld16_raw(tS, xa);
-            if (mine > 0) tmem_ld16_raw(tO, t);
             mt = px_max<HAS_R>(rb, bias + 96, p.qscale, mt);
           }
           if (!HAS_R) mt *= p.qscale;           // qscale > 0: the maximum of the products
@@ -419,28 +446,20 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
           const bool rescale = __any_sync(FULL, grow);
           const float corr = grow ? ex2(m - mt) : 1.f;   // 0 while nothing was seen
           if (grow) m = mt;
-          lsum *= corr;
+          if (rescale) {
+            lsum *= corr;
+#pragma unroll
+            for (int k = 0; k < D; ++k) acc[k] *= corr;
+          }
           const float mref = m == -INFINITY ? 0.f : m;
           const uint64_t qs2 = pk2(p.qscale, p.qscale), nm2 = pk2(-mref, -mref), neg1 = pk2(-1.f, -1.f);
           uint64_t sum2 = 0;
-          // chunk q: 16 dimensions of the tile before's P V (done: S waited for it) into O, and the P
-          // of 16 keys from x, while the loads of chunk q + 1 go to xn and t
-          auto chunk = [&](int q, uint32_t (&x)[16], uint32_t (&xn)[16]) {
+          // chunk q: P of 16 keys from x to u, while the loads of chunk q + 1 go to xn and the store of
+          // chunk q - 1 (un) is under way
+          auto chunk = [&](int q, uint32_t (&x)[16], uint32_t (&xn)[16], uint32_t (&u)[16], uint32_t (&un)[16]) {
             tmem_wait_ld16(x);
-            if (q < D / 16) {
-              if (mine > 0) {
-                tmem_wait_ld16(t);
-#pragma unroll
-                for (int k = 0; k < 16; ++k) acc[q * 16 + k] += __uint_as_float(t[k]);
-                if (rescale) {
-#pragma unroll
-                  for (int k = 0; k < 16; ++k) acc[q * 16 + k] *= corr;
-                }
-                if (q + 1 < D / 16) tmem_ld16_raw(tO + q * 16 + 16, t);
-              }
-            }
             if (q + 1 < PX_KEYS / 16) tmem_ld16_raw(tS + q * 16 + 16, xn);
-            uint32_t u[16];
+            if (q > 0) tmem_st16(tS + q * 16 - 16, un);
 #pragma unroll
             for (int k = 0; k < 16; k += 2) {
               uint64_t off = nm2;
@@ -457,13 +476,13 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
               u[k >> 1] = hi;
               u[8 + (k >> 1)] = pack_bf16x2(lo.x, lo.y);
             }
-            tmem_st16(tS + q * 16, u);
           };
 #pragma unroll
           for (int q = 0; q < PX_KEYS / 16; q += 2) {
-            chunk(q, xa, xb);
-            chunk(q + 1, xb, xa);
+            chunk(q, xa, xb, ua, ub);
+            chunk(q + 1, xb, xa, ub, ua);
           }
+          tmem_st16(tS + PX_KEYS - 16, ub);
           const float2 s2 = upk2(sum2);
           lsum += s2.x + s2.y;
           tmem_wait_st();
@@ -487,19 +506,10 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
         fence_after();
         if (live) {
           p.pp.ml[rec] = make_float2(m, lsum);
+          px_add_o<D>(tO, acc);
 #pragma unroll
-          for (int q4 = 0; q4 < D / 32; ++q4) {
-            uint32_t t[32];
-            tmem_ld32_raw(tO + q4 * 32, t);
-            tmem_wait_ld32(t);
-#pragma unroll
-            for (int k = 0; k < 32; k += 4) {
-              const float* x = acc + q4 * 32 + k;
-              *reinterpret_cast<float4*>(p.pp.o + rec * D + q4 * 32 + k) =
-                  make_float4(x[0] + __uint_as_float(t[k]), x[1] + __uint_as_float(t[k + 1]),
-                              x[2] + __uint_as_float(t[k + 2]), x[3] + __uint_as_float(t[k + 3]));
-            }
-          }
+          for (int k = 0; k < D; k += 4)
+            *reinterpret_cast<float4*>(p.pp.o + rec * D + k) = make_float4(acc[k], acc[k + 1], acc[k + 2], acc[k + 3]);
         }
         fence_before();
       } else if (live) {
