@@ -700,10 +700,15 @@ def kvc_append(m: Model, *, k, v, K, V, lens, pos: int, side_pos=None, side_H=No
 
 def _one_device(*tensors):
     """Every tensor given lives on the current CUDA device (the library launches there)."""
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -1
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != dev):
+        if t is not None and (t.get_device() != dev or dev < 0):
             raise ValueError(f"tensor on {t.device}: device tensors of the current device (cuda:{dev}) required")
+
+
+def _raw_stream(stream) -> int:
+    """Handle of `stream`, or of the current stream without building a Stream object for it."""
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _flat(t: Optional[torch.Tensor], name: str, dtype, n: int) -> Optional[int]:
@@ -718,12 +723,13 @@ def _flat(t: Optional[torch.Tensor], name: str, dtype, n: int) -> Optional[int]:
 
 
 def _own_ws(op, m, args, workspace, device, stream):
-    """The workspace (None where none is needed); one allocated here is held for `stream`."""
-    need = workspace_size(op, m, args)
+    """(workspace, its bytes).  A workspace given is checked by the library; without one, the bytes
+    it wants are allocated here (None where none are) and held for `stream`."""
     if workspace is not None:
-        if workspace.device != device or not workspace.is_contiguous() or workspace.element_size() * workspace.numel() < need:
-            raise ValueError(f"workspace must be contiguous device memory of {need} bytes")
-        return workspace, need
+        if workspace.get_device() != torch.cuda.current_device() or not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous memory of the current device")
+        return workspace, workspace.numel() * workspace.element_size()
+    need = workspace_size(op, m, args)
     if need == 0:
         return None, 0
     workspace = torch.empty(need, dtype=torch.uint8, device=device)
@@ -773,7 +779,7 @@ def kvc_page_tables(*, workspace=None, stream=None, **kw):
     slots, slot_start [rows + 1] where each row's begin.  Returns the workspace (None out of place)."""
     a = page_tables_args(**kw)
     ws, need = _own_ws(OP_PAGE_TABLES, None, a, workspace, kw["lens"].device, stream)
-    _check(lib().kvc_page_tables(C.byref(a), ws.data_ptr() if ws is not None else None, need, _stream(stream)))
+    _check(lib().kvc_page_tables(C.byref(a), ws.data_ptr() if ws is not None else None, need, _raw_stream(stream)))
     return ws
 
 
@@ -797,7 +803,7 @@ def kvc_page_append(m: Model, *, k, v, K, V, slots, stream=None):
         return
     a.k, a.v, a.K, a.V = src(k), src(v), _pool(K, H, d, "K"), _pool(V, H, d, "V")
     a.slots = _flat(slots, "slots", torch.int32, T)
-    _check(lib().kvc_page_append(C.byref(m), C.byref(a), _stream(stream)))
+    _check(lib().kvc_page_append(C.byref(m), C.byref(a), _raw_stream(stream)))
 
 
 def _strides_of(t: torch.Tensor, shape, d: int, name: str):
@@ -868,8 +874,7 @@ def kvc_prefix_decode_attn(m: Model, *, workspace=None, stream=None, **kw):
     workspace; without one given, one is allocated."""
     a = prefix_decode_args(m, **kw)
     ws, need = _own_ws(OP_PREFIX_DECODE, m, a, workspace, kw["q"].device, stream)
-    _check(lib().kvc_prefix_decode_attn(C.byref(m), C.byref(a), ws.data_ptr(), ws.element_size() * ws.numel(),
-                                        _stream(stream)))
+    _check(lib().kvc_prefix_decode_attn(C.byref(m), C.byref(a), ws.data_ptr(), need, _raw_stream(stream)))
     return ws
 
 
@@ -890,7 +895,7 @@ def kvc_sample(*, logits, u, token, temperature=None, top_k=None, top_p=None, mi
     a.top_k, a.top_p = _flat(top_k, "top_k", i32, n), _flat(top_p, "top_p", f32, n)
     a.min_p, a.token = _flat(min_p, "min_p", f32, n), _flat(token, "token", i32, n)
     a.logprob, a.kept = _flat(logprob, "logprob", f32, n), _flat(kept, "kept", i32, n)
-    _check(lib().kvc_sample(C.byref(a), _stream(stream)))
+    _check(lib().kvc_sample(C.byref(a), _raw_stream(stream)))
 
 
 def kvc_check_status(stream=None) -> int:

@@ -287,20 +287,27 @@ static int po_box(const PrefixParams& p) {
   return p.table && page < PO_KEYS ? page : PO_KEYS;
 }
 
+// Byte strides of the 5-D map below; a dimension of extent 1 gets its inner neighbour's.
+static bool po_strides(int64_t (&s)[4], int64_t sb, int64_t sl, int64_t sh, int64_t st, const PrefixParams& p) {
+  const bool paged = p.table != nullptr;
+  const int64_t dims[5] = {p.d, paged ? 1 << p.shift : p.max_len, p.Hkv, paged ? p.n_pages : p.L, paged ? 1 : p.B};
+  const int64_t in[4] = {st, sh, paged ? sb : sl, sb};
+  for (int i = 0; i < 4; ++i) {
+    s[i] = dims[i + 1] > 1 ? in[i] : i ? s[i - 1] : p.d * 2;
+    if (s[i] <= 0 || s[i] % 16 || s[i] >= (1LL << 40)) return false;
+  }
+  return true;
+}
+
 // 5-D map: (dim, token, KV head, layer, sequence), or (dim, token of the page, KV head, page, 1).
 static bool po_map(CUtensorMap* m, const char* base, int64_t sb, int64_t sl, int64_t sh, int64_t st,
                    const PrefixParams& p) {
   auto enc = po_encode();
-  if (!enc) return false;
+  int64_t s[4];
+  if (!enc || !po_strides(s, sb, sl, sh, st, p)) return false;
   const bool paged = p.table != nullptr;
   cuuint64_t dims[5] = {(cuuint64_t)p.d, (cuuint64_t)(paged ? 1 << p.shift : p.max_len), (cuuint64_t)p.Hkv,
                         (cuuint64_t)(paged ? p.n_pages : p.L), (cuuint64_t)(paged ? 1 : p.B)};
-  int64_t s[4] = {st, sh, paged ? sb : sl, sb};
-  if (dims[1] == 1) s[0] = p.d * 2;
-  for (int i = 1; i < 4; ++i)
-    if (dims[i + 1] == 1) s[i] = s[i - 1];
-  for (int i = 0; i < 4; ++i)
-    if (s[i] <= 0 || s[i] % 16 || s[i] >= (1LL << 40)) return false;
   cuuint64_t strides[4] = {(cuuint64_t)s[0], (cuuint64_t)s[1], (cuuint64_t)s[2], (cuuint64_t)s[3]};
   cuuint32_t box[5] = {64, (cuuint32_t)po_box(p), 1, 1, 1};
   cuuint32_t el[5] = {1, 1, 1, 1, 1};
@@ -310,9 +317,10 @@ static bool po_map(CUtensorMap* m, const char* base, int64_t sb, int64_t sl, int
 }
 
 bool prefix_own_mma_supported(const PrefixParams& p) {
-  if (!p.qbf16 || !p.kbf16 || (p.d != 64 && p.d != 128) || p.G > 8 || (uintptr_t)p.q % 16) return false;
-  CUtensorMap a, b;
-  return po_map(&a, p.K, p.Ksb, p.Ksl, p.Ksh, p.Kst, p) && po_map(&b, p.V, p.Vsb, p.Vsl, p.Vsh, p.Vst, p);
+  if (!p.qbf16 || !p.kbf16 || (p.d != 64 && p.d != 128) || p.G > 8) return false;
+  if (((uintptr_t)p.q | (uintptr_t)p.K | (uintptr_t)p.V) % 16) return false;
+  int64_t s[4];
+  return po_strides(s, p.Ksb, p.Ksl, p.Ksh, p.Kst, p) && po_strides(s, p.Vsb, p.Vsl, p.Vsh, p.Vst, p);
 }
 
 template <int D>

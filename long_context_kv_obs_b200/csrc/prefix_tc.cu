@@ -536,18 +536,24 @@ static PFN_cuTensorMapEncodeTiled_v12000 px_encode() {
   return fn;
 }
 
-// 4-D map (dim, token, KV head, layer) with 64 x 128-token boxes, 128B swizzle.  A dimension of
-// extent 1 gets the stride its inner neighbour implies (any legal value works).
-static bool px_map(CUtensorMap* m, const char* base, int64_t sl, int64_t sh, int64_t st, const PrefixParams& p) {
-  auto enc = px_encode();
-  if (!enc) return false;
-  cuuint64_t dims[4] = {(cuuint64_t)p.d, (cuuint64_t)p.max_p, (cuuint64_t)p.Hkv, (cuuint64_t)p.L};
-  int64_t s[3] = {st, sh, sl};
-  if (dims[1] == 1) s[0] = p.d * 2;
-  for (int i = 1; i < 3; ++i)
-    if (dims[i + 1] == 1) s[i] = s[i - 1] * (int64_t)dims[i];
+// Byte strides (token, head, layer) of the 4-D map below.  A dimension of extent 1 gets the stride its
+// inner neighbour implies (any legal value works).
+static bool px_strides(int64_t (&s)[3], int64_t sl, int64_t sh, int64_t st, const PrefixParams& p) {
+  const int64_t dims[4] = {p.d, p.max_p, p.Hkv, p.L};
+  s[0] = dims[1] == 1 ? p.d * 2 : st;
+  s[1] = dims[2] == 1 ? s[0] * dims[1] : sh;
+  s[2] = dims[3] == 1 ? s[1] * dims[2] : sl;
   for (int i = 0; i < 3; ++i)
     if (s[i] <= 0 || s[i] % 16 || s[i] >= (1LL << 40)) return false;
+  return true;
+}
+
+// 4-D map (dim, token, KV head, layer) with 64 x 128-token boxes, 128B swizzle.
+static bool px_map(CUtensorMap* m, const char* base, int64_t sl, int64_t sh, int64_t st, const PrefixParams& p) {
+  auto enc = px_encode();
+  int64_t s[3];
+  if (!enc || !px_strides(s, sl, sh, st, p)) return false;
+  cuuint64_t dims[4] = {(cuuint64_t)p.d, (cuuint64_t)p.max_p, (cuuint64_t)p.Hkv, (cuuint64_t)p.L};
   cuuint64_t strides[3] = {(cuuint64_t)s[0], (cuuint64_t)s[1], (cuuint64_t)s[2]};
   cuuint32_t box[4] = {64, PX_KEYS, 1, 1};
   cuuint32_t el[4] = {1, 1, 1, 1};
@@ -559,9 +565,9 @@ static bool px_map(CUtensorMap* m, const char* base, int64_t sl, int64_t sh, int
 // bf16 queries and keys, at most 128 layers, and cache layouts a TMA map can describe.
 bool prefix_tc_supported(const PrefixParams& p) {
   if (!p.qbf16 || !p.kbf16 || (p.d != 64 && p.d != 128) || p.L > PX_MAXL) return false;
-  if ((uintptr_t)p.q % 16) return false;
-  CUtensorMap a, b;
-  return px_map(&a, p.Kp, p.Kpl, p.Kph, p.Kpt, p) && px_map(&b, p.Vp, p.Vpl, p.Vph, p.Vpt, p);
+  if (((uintptr_t)p.q | (uintptr_t)p.Kp | (uintptr_t)p.Vp) % 16) return false;
+  int64_t s[3];
+  return px_strides(s, p.Kpl, p.Kph, p.Kpt, p) && px_strides(s, p.Vpl, p.Vph, p.Vpt, p);
 }
 
 template <int D, int MT, bool HAS_R>
