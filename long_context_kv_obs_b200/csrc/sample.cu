@@ -2,25 +2,31 @@
 //
 // Which tokens stay is decided on the row's order (logit down, index up): each filter keeps a
 // head of it, so the outcome is one cut (key, index), and the token is found where the kept
-// mass, summed in index order, passes u times its total.  No sort: the cut of top-k is the k-th
-// key by counts, that of top-p the key at which the summed mass reaches top_p of the total.
+// mass, summed in index order, passes u times its total.  No sort of the row.
 //
 // Masses.  A vocabulary of 10^5 flat probabilities puts borders 10^-5 apart, so fp32 sums
 // (errors near 10^-7) would move a border once in a hundred rows.  Weights are formed in fp64:
 // 2^t with t = (z - max) log2(e) / T split as t = k / 64 + f, |f| <= 1/128; 2^(k mod 64 / 64) from a
 // table that the CUDA function exp2 fills, 2^f by the Taylor series of exp(f ln 2) to degree 4
-// (relative error below 4e-14), and the exponent added.  Sums run in fp64 in a fixed order.
+// (relative error below 4e-14), and the exponent added.  Weights below 2^-64 of the largest count
+// as nothing: all of them together are below 2^-46 of the mass.  Sums run in a fixed order.
 //
 // A row is a cluster of CTAs, each with a slice of it in shared memory, read from HBM once.
-//   A  the maximum and its first index
-//   B  cut search: counts or masses by bins of 1/16 octave of weight below the maximum (shared-memory
-//      integer atomics: order does not matter), combined over the cluster through distributed
-//      shared memory; the bin that holds the border is searched again by ranges of the key, until
-//      one key is left; of its ties the lowest indices stay.  In the first search of top-p the bins
-//      hold masses to 16 bits only: the exact fp64 sums of pass C decide whether the bin is the
-//      right one (else its neighbour is taken), the later searches count in 2^-40 units.
-//   C  fp64 sums of the kept weights by 32-vector stretches of a warp, in index order
-//   D  the stretch, lane and element where u * total falls
+//   A  the maximum
+//   B  top-k, few: the k-th largest of the threads' own maxima is a bound that k elements reach; what
+//      reaches it goes to one CTA, which sorts it, sums it in that order for top-p, and again in
+//      index order for the token
+//   C  else the cut is searched: counts (top-k) or masses (top-p) by bins of 1/16 octave of weight below
+//      the maximum (shared-memory integer atomics: order does not matter), summed over the
+//      cluster through distributed shared memory; the bin that holds the border is searched
+//      again by ranges of the key, until one key is left; of its ties the lowest indices stay.
+//      Tokens whose weight is below (1 - top_p) of the mean are left out of the first search of
+//      masses: together they hold less than the 1 - top_p that is cut.  Its bins hold masses to 16
+//      bits only: the exact sums of D decide whether the bin is the right one (else its neighbour is
+//      taken), the later searches count in 2^-33 units of the bin's weights, or exactly once a
+//      bin is one key.
+//   D  fp64 sums of the kept weights by 32-vector stretches of a warp, in index order
+//   E  the stretch, lane and element where u * total falls
 #include <cooperative_groups.h>
 
 #include <climits>
@@ -33,28 +39,50 @@ namespace cg = cooperative_groups;
 constexpr int SP_THREADS = 512;
 constexpr int SP_WARPS = SP_THREADS / 32;
 constexpr int SP_BINS = 2048;
-constexpr int SP_MAXC = 8;
+constexpr int SP_MAXC = 16;
+constexpr int SP_LIST = 4096;                   // candidates that one CTA sorts
+constexpr float SP_ONE = 8388608.f;             // 2^23: adding it leaves the rounded integer in a float's low bits
 
 struct alignas(16) SpShared {                   // the slice follows: its vectors are 16-byte aligned
-  unsigned long long hist[SP_BINS];             // u32 counts / 16-bit masses, or u64 in 2^-40 units
-  double comb[SP_BINS];                         // this CTA's share of the bins, combined over the cluster
+  union {
+    unsigned hist[2][2 * SP_BINS];              // two searches deep: counts or masses; two 17-bit limbs of a mass
+    unsigned long long list[SP_LIST];
+  };
   double table[64];                             // 2^(j / 64)
-  unsigned long long xch[2][4];                 // values exchanged over the cluster, two steps deep
+  unsigned long long xch[2][SP_MAXC][4];        // values of every CTA of the cluster, two steps deep
   unsigned long long red[SP_WARPS][4];
-  double found[2];
+  double found[4];
   int ifound[2];
+  int cand[SP_WARPS][2];
+  int nlist;
 };
 
 template <typename T> struct SpVec;
 template <> struct SpVec<__nv_bfloat16> {
   static constexpr int N = 8, KSHIFT = 16;      // keys differ in their upper 16 bits only
+  // NaN to -infinity and -0 to +0
+  __device__ __forceinline__ static uint4 clean(uint4 u) {
+    uint32_t* w = &u.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      __nv_bfloat162 x = *reinterpret_cast<__nv_bfloat162*>(w + i);
+      x = __hadd2(__hmax2(x, __float2bfloat162_rn(-INFINITY)), __float2bfloat162_rn(0.f));
+      w[i] = *reinterpret_cast<uint32_t*>(&x);
+    }
+    return u;
+  }
 };
 template <> struct SpVec<float> {
   static constexpr int N = 4, KSHIFT = 0;
+  __device__ __forceinline__ static uint4 clean(uint4 u) {
+    uint32_t* w = &u.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(fmaxf(__uint_as_float(w[i]), -INFINITY) + 0.f);
+    return u;
+  }
 };
 
-__device__ __forceinline__ uint32_t sp_key(float z, int shift) { return f2key(z + 0.f) >> shift; }   // -0 counts as +0
-
+__device__ __forceinline__ uint32_t sp_key(float z, int shift) { return f2key(z) >> shift; }
 template <int KSHIFT>
 __device__ __forceinline__ float sp_value(uint32_t key) {
   // the dropped low bits of a negative value's key are ones
@@ -80,37 +108,38 @@ struct SpRow {
   static constexpr int N = SpVec<T>::N, KS = SpVec<T>::KSHIFT;
   cg::cluster_group cl;
   SpShared& sh;
-  const uint4* slice;                           // this CTA's vectors
+  uint4* slice;                                 // this CTA's vectors; thread t owns t, t + SP_THREADS, ...
   double* wsum;                                 // kept mass of every 32-vector stretch
   int C, rank, nvec, i0;                        // cluster size, rank, vectors of the slice, its first index
-  int step;
-  float zmax, ybin;                             // bin = (zmax - z) * ybin
+  int step, search;
+  float zmax, ybin;                             // bins below the maximum: (zmax - z) * ybin
   double c;                                     // log2(e) / T
-  // tokens left by top-k: key > ck, or key == ck and index <= ci
+  bool cut;                                     // top-k left: key > ck, or key == ck and index <= ci
   uint32_t ck;
   int ci;
-  double zcut;                                  // min-p: z >= zcut
 
   __device__ __forceinline__ SpRow(SpShared& s) : cl(cg::this_cluster()), sh(s) {}
 
-  // value of every CTA's thread 0; slots are reused two steps later, with a barrier between
+  // The values v of every CTA, which all its threads know: each CTA writes its own into every other's
+  // shared memory (a store does not wait), and after the cluster barrier the reads are local.  A slot
+  // is written again two steps later: by then its reader has passed the barrier between.
   template <int K, typename F>
   __device__ __forceinline__ void exchange(const unsigned long long (&v)[K], F&& use) {
-    if (threadIdx.x == 0) {
+    if ((int)threadIdx.x < C) {
+      unsigned long long* o = cl.map_shared_rank(&sh.xch[step & 1][rank][0], threadIdx.x);
 #pragma unroll
-      for (int k = 0; k < K; ++k) sh.xch[step & 1][k] = v[k];
+      for (int k = 0; k < K; ++k) o[k] = v[k];
     }
     cl.sync();
     for (int r = 0; r < C; ++r) {
-      const unsigned long long* o = cl.map_shared_rank(&sh.xch[step & 1][0], r);
       unsigned long long w[K];
 #pragma unroll
-      for (int k = 0; k < K; ++k) w[k] = o[k];
+      for (int k = 0; k < K; ++k) w[k] = sh.xch[step & 1][r][k];
       use(r, w);
     }
     ++step;
   }
-  // sum over the CTA, in a fixed order, known to every thread
+  // Sums over the CTA, in a fixed order, known to every thread.
   template <int K, typename V>
   __device__ __forceinline__ void block_sum(V (&v)[K]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -128,26 +157,22 @@ struct SpRow {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       V s = V(0);
+#pragma unroll
       for (int w = 0; w < SP_WARPS; ++w) s += *reinterpret_cast<V*>(&sh.red[w][k]);
       v[k] = s;
     }
   }
 
-  __device__ __forceinline__ void unpack(int v, float (&z)[N]) const {
-    Vec<T>::unpack(slice[v], z);
-#pragma unroll
-    for (int j = 0; j < N; ++j) z[j] = fmaxf(z[j], -INFINITY);   // NaN counts as -infinity
-  }
-  // distance below the maximum in bins, monotone in z; infinite maxima and steps: only the maximum is at 0
-  __device__ __forceinline__ float dist(float z) const { return z == zmax ? 0.f : (zmax - z) * ybin; }
+  __device__ __forceinline__ void unpack(int v, float (&z)[N]) const { Vec<T>::unpack(slice[v], z); }
+  // Monotone in z; the maximum is in bin 0, the last bin holds all that is farther.
   __device__ __forceinline__ int bin(float z) const {
-    const float y = dist(z);
-    return y < (float)(SP_BINS - 1) ? (int)y : SP_BINS - 1;      // NaN: the last
+    const float r = fmaf(zmax - z, ybin, SP_ONE);
+    return min(__float_as_int(r) - 0x4B000000, SP_BINS - 1);
   }
   __device__ __forceinline__ double weight(float z) const {
-    const double d = (double)z - (double)zmax;
-    double t = z == zmax ? 0.0 : d * c;
-    if (!(t > -1020.0)) return 0.0;             // below any sum's last bit; infinite distances too
+    double t = ((double)z - (double)zmax) * c;
+    const bool none = !(t > -64.0);             // -infinity at an infinite temperature (NaN) too
+    t = none ? -64.0 : t;
     const double magic = 6755399441055744.0 / 64;   // 1.5 * 2^52 / 64: rounds t to a multiple of 1/64
     const double r = t + magic;
     const int k = __double2loint(r);
@@ -158,214 +183,272 @@ struct SpRow {
     p = fma(f, p, 6.931471805599453e-1);
     p = fma(f, p, 1.0);
     p *= sh.table[k & 63];
-    return __hiloint2double(__double2hiint(p) + ((k >> 6) << 20), __double2loint(p));
+    return none ? 0.0 : __hiloint2double(__double2hiint(p) + ((k >> 6) << 20), __double2loint(p));
   }
-  __device__ __forceinline__ bool left(uint32_t key, int idx) const { return key > ck || (key == ck && idx <= ci); }
+  __device__ __forceinline__ bool left(float z, int idx) const {
+    if (!cut) return z > -INFINITY;
+    const uint32_t key = sp_key(z, KS);
+    return key > ck || (key == ck && idx <= ci);
+  }
+  // A lower and an upper bound on the values of bin b, outside by a thousandth of a bin (the
+  // roundings of bin() are below 2^-11 of one) and a step of z.
+  __device__ __forceinline__ float edge_low(int b) const {
+    if (b >= SP_BINS - 1 || !(ybin > 0.f)) return -INFINITY;
+    const float x = zmax - ((float)b + 0.501f) / ybin;
+    return x > -3.4028234663852886e38f ? key2f(f2key(x) - 1u) : -INFINITY;
+  }
+  __device__ __forceinline__ float edge_high(int b) const {
+    if (b == 0 || !(ybin > 0.f)) return zmax;
+    return fminf(zmax, key2f(f2key(zmax - ((float)b - 0.501f) / ybin) + 1u));
+  }
 
-  // The first bin at which the sum of comb reaches `target`, over the cluster's shares; `above`
-  // receives the sum before it.  The shares were written before a cluster barrier.
-  __device__ __forceinline__ void border(double share, double frac, double target, int& b, double& above) {
-    const int per = SP_BINS / C;
-    double tot[SP_MAXC], all = 0.0;
-    unsigned long long x[1] = {(unsigned long long)__double_as_longlong(share)};
-    exchange<1>(x, [&](int r, unsigned long long (&w)[1]) {
-      tot[r & (SP_MAXC - 1)] = __longlong_as_double((long long)w[0]);
-      all += tot[r & (SP_MAXC - 1)];
-    });
-    if (frac > 0.0) target = frac * all;
-    if (threadIdx.x < 32) {
-      const int lane = threadIdx.x;
-      double before = 0.0;
-      int r = 0, end = 0;                       // shares that hold something: the one that reaches target, else the last
-      for (int x = 0; x < C; ++x)
-        if (tot[x] > 0.0) end = x;
-      while (r < end && (!(tot[r] > 0.0) || before + tot[r] < target)) before += tot[r++];
-      // the share's bins, per / 32 a lane
-      const double* o = cl.map_shared_rank(&sh.comb[0], r);
-      const int q = per / 32;
-      double s = 0.0;
-      for (int j = 0; j < q; ++j) s += o[lane * q + j];
-      double inc = s;
+  // The histogram of this search, cleared for use (its words are used again two searches on).
+  __device__ __forceinline__ unsigned* clear_hist(int words) {
+    unsigned* h = sh.hist[search & 1];
+    for (int j = threadIdx.x; j < words / 4; j += SP_THREADS) reinterpret_cast<uint4*>(h)[j] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    return h;
+  }
+  // The first bin at which the sum over the cluster's histograms reaches `target`, or the last that
+  // holds something; the sum before it and the bin's own value.  A bin's value is val(bin, words
+  // summed over the cluster); LIMBS: the histogram has a second half, 2^17 times the first's unit.
+  // Every CTA reads all histograms (a thread four bins, all its loads in flight) and scans them for
+  // itself: one cluster barrier a search.  The next search uses the other buffer, so a slow reader is
+  // not overtaken.
+  template <bool LIMBS, typename F>
+  __device__ __forceinline__ void border(double target, F&& val, int& b, double& above, double& value) {
+    static_assert(SP_BINS == 4 * SP_THREADS, "four bins a thread");
+    cl.sync();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    unsigned long long h[4] = {0, 0, 0, 0};
+#pragma unroll 8
+    for (int r = 0; r < C; ++r) {
+      const uint4* o = reinterpret_cast<const uint4*>(cl.map_shared_rank(&sh.hist[search & 1][0], r));
+      const uint4 x = o[threadIdx.x];
+      h[0] += x.x; h[1] += x.y; h[2] += x.z; h[3] += x.w;
+      if (LIMBS) {
+        const uint4 y = o[SP_BINS / 4 + threadIdx.x];
+        h[0] += (unsigned long long)y.x << 17; h[1] += (unsigned long long)y.y << 17;
+        h[2] += (unsigned long long)y.z << 17; h[3] += (unsigned long long)y.w << 17;
+      }
+    }
+    ++search;
+    double v[4], sum = 0.0;
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const double y = __shfl_up_sync(FULL, inc, d);
-        if (lane >= d) inc += y;
-      }
-      const unsigned hit = __ballot_sync(FULL, before + inc >= target && s > 0.0);
-      const unsigned any = __ballot_sync(FULL, s > 0.0);
-      const int at = hit ? __ffs(hit) - 1 : any ? 31 - __clz(any) : 31;   // none by rounding: the last that holds something
-      if (lane == at) {
-        double run = before + inc - s;
-        int j = 0, last = 0;
-        double last_run = run;
-        for (; j < q; ++j) {
-          const double w = o[lane * q + j];
-          if (w > 0.0) {
-            last = j;
-            last_run = run;
-            if (run + w >= target) break;
-          }
-          run += w;
+    for (int j = 0; j < 4; ++j) {
+      v[j] = h[j] ? val(4 * (int)threadIdx.x + j, (double)h[j]) : 0.0;
+      sum += v[j];
+    }
+    double inc = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const double y = __shfl_up_sync(FULL, inc, d);
+      if (lane >= d) inc += y;
+    }
+    if (lane == 31) *reinterpret_cast<double*>(&sh.red[warp][0]) = inc;
+    __syncthreads();
+    double before = 0.0;
+    for (int w = 0; w < warp; ++w) before += *reinterpret_cast<double*>(&sh.red[w][0]);
+    const unsigned some = __ballot_sync(FULL, sum > 0.0);
+    const unsigned hit = __ballot_sync(FULL, sum > 0.0 && before + inc >= target);
+    if (lane == 0) {
+      sh.cand[warp][0] = hit ? warp * 32 + __ffs(hit) - 1 : INT_MAX;
+      sh.cand[warp][1] = some ? warp * 32 + 31 - __clz(some) : -1;
+    }
+    __syncthreads();
+    int at = INT_MAX, end = -1;
+#pragma unroll
+    for (int w = 0; w < SP_WARPS; ++w) {
+      at = min(at, sh.cand[w][0]);
+      end = max(end, sh.cand[w][1]);
+    }
+    if (at == INT_MAX) at = max(end, 0);
+    if ((int)threadIdx.x == at) {
+      double run = before + inc - sum, last_run = run, last_v = 0.0;
+      int last = 0;
+      bool done = false;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (!done && v[j] > 0.0) {
+          last = j;
+          last_run = run;
+          last_v = v[j];
+          done = run + v[j] >= target;
         }
-        sh.ifound[0] = r * per + lane * q + last;
-        sh.found[0] = last_run;
+        run += v[j];
       }
+      sh.ifound[0] = 4 * at + last;
+      sh.found[0] = last_run;
+      sh.found[1] = last_v;
     }
     __syncthreads();
     b = sh.ifound[0];
     above = sh.found[0];
-    __syncthreads();
-  }
-  // Every CTA's histogram summed into shares of the bins; returns this CTA's share's sum.
-  // kind 0: counts, 1: 16-bit masses relative to the bin's upper edge, 2: u64.
-  __device__ __forceinline__ double combine(int kind) {
-    cl.sync();
-    const int per = SP_BINS / C;
-    double s[1] = {0.0};
-    for (int j = threadIdx.x; j < per; j += SP_THREADS) {
-      const int b = rank * per + j;
-      unsigned long long h = 0;
-      for (int r = 0; r < C; ++r) {
-        if (kind == 2) h += cl.map_shared_rank(&sh.hist[0], r)[b];
-        else h += reinterpret_cast<unsigned*>(cl.map_shared_rank(&sh.hist[0], r))[b];
-      }
-      double v = (double)h;
-      if (kind == 1) v *= (double)exp2f(-(float)b * (1.f / 16.f));
-      sh.comb[j] = v;
-      s[0] += v;
-    }
-    block_sum<1>(s);
-    return s[0];
-  }
-  __device__ __forceinline__ void clear_hist(int words) {
-    for (int j = threadIdx.x; j < words; j += SP_THREADS) sh.hist[j] = 0ull;
+    value = sh.found[1];
     __syncthreads();
   }
 
-  // Within bin b0 (of the tokens left by top-k when in_left), the key at which the count (MASS:
-  // the mass, in units of 2^-(40 + e)) reaches `need`, and the index of the last tie that stays.
-  template <bool MASS>
-  __device__ __forceinline__ void refine(int b0, double need, int e, bool in_left, uint32_t& tkey, int& tidx) {
-    // keys the bin can hold: its edges, a thousandth of a bin wider for the roundings of bin()
-    uint32_t hi, lo;
-    {
-      const float w = ybin > 0.f ? 1.f / ybin : INFINITY;
-      const float zh = b0 == 0 ? zmax : zmax - ((float)b0 - 0.001f) * w;
-      const float zl = b0 == SP_BINS - 1 ? -INFINITY : zmax - ((float)b0 + 1.001f) * w;
-      hi = min(sp_key(zh, KS) + 1u, sp_key(zmax, KS));
-      lo = zl > -INFINITY ? sp_key(zl, KS) : 0u;
-      lo = lo > 0u ? lo - 1u : 0u;
-      lo = max(lo, sp_key(-INFINITY, KS) + 1u);
-      if (!(zh > -INFINITY)) hi = sp_key(zmax, KS);
+  // use(value, index) for every element of the slice with lo <= value <= hi; they are few
+  template <typename F>
+  __device__ __forceinline__ void in_range(float lo, float hi, F&& use) {
+    for (int v = threadIdx.x; v < nvec; v += SP_THREADS) {
+      float z[N];
+      unpack(v, z);
+      unsigned in = 0;
+#pragma unroll
+      for (int j = 0; j < N; ++j) in |= (z[j] >= lo && z[j] <= hi ? 1u : 0u) << j;
+      while (in) {
+        const int j = __ffs(in) - 1;
+        in &= in - 1;
+        use((float)reinterpret_cast<const T*>(slice + v)[j], i0 + v * N + j);
+      }
     }
-    double above = 0.0;
+  }
+
+  // Within bin b0 (of the tokens left by top-k), the key at which the count (MASS: the mass, in units
+  // of 2^-(33 + e)) reaches `need`, and the index of the last tie that stays.
+  template <bool MASS>
+  __device__ __forceinline__ void refine(int b0, double need, int e, uint32_t& tkey, int& tidx) {
+    uint32_t hi = sp_key(edge_high(b0), KS), lo = max(sp_key(edge_low(b0), KS), sp_key(-INFINITY, KS) + 1u);
+    double above = 0.0, value = 0.0;
     int shift = 0;
     while (((hi - lo) >> shift) >= SP_BINS) ++shift;
     while (true) {
-      clear_hist(MASS ? SP_BINS : SP_BINS / 2);
-      for (int v = threadIdx.x; v < nvec; v += SP_THREADS) {
-        float z[N];
-        unpack(v, z);
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-          const uint32_t key = sp_key(z[j], KS);
-          if (key < lo || key > hi || bin(z[j]) != b0) continue;
-          if (in_left && !left(key, i0 + v * N + j)) continue;
-          const uint32_t hb = (hi - key) >> shift;
-          if (MASS) {
-            const unsigned long long q = (unsigned long long)__double2ll_rn(scalbn(weight(z[j]), 40 + e));
-            atomicAdd(&sh.hist[hb], q);
-          } else {
-            atomicAdd(reinterpret_cast<unsigned*>(sh.hist) + hb, 1u);
-          }
+      const bool limbs = MASS && shift > 0;
+      unsigned* hist = clear_hist(limbs ? 2 * SP_BINS : SP_BINS);
+      in_range(sp_value<KS>(lo), sp_value<KS>(hi), [&](float z, int idx) {
+        if (bin(z) != b0 || !left(z, idx)) return;
+        const uint32_t hb = (hi - sp_key(z, KS)) >> shift;
+        if (limbs) {
+          const unsigned long long q = (unsigned long long)__double2ll_rn(scalbn(weight(z), 33 + e));
+          atomicAdd(hist + hb, (unsigned)(q & 0x1ffffu));
+          atomicAdd(hist + SP_BINS + hb, (unsigned)(q >> 17));
+        } else {
+          atomicAdd(hist + hb, 1u);
         }
-      }
-      __syncthreads();
-      const double share = combine(MASS ? 2 : 0);
+      });
       int hb;
       double ab;
-      border(share, 0.0, need - above, hb, ab);
+      if (limbs) {
+        border<true>(need - above, [](int, double n) { return n; }, hb, ab, value);
+      } else if (MASS) {                        // a bin is one key: its weight times its count
+        const uint32_t first = hi;
+        border<false>(need - above,
+                      [&](int i, double n) { return n * scalbn(weight(sp_value<KS>(first - (uint32_t)i)), 33 + e); }, hb, ab,
+                      value);
+      } else {
+        border<false>(need - above, [](int, double n) { return n; }, hb, ab, value);
+      }
       above += ab;
       const uint32_t top = hi - ((uint32_t)hb << shift);
       const uint32_t span = (1u << shift) - 1u;
       lo = top - lo > span ? top - span : lo;
       hi = top;
       if (shift == 0) break;
-      shift = shift > 11 ? shift - 11 : 0;
-      if (((hi - lo) >> shift) >= SP_BINS) ++shift;
+      shift = 0;
+      while (((hi - lo) >> shift) >= SP_BINS) ++shift;
     }
     tkey = hi;
-    // of the ties of tkey the first `take` in index order stay
-    double take = need - above;
+    // of the ties of tkey the first `take` in index order stay; `value` tells how many there are
+    double take = need - above, ties = value;
     if (MASS) {
-      const double w = rint(scalbn(weight(sp_value<KS>(tkey)), 40 + e));
+      const double w = scalbn(weight(sp_value<KS>(tkey)), 33 + e);
       take = w > 0.0 ? ceil(take / w) : 1.0;
+      ties = w > 0.0 ? rint(value / w) : 1.0;
     }
     if (take < 1.0) take = 1.0;
+    tidx = INT_MAX;
+    if (take >= ties) return;
+    // ties of every 32-vector stretch, in the histogram words of the next search
+    const int lane = threadIdx.x & 31, nst = (nvec + 31) / 32;
+    const float zt = sp_value<KS>(tkey);
+    unsigned* count = sh.hist[search & 1];
     int mine[1] = {0};
-    for (int v = threadIdx.x; v < nvec; v += SP_THREADS) {
-      float z[N];
-      unpack(v, z);
+    for (int v0 = threadIdx.x - lane; v0 < nvec; v0 += SP_THREADS) {
+      const int v = v0 + lane;
+      int n = 0;
+      if (v < nvec) {
+        float z[N];
+        unpack(v, z);
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const uint32_t key = sp_key(z[j], KS);
-        mine[0] += key == tkey && (!in_left || left(key, i0 + v * N + j));
+        for (int j = 0; j < N; ++j) n += z[j] == zt && left(z[j], i0 + v * N + j);
+      }
+      n = __reduce_add_sync(FULL, n);
+      if (lane == 0) {
+        count[v0 >> 5] = (unsigned)n;
+        mine[0] += n;
       }
     }
     block_sum<1>(mine);
-    double before = 0.0, total = 0.0;
-    unsigned long long x[1] = {(unsigned long long)mine[0]};
-    exchange<1>(x, [&](int r, unsigned long long (&w)[1]) {
-      if (r < rank) before += (double)w[0];
-      total += (double)w[0];
-    });
-    tidx = INT_MAX;
-    if (take < total) {
-      // this slice holds the last tie that stays: walk its stretches in order
-      if (before < take && take <= before + (double)mine[0] && threadIdx.x < 32) {
-        int want = (int)(take - before);        // the want-th tie of the slice
-        for (int s0 = 0; s0 < nvec; s0 += 32) {
-          const int v = s0 + threadIdx.x;
-          int n = 0;
-          float z[N];
-          if (v < nvec) {
-            unpack(v, z);
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-              const uint32_t key = sp_key(z[j], KS);
-              n += key == tkey && (!in_left || left(key, i0 + v * N + j));
-            }
-          }
-          int inc = n;
-#pragma unroll
-          for (int d = 1; d < 32; d <<= 1) {
-            const int y = __shfl_up_sync(FULL, inc, d);
-            if ((int)threadIdx.x >= d) inc += y;
-          }
-          const int all = __shfl_sync(FULL, inc, 31);
-          if (all >= want) {
-            const unsigned hit = __ballot_sync(FULL, inc >= want);
-            if ((int)threadIdx.x == __ffs(hit) - 1) {
-              int k = inc - n;
-#pragma unroll
-              for (int j = 0; j < N; ++j) {
-                const uint32_t key = sp_key(z[j], KS);
-                if (key == tkey && (!in_left || left(key, i0 + v * N + j)) && ++k == want) sh.ifound[1] = i0 + v * N + j;
-              }
-            }
-            break;
-          }
-          want -= all;
-        }
-      }
-      __syncthreads();
-      unsigned long long y[1] = {(unsigned long long)(before < take && take <= before + (double)mine[0] ? sh.ifound[1] + 1 : 0)};
-      int at = 0;
-      exchange<1>(y, [&](int, unsigned long long (&w)[1]) { at = max(at, (int)w[0]); });
-      tidx = at - 1;
+    double before = 0.0;
+    {
+      unsigned long long x[1] = {(unsigned long long)mine[0]};
+      exchange<1>(x, [&](int r, unsigned long long (&w)[1]) { before += r < rank ? (double)w[0] : 0.0; });
     }
+    const bool here = before < take && take <= before + (double)mine[0];
+    if (here && threadIdx.x < 32) {             // this slice holds the last tie that stays
+      int want = (int)(take - before), st = 0;
+      for (int s0 = 0; s0 < nst; s0 += 32) {
+        const int n = s0 + lane < nst ? (int)count[s0 + lane] : 0;
+        int inc = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int y = __shfl_up_sync(FULL, inc, d);
+          if (lane >= d) inc += y;
+        }
+        const unsigned hit = __ballot_sync(FULL, inc >= want);
+        if (hit) {
+          st = s0 + __ffs(hit) - 1;
+          want -= __shfl_sync(FULL, inc - n, __ffs(hit) - 1);
+          break;
+        }
+        want -= __shfl_sync(FULL, inc, 31);
+      }
+      const int v = st * 32 + lane;
+      unsigned in = 0;
+      if (v < nvec) {
+        float z[N];
+        unpack(v, z);
+#pragma unroll
+        for (int j = 0; j < N; ++j) in |= (z[j] == zt && left(z[j], i0 + v * N + j) ? 1u : 0u) << j;
+      }
+      int inc = __popc(in);
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(FULL, inc, d);
+        if (lane >= d) inc += y;
+      }
+      int k = inc - __popc(in);
+      while (in) {
+        const int j = __ffs(in) - 1;
+        in &= in - 1;
+        if (++k == want) sh.ifound[1] = i0 + v * N + j;
+      }
+    }
+    __syncthreads();
+    unsigned long long y[1] = {(unsigned long long)(here ? sh.ifound[1] + 1 : 0)};
+    int at = 0;
+    exchange<1>(y, [&](int, unsigned long long (&w)[1]) { at = max(at, (int)w[0]); });
+    tidx = at - 1;
   }
 };
+
+// a[0, n) sorted downwards, n a power of two (bitonic merges).
+__device__ __forceinline__ void sp_sort(unsigned long long* a, int n) {
+  for (int k = 2; k <= n; k <<= 1)
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      __syncthreads();
+      for (int p = threadIdx.x; p < n / 2; p += SP_THREADS) {
+        const int i = 2 * p - (p & (j - 1)), q = i + j;
+        const unsigned long long x = a[i], y = a[q];
+        if ((x < y) == ((i & k) == 0)) {
+          a[i] = y;
+          a[q] = x;
+        }
+      }
+    }
+  __syncthreads();
+}
 
 template <typename T, bool ALIGNED>
 __global__ void __launch_bounds__(SP_THREADS) sample_kernel(SampleParams p, int per_cta) {
@@ -375,125 +458,315 @@ __global__ void __launch_bounds__(SP_THREADS) sample_kernel(SampleParams p, int 
   SpShared& sh = *reinterpret_cast<SpShared*>(sp_raw);
   uint4* slice = reinterpret_cast<uint4*>(sp_raw + sizeof(SpShared));
   SpRow<T> s(sh);
+  s.cl.barrier_arrive();                        // every CTA of the cluster runs before its shared memory is written
   s.C = (int)s.cl.num_blocks();
   s.rank = (int)s.cl.block_rank();
-  const int row = blockIdx.x / s.C, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row = blockIdx.x / s.C, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   s.slice = slice;
   s.wsum = reinterpret_cast<double*>(slice + per_cta / N);
   s.i0 = s.rank * per_cta;
   s.nvec = max(0, min(per_cta, p.V - s.i0) + N - 1) / N;
-  s.step = 0;
+  s.step = s.search = 0;
+  s.cut = false;
   const T* z0 = reinterpret_cast<const T*>(p.logits) + row * p.row_stride;
 
-  // A: the slice into shared memory, the maximum and its first index
+  // A: the slice into shared memory and the maximum
   float best = -INFINITY;
-  int at = INT_MAX;
 #pragma unroll 4
-  for (int v = threadIdx.x; v < s.nvec; v += SP_THREADS) {
-    const uint4 u = sp_load<T, ALIGNED>(z0, s.i0 + (int64_t)v * N, p.V);
+  for (int v = tid; v < s.nvec; v += SP_THREADS) {
+    const uint4 u = SpVec<T>::clean(sp_load<T, ALIGNED>(z0, s.i0 + (int64_t)v * N, p.V));
     slice[v] = u;
     float z[N];
     Vec<T>::unpack(u, z);
 #pragma unroll
-    for (int j = 0; j < N; ++j)
-      if (z[j] > best) {
-        best = z[j];
-        at = s.i0 + v * N + j;
-      }
+    for (int j = 0; j < N; ++j) best = fmaxf(best, z[j]);
   }
-  if (threadIdx.x < 64) sh.table[threadIdx.x] = exp2((double)threadIdx.x / 64.0);
-  unsigned long long bk = at == INT_MAX ? 0ull : ((unsigned long long)f2key(best + 0.f) << 32) | (unsigned)~at;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) bk = max(bk, __shfl_xor_sync(FULL, bk, o));
-  if (lane == 0) sh.red[warp][0] = bk;
-  __syncthreads();
-  for (int w = 0; w < SP_WARPS; ++w) bk = max(bk, sh.red[w][0]);
-  {
-    unsigned long long x[1] = {bk};
-    s.exchange(x, [&](int, unsigned long long (&w)[1]) { bk = max(bk, w[0]); });
-  }
-  const bool leader = s.rank == 0 && threadIdx.x == 0;
+  if (tid < 64) sh.table[tid] = exp2((double)tid / 64.0);
   const float T_ = p.temperature ? p.temperature[row] : 1.f;
-  if (bk == 0ull || !(T_ > 0.f)) {
-    if (leader) {
-      p.token[row] = bk == 0ull ? -1 : (int)~(unsigned)bk;
-      if (p.logprob) p.logprob[row] = bk == 0ull ? -INFINITY : 0.f;
-      if (p.kept) p.kept[row] = bk != 0ull;
+  const int k = p.top_k ? p.top_k[row] : 0;
+  const float pf = p.top_p ? p.top_p[row] : 1.f, mf = p.min_p ? p.min_p[row] : 0.f;
+  {
+    const float m = warp_max(best);
+    if (lane == 0) sh.red[warp][0] = f2key(m);
+    __syncthreads();
+    unsigned long long x[1] = {0};
+#pragma unroll
+    for (int w = 0; w < SP_WARPS; ++w) x[0] = max(x[0], sh.red[w][0]);
+    s.cl.barrier_wait();
+    unsigned long long top = 0;
+    s.exchange(x, [&](int, unsigned long long (&w)[1]) { top = max(top, w[0]); });
+    s.zmax = key2f((uint32_t)top);
+  }
+  if (s.zmax == -INFINITY || !(T_ > 0.f)) {
+    // nothing to take, or the first token of the order
+    int at = INT_MAX;
+    if (s.zmax > -INFINITY)
+      s.in_range(s.zmax, s.zmax, [&](float, int idx) { at = min(at, idx); });
+    at = __reduce_min_sync(FULL, at);
+    __syncthreads();
+    if (lane == 0) sh.red[warp][0] = (unsigned long long)at;
+    __syncthreads();
+    unsigned long long x[1] = {INT_MAX};
+#pragma unroll
+    for (int w = 0; w < SP_WARPS; ++w) x[0] = min(x[0], sh.red[w][0]);
+    unsigned long long first = INT_MAX;
+    s.exchange(x, [&](int, unsigned long long (&w)[1]) { first = min(first, w[0]); });
+    if (s.rank == 0 && tid == 0) {
+      const bool any = s.zmax > -INFINITY;
+      p.token[row] = any ? (int)first : -1;
+      if (p.logprob) p.logprob[row] = any ? 0.f : -INFINITY;
+      if (p.kept) p.kept[row] = any;
     }
-    s.cl.sync();                                // no CTA leaves while another reads its shared memory
     return;
   }
-  s.zmax = key2f((uint32_t)(bk >> 32));
+  if (s.zmax == INFINITY) {
+    // infinite logits share the mass: they become 0, all others -infinity
+    for (int v = tid; v < s.nvec; v += SP_THREADS) {
+      T* e = reinterpret_cast<T*>(slice + v);
+#pragma unroll
+      for (int j = 0; j < N; ++j) e[j] = (float)e[j] == INFINITY ? T(0.f) : T(-INFINITY);
+    }
+    best = best == INFINITY ? 0.f : -INFINITY;
+    s.zmax = 0.f;
+  }
   s.c = 1.4426950408889634 / (double)T_;
-  s.ybin = (float)(16.0 * s.c);
-  s.ck = sp_key(-INFINITY, KS);                 // everything above -infinity
-  s.ci = -1;
-  const int k = p.top_k ? p.top_k[row] : 0;
-  const double top_p = p.top_p ? (double)p.top_p[row] : 1.0;
-  double min_p = p.min_p ? (double)p.min_p[row] : 0.0;
-  min_p = min_p > 0.0 ? fmin(min_p, 1.0) : 0.0;   // NaN: off
-  // p_i >= min_p max p  <=>  z_i >= max z + T ln(min_p)
-  s.zcut = min_p > 0.0 ? (double)s.zmax + (min_p < 1.0 ? (double)T_ * log(min_p) : 0.0) : -INFINITY;
-  if (!(s.zcut <= (double)s.zmax)) s.zcut = (double)s.zmax;   // infinite maximum and temperature
-  const bool use_k = k > 0 && k < p.V, use_p = top_p < 1.0;
+  s.ybin = fminf((float)(16.0 * s.c), 3e38f);
+  const double top_p = (double)pf;
+  const bool use_p = pf < 1.f;
+  // p_i >= min_p max p  <=>  z_i >= max z + T ln(min_p); as the least such value of the dtype's keys
+  float zcut = -INFINITY;
+  if (mf > 0.f) {
+    const double x = (double)s.zmax + (mf < 1.f ? (double)T_ * log((double)mf) : 0.0);
+    zcut = x > -3.4028234663852886e38 ? __double2float_ru(x) : -INFINITY;
+  }
+  float u = p.u[row];
+  u = u > 0.f ? fminf(u, 1.f - 0x1p-24f) : 0.f;   // NaN and negatives: 0
 
-  if (use_k) {
-    // B: the k-th key by counts
-    s.clear_hist(SP_BINS / 2);
+  if (k > 0 && k < p.V) {
+    double above, value;
+    auto number = [](int, double n) { return n; };
+    if (k <= s.C * (SP_THREADS / 4)) {
+      // B: a bin that the k-th largest cannot lie beyond, from the threads' own maxima
+      unsigned* hist = s.clear_hist(SP_BINS);
+      if (best > -INFINITY) atomicAdd(hist + s.bin(best), 1u);
+      int far;
+      s.template border<false>((double)k, number, far, above, value);
+      const float low = above + value >= (double)k ? s.edge_low(far) : -INFINITY;
+      const float floor_ = fmaxf(low, -3.4028234663852886e38f);   // never -infinity itself
+      // what reaches it, first counted
+      int n[1] = {0};
+      s.in_range(floor_, INFINITY, [&](float, int) { ++n[0]; });
+      s.block_sum(n);
+      unsigned long long x[1] = {(unsigned long long)n[0]};
+      int off = 0, m = 0;
+      s.exchange(x, [&](int r, unsigned long long (&w)[1]) {
+        off += r < s.rank ? (int)w[0] : 0;
+        m += (int)w[0];
+      });
+      if (m <= SP_LIST) {
+        // the candidates, to the first CTA (its histograms are read no more: all have passed the exchange)
+        if (tid == 0) sh.nlist = off;
+        __syncthreads();
+        unsigned long long* list = s.cl.map_shared_rank(&sh.list[0], 0);
+        s.in_range(floor_, INFINITY, [&](float z, int idx) {
+          list[atomicAdd(&sh.nlist, 1)] = ((unsigned long long)f2key(z) << 32) | (unsigned)~idx;
+        });
+        s.cl.sync();
+        if (s.rank != 0) return;                // the rest is the first CTA's own
+        int np = 2;
+        while (np < m) np <<= 1;
+        for (int i = m + tid; i < np; i += SP_THREADS) sh.list[i] = 0ull;
+        sp_sort(sh.list, np);
+        const int kk = min(k, m);
+        // weights in the order, eight a thread, and their running sum
+        constexpr int Q = SP_LIST / SP_THREADS;
+        double w[Q], sum = 0.0;
+#pragma unroll
+        for (int j = 0; j < Q; ++j) {
+          const int i = tid * Q + j;
+          w[j] = i < kk ? s.weight(key2f((uint32_t)(sh.list[i] >> 32))) : 0.0;
+          sum += w[j];
+        }
+        auto scan = [&](double mine, double& total) {   // sum of the threads before
+          double inc = mine;
+#pragma unroll
+          for (int d = 1; d < 32; d <<= 1) {
+            const double y = __shfl_up_sync(FULL, inc, d);
+            if (lane >= d) inc += y;
+          }
+          __syncthreads();
+          if (lane == 31) *reinterpret_cast<double*>(&sh.red[warp][0]) = inc;
+          __syncthreads();
+          double b = 0.0;
+          total = 0.0;
+#pragma unroll
+          for (int q = 0; q < SP_WARPS; ++q) {
+            const double y = *reinterpret_cast<double*>(&sh.red[q][0]);
+            b += q < warp ? y : 0.0;
+            total += y;
+          }
+          return b + inc - mine;
+        };
+        double total;
+        double run = scan(sum, total);
+        int keep[1] = {0};
+#pragma unroll
+        for (int j = 0; j < Q; ++j) {
+          const int i = tid * Q + j;
+          if (i < kk) {
+            const bool in = i == 0 || ((!use_p || run < top_p * total) && key2f((uint32_t)(sh.list[i] >> 32)) >= zcut);
+            keep[0] += in;                      // a head of the order: both conditions only turn false
+          }
+          run += w[j];
+        }
+        s.block_sum(keep);
+        // the kept ones in index order
+        int nk = 2;
+        while (nk < keep[0]) nk <<= 1;
+        for (int i = tid; i < nk; i += SP_THREADS) {
+          const unsigned long long x = sh.list[i];
+          // sorted downwards: index up is ~index down; what is cut sinks
+          sh.list[i] = i < keep[0] ? (x << 32) | (x >> 32) : 0ull;
+        }
+        sp_sort(sh.list, nk);
+        sum = 0.0;
+#pragma unroll
+        for (int j = 0; j < Q; ++j) {
+          const int i = tid * Q + j;
+          w[j] = i < keep[0] ? s.weight(key2f((uint32_t)sh.list[i])) : 0.0;
+          sum += w[j];
+        }
+        run = scan(sum, total);
+        const double goal = (double)u * total;
+        // the first whose running sum passes the goal (else, by rounding, the last with mass)
+        int at = INT_MAX, last = -1;
+#pragma unroll
+        for (int j = 0; j < Q; ++j) {
+          if (w[j] > 0.0) {
+            last = tid * Q + j;
+            if (at == INT_MAX && run + w[j] > goal) at = last;
+          }
+          run += w[j];
+        }
+        at = __reduce_min_sync(FULL, at);
+        last = __reduce_max_sync(FULL, last);
+        if (lane == 0) {
+          sh.cand[warp][0] = at;
+          sh.cand[warp][1] = last;
+        }
+        __syncthreads();
+        if (tid == 0) {
+          for (int q = 0; q < SP_WARPS; ++q) {
+            at = min(at, sh.cand[q][0]);
+            last = max(last, sh.cand[q][1]);
+          }
+          const unsigned long long x = sh.list[at == INT_MAX ? last : at];
+          p.token[row] = (int)~(unsigned)(x >> 32);
+          if (p.logprob) p.logprob[row] = (float)log(s.weight(key2f((uint32_t)x)) / total);
+          if (p.kept) p.kept[row] = keep[0];
+        }
+        return;
+      }
+    }
+    // C: the k-th key by counts
+    unsigned* hist = s.clear_hist(SP_BINS);
     int have[1] = {0};
-    for (int v = threadIdx.x; v < s.nvec; v += SP_THREADS) {
+    for (int v = tid; v < s.nvec; v += SP_THREADS) {
       float z[N];
       s.unpack(v, z);
+      int run = 0, rb = -1;                     // equal neighbours in one atomic
 #pragma unroll
-      for (int j = 0; j < N; ++j)
-        if (z[j] > -INFINITY) {
-          ++have[0];
-          atomicAdd(reinterpret_cast<unsigned*>(sh.hist) + s.bin(z[j]), 1u);
+      for (int j = 0; j < N; ++j) {
+        if (!(z[j] > -INFINITY)) continue;
+        ++have[0];
+        const int bb = s.bin(z[j]);
+        if (bb != rb) {
+          if (run) atomicAdd(hist + rb, (unsigned)run);
+          rb = bb;
+          run = 0;
         }
+        ++run;
+      }
+      if (run) atomicAdd(hist + rb, (unsigned)run);
     }
     s.block_sum(have);
     int total = 0;
     unsigned long long x[1] = {(unsigned long long)have[0]};
     s.exchange(x, [&](int, unsigned long long (&w)[1]) { total += (int)w[0]; });
     if (k < total) {
-      const double share = s.combine(0);
-      int b;
-      double above;
-      s.border(share, 0.0, (double)k, b, above);
+      int b, ti;
       uint32_t tk;
-      int ti;
-      s.template refine<false>(b, (double)k - above, 0, false, tk, ti);
+      s.template border<false>((double)k, number, b, above, value);
+      s.template refine<false>(b, (double)k - above, 0, tk, ti);
+      s.cut = true;
       s.ck = tk;
       s.ci = ti;
     }
   }
 
-  // C (and B for top-p): the kept mass by stretches of 32 vectors
   int b = SP_BINS;                              // top-p: kept are the bins before b and a part of b
   double above = 0.0;
-  if (use_p && top_p > 0.0) {
-    s.clear_hist(SP_BINS / 2);
-    for (int v = threadIdx.x; v < s.nvec; v += SP_THREADS) {
+  if (use_p && pf > 0.f) {
+    // C: the mass to fp32, which says what can be left out and where the border is about
+    float part = 0.f;
+    int held[1] = {0};
+    const float scale = s.ybin * (-1.f / 16.f);
+    for (int v = tid; v < s.nvec; v += SP_THREADS) {
       float z[N];
       s.unpack(v, z);
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        if (!s.left(sp_key(z[j], KS), s.i0 + v * N + j)) continue;
-        const int bb = s.bin(z[j]);
-        if (bb >= SP_BINS - 1) continue;        // below 2^-128 of the maximum
-        const float y = s.dist(z[j]) - (float)bb;
-        atomicAdd(reinterpret_cast<unsigned*>(sh.hist) + bb, (unsigned)(exp2f(y * (-1.f / 16.f)) * 65536.f));
+        const bool in = s.left(z[j], s.i0 + v * N + j);
+        part += in ? exp2f((s.zmax - z[j]) * scale) : 0.f;
+        held[0] += in;
       }
     }
-    __syncthreads();
-    const double share = s.combine(1);
-    s.border(share, top_p, 0.0, b, above);
+    double about[1] = {(double)part};
+    s.block_sum(about);
+    s.block_sum(held);
+    double mass32 = 0.0, count = 0.0;
+    unsigned long long x[2] = {(unsigned long long)__double_as_longlong(about[0]), (unsigned long long)held[0]};
+    s.exchange(x, [&](int, unsigned long long (&w)[2]) {
+      mass32 += __longlong_as_double((long long)w[0]);
+      count += (double)w[1];
+    });
+    const float mean = (float)(0.99 * (1.0 - top_p) * mass32 / count);
+    // bins up to this one; the last bin is below 2^-127 of the maximum
+    const int far = mean > 0.f ? min((int)(-16.f * log2f(mean)) + 1, SP_BINS - 2) : SP_BINS - 2;
+    const float low = s.edge_low(far);
+    unsigned* hist = s.clear_hist(SP_BINS);
+    for (int v = tid; v < s.nvec; v += SP_THREADS) {
+      float z[N];
+      s.unpack(v, z);
+      unsigned run = 0;                         // equal neighbours in one atomic
+      int rb = -1;
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        if (!(z[j] >= low) || !s.left(z[j], s.i0 + v * N + j)) continue;
+        const float d = s.zmax - z[j], r = fmaf(d, s.ybin, SP_ONE);
+        const int bb = __float_as_int(r) - 0x4B000000;
+        if (bb > far) continue;
+        if (bb != rb) {
+          if (run) atomicAdd(hist + rb, run);
+          rb = bb;
+          run = 0;
+        }
+        // 2^-(distance from the bin's middle, in sixteenths), below 1.022, in 2^-15 units
+        const float y = fmaf(d, s.ybin, SP_ONE - r);
+        run += (unsigned)__float_as_int(fmaf(exp2f(y * (-1.f / 16.f)), 32768.f, SP_ONE)) - 0x4B000000u;
+      }
+      if (run) atomicAdd(hist + rb, run);
+    }
+    double value;
+    s.template border<false>(top_p * mass32,
+                             [](int i, double n) { return n * (double)exp2f((float)i * (-1.f / 16.f)) * 0x1p-15; }, b,
+                             above, value);
   } else if (use_p) {
     b = 0;                                      // top_p <= 0: one token
   }
+  // D: the kept mass by stretches of 32 vectors
   const int nst = (s.nvec + 31) / 32;
-  double mass = 0.0, in_b = 0.0;
-  int kept = 0, kept_all = 0;
+  int kept = 0;
   double total = 0.0;
   for (int moved = 0;;) {
     double sums[3] = {0.0, 0.0, 0.0};           // all that is left, bins before b, bin b
@@ -504,22 +777,26 @@ __global__ void __launch_bounds__(SP_THREADS) sample_kernel(SampleParams p, int 
       if (v < s.nvec) {
         float z[N];
         s.unpack(v, z);
+        if (use_p) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-          if (!s.left(sp_key(z[j], KS), s.i0 + v * N + j)) continue;
-          const bool over = (double)z[j] >= s.zcut;
-          if (!use_p && !over) continue;
-          const double w = s.weight(z[j]);
-          const int bb = use_p ? s.bin(z[j]) : 0;
-          sums[0] += w;
-          if (bb < b) {
-            sums[1] += w;
-            if (over) {
-              mine += w;
-              ++kept;
-            }
-          } else if (bb == b) {
-            sums[2] += w;
+          for (int j = 0; j < N; ++j) {         // no branches: the chains of the N weights interleave
+            const bool in = s.left(z[j], s.i0 + v * N + j), over = z[j] >= zcut;
+            const double w = in ? s.weight(z[j]) : 0.0;
+            const int bb = s.bin(z[j]);
+            const bool keep = in && over && bb < b;
+            sums[0] += w;
+            sums[1] += bb < b ? w : 0.0;
+            sums[2] += bb == b ? w : 0.0;
+            mine += keep ? w : 0.0;
+            kept += keep;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < N; ++j) {
+            const bool in = s.left(z[j], s.i0 + v * N + j) && z[j] >= zcut;
+            const double w = s.weight(z[j]);
+            mine += in ? w : 0.0;
+            kept += in;
           }
         }
       }
@@ -531,7 +808,8 @@ __global__ void __launch_bounds__(SP_THREADS) sample_kernel(SampleParams p, int 
     unsigned long long x[3];
 #pragma unroll
     for (int q = 0; q < 3; ++q) x[q] = (unsigned long long)__double_as_longlong(sums[q]);
-    total = above = in_b = 0.0;
+    double in_b = 0.0;
+    total = above = 0.0;
     s.exchange(x, [&](int, unsigned long long (&w)[3]) {
       total += __longlong_as_double((long long)w[0]);
       above += __longlong_as_double((long long)w[1]);
@@ -539,98 +817,92 @@ __global__ void __launch_bounds__(SP_THREADS) sample_kernel(SampleParams p, int 
     });
     // the bin is right if the sum passes top_p of the total inside it
     const double goal = top_p * total;
-    if (top_p <= 0.0) break;
+    if (!(pf > 0.f)) break;
     const int way = above >= goal && b > 0 ? -1 : above + in_b < goal && b < SP_BINS - 2 ? 1 : 0;
     if (way == 0 || way == -moved) break;       // right, or between two bins by the sums' last bits
     b += way;
     moved = way;
   }
   if (use_p) {
-    const int e = b / 16;                       // the bin's weights lie in (2^(-e-1), 2^-e], about
+    // the bin's weights lie within 2^(-(b +- 1/2) / 16) of the maximum: scaled by 2^e they are at most 2^(1/16)
+    const int e = b / 16;
     uint32_t tk;
     int ti;
-    double need = ldexp(top_p * total - above, 40 + e);
+    double need = ldexp(top_p * total - above, 33 + e);
     if (!(need > 0.0)) need = 0.0;
-    s.template refine<true>(b, need, e, true, tk, ti);
+    s.template refine<true>(b, need, e, tk, ti);
     // the part of bin b that stays
+    const float zt = sp_value<KS>(tk), top = s.edge_high(b);
     for (int st = warp; st < nst; st += SP_WARPS) {
       const int v = st * 32 + lane;
-      double mine = 0.0;
-      bool any = false;
+      unsigned in = 0;
+      float z[N];
       if (v < s.nvec) {
-        float z[N];
         s.unpack(v, z);
 #pragma unroll
+        for (int j = 0; j < N; ++j) in |= (z[j] >= zt && z[j] <= top && z[j] >= zcut ? 1u : 0u) << j;
+      }
+      if (!__any_sync(FULL, in != 0)) continue;
+      double mine = 0.0;
+      if (in) {
+#pragma unroll
         for (int j = 0; j < N; ++j) {
-          const uint32_t key = sp_key(z[j], KS);
           const int idx = s.i0 + v * N + j;
-          if (key < tk || (key == tk && idx > ti) || s.bin(z[j]) != b || !s.left(key, idx) || (double)z[j] < s.zcut) continue;
+          if (!((in >> j) & 1u) || (z[j] == zt && idx > ti) || s.bin(z[j]) != b || !s.left(z[j], idx)) continue;
           mine += s.weight(z[j]);
           ++kept;
-          any = true;
         }
       }
-      if (__any_sync(FULL, any)) {
-        mine = warp_sum_d(mine);
-        if (lane == 0) s.wsum[st] += mine;
-      }
+      mine = warp_sum_d(mine);
+      if (lane == 0) s.wsum[st] += mine;
     }
     // from here on `left` is the final cut
-    s.ci = tk == s.ck ? min(ti, s.ci) : ti;
+    s.ci = s.cut && tk == s.ck ? min(ti, s.ci) : ti;
     s.ck = tk;
+    s.cut = true;
   }
   int kk[1] = {kept};
   s.block_sum(kk);                              // also orders the stretches' sums before their use
-  // D: the slices' masses, the slice, the stretch, the element
+  // E: the slices' masses, the slice, the stretch, the element
+  const int q = (nst + 31) / 32;                // stretches a lane of the first warp
+  double lane_sum = 0.0, lane_inc = 0.0;
   if (warp == 0) {
-    const int q = (nst + 31) / 32;
-    double sum = 0.0;
-    for (int j = lane * q; j < min(nst, (lane + 1) * q); ++j) sum += s.wsum[j];
-    double inc = sum;
+    for (int j = lane * q; j < min(nst, (lane + 1) * q); ++j) lane_sum += s.wsum[j];
+    lane_inc = lane_sum;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const double y = __shfl_up_sync(FULL, inc, d);
-      if (lane >= d) inc += y;
+      const double y = __shfl_up_sync(FULL, lane_inc, d);
+      if (lane >= d) lane_inc += y;
     }
-    if (lane == 31) sh.found[1] = inc;
+    if (lane == 31) sh.found[2] = lane_inc;
   }
   __syncthreads();
-  double before = 0.0, upto = 0.0;
-  int chosen = -1, last = 0;
-  mass = 0.0;
+  double mass = 0.0, before = 0.0, chosen_before = 0.0;
+  int chosen = -1, kept_all = 0;
   {
-    double cum[SP_MAXC];
-    unsigned long long x[2] = {(unsigned long long)__double_as_longlong(sh.found[1]), (unsigned long long)kk[0]};
-    s.exchange(x, [&](int r, unsigned long long (&w)[2]) {
-      const double m = __longlong_as_double((long long)w[0]);
-      if (m > 0.0) last = r;
-      mass += m;
-      cum[r & (SP_MAXC - 1)] = mass;
+    // twice over the slices' masses: the total, then the first slice whose running sum passes u of it
+    unsigned long long x[2] = {(unsigned long long)__double_as_longlong(sh.found[2]), (unsigned long long)kk[0]};
+    s.exchange(x, [&](int, unsigned long long (&w)[2]) {
+      mass += __longlong_as_double((long long)w[0]);
       kept_all += (int)w[1];
     });
-    float u = p.u[row];
-    u = u > 0.f ? fminf(u, 1.f - 0x1p-24f) : 0.f;   // NaN and negatives: 0
-    upto = (double)u * mass;
-    for (int r = 0; r < s.C; ++r)
-      if (chosen < 0 && cum[r & (SP_MAXC - 1)] > upto) chosen = r;
-    if (chosen < 0) chosen = last;
-    before = chosen > 0 ? cum[(chosen - 1) & (SP_MAXC - 1)] : 0.0;
+    for (int r = 0; r < s.C; ++r) {
+      const double m = __longlong_as_double((long long)sh.xch[(s.step - 1) & 1][r][0]);
+      if (m > 0.0 && (chosen < 0 || chosen_before + __longlong_as_double((long long)sh.xch[(s.step - 1) & 1][chosen][0]) <=
+                                        (double)u * mass)) {
+        chosen = r;                             // (else, by rounding, the last slice with mass)
+        chosen_before = before;
+      }
+      before += m;
+    }
   }
+  const double goal = (double)u * mass;
   if (s.rank == chosen && warp == 0) {
     // the stretch whose running sum passes the goal, or the last one with mass
-    const int q = (nst + 31) / 32;
-    double sum = 0.0;
-    for (int j = lane * q; j < min(nst, (lane + 1) * q); ++j) sum += s.wsum[j];
-    double inc = sum;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const double y = __shfl_up_sync(FULL, inc, d);
-      if (lane >= d) inc += y;
-    }
-    const unsigned hit = __ballot_sync(FULL, before + inc > upto && sum > 0.0);
-    const unsigned any = __ballot_sync(FULL, sum > 0.0);
+    const unsigned hit = __ballot_sync(FULL, chosen_before + lane_inc > goal && lane_sum > 0.0);
+    const unsigned any = __ballot_sync(FULL, lane_sum > 0.0);
     const int l = hit ? __ffs(hit) - 1 : 31 - __clz(any);
-    double run = before + __shfl_sync(FULL, inc - sum, l);
+    double run = chosen_before + __shfl_sync(FULL, lane_inc - lane_sum, l);
     int st = -1;
     double st_run = 0.0;
     for (int j = l * q; j < min(nst, (l + 1) * q); ++j) {
@@ -638,30 +910,30 @@ __global__ void __launch_bounds__(SP_THREADS) sample_kernel(SampleParams p, int 
       if (w > 0.0) {
         st = j;
         st_run = run;
-        if (run + w > upto) break;
+        if (run + w > goal) break;
       }
       run += w;
     }
     const int v = st * 32 + lane;
-    float z[N];
     double w[N], mine = 0.0;
 #pragma unroll
     for (int j = 0; j < N; ++j) w[j] = 0.0;
     if (v < s.nvec) {
+      float z[N];
       s.unpack(v, z);
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        if (s.left(sp_key(z[j], KS), s.i0 + v * N + j) && (double)z[j] >= s.zcut) w[j] = s.weight(z[j]);
+        if (s.left(z[j], s.i0 + v * N + j) && z[j] >= zcut) w[j] = s.weight(z[j]);
         mine += w[j];
       }
     }
-    inc = mine;
+    double inc = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const double y = __shfl_up_sync(FULL, inc, d);
       if (lane >= d) inc += y;
     }
-    const unsigned hit2 = __ballot_sync(FULL, st_run + inc > upto && mine > 0.0);
+    const unsigned hit2 = __ballot_sync(FULL, st_run + inc > goal && mine > 0.0);
     const unsigned any2 = __ballot_sync(FULL, mine > 0.0);
     const int l2 = hit2 ? __ffs(hit2) - 1 : 31 - __clz(any2);
     if (lane == l2) {
@@ -670,7 +942,7 @@ __global__ void __launch_bounds__(SP_THREADS) sample_kernel(SampleParams p, int 
       double tw = 1.0;
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        if (w[j] > 0.0 && (tok < 0 || r2 <= upto)) {
+        if (w[j] > 0.0 && (tok < 0 || r2 <= goal)) {
           tok = s.i0 + v * N + j;
           tw = w[j];
         }
@@ -681,16 +953,15 @@ __global__ void __launch_bounds__(SP_THREADS) sample_kernel(SampleParams p, int 
       if (p.kept) p.kept[row] = kept_all;
     }
   }
-  s.cl.sync();
 }
 
 cudaError_t launch_sample(const SampleParams& p, cudaStream_t st) {
   const int es = p.bf16 ? 2 : 4, vn = 16 / es;
-  // the cluster: slices of at most 19456 elements for few rows, so that the passes over a slice are
-  // short; of at most 32768 once the rows alone fill the GPU
-  const int most = p.n * 8 >= 4 * num_sms() ? 32768 : 19456;
+  // the cluster: slices of at most `most` elements.  Few rows: short slices, for short passes, up to 16
+  // CTAs a row (more than 8 need the non-portable size) while all rows fit the GPU at once
   int C = 1;
-  while (C < SP_MAXC && (p.V + C - 1) / C > most) C <<= 1;
+  while (C < 8 && (p.V + C - 1) / C > 16384) C <<= 1;
+  if (C == 8 && p.n * 16 <= num_sms()) C = 16;
   const int unit = 32 * vn;
   const int per = ((p.V + C - 1) / C + unit - 1) / unit * unit;
   const size_t smem = sizeof(SpShared) + (size_t)per * es + (size_t)(per / unit) * sizeof(double);
@@ -708,6 +979,7 @@ cudaError_t launch_sample(const SampleParams& p, cudaStream_t st) {
   cfg.numAttrs = 1;
   auto go = [&](auto kern) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess && C > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kern, p, per);
     if (e == cudaSuccess) count_launch();
     return e;

@@ -88,8 +88,12 @@ def sample(z, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
     if not temperature > 0:
         return int(order[0]), 0.0, 1
     zm = z[order[0]]
+    if zm == np.inf:                           # infinite logits are the only ones kept, all alike
+        order = order[z[order] == np.inf]
+        z = np.where(z == np.inf, 0.0, -np.inf)
+        zm = 0.0
+    dist = z - zm
     with np.errstate(invalid="ignore"):
-        dist = np.where(z == zm, 0.0, z - zm)
         x = np.where(np.isneginf(dist), -np.inf, dist / temperature)
     w = np.exp(x)
     if top_k > 0:
