@@ -16,15 +16,16 @@
 //   B  top-k, few: the k-th largest of the threads' own maxima is a bound that k elements reach; what
 //      reaches it goes to one CTA, which sorts it, sums it in that order for top-p, and again in
 //      index order for the token
-//   C  else the cut is searched: counts (top-k) or masses (top-p) by bins of 1/16 octave of weight below
+//   C  else the cut is searched: counts (top-k) or masses (top-p) by bins of 1/8 octave of weight below
 //      the maximum (shared-memory integer atomics: order does not matter), summed over the
 //      cluster through distributed shared memory; the bin that holds the border is searched
 //      again by ranges of the key, until one key is left; of its ties the lowest indices stay.
-//      Tokens whose weight is below (1 - top_p) of the mean are left out of the first search of
-//      masses: together they hold less than the 1 - top_p that is cut.  Its bins hold masses to 16
-//      bits only: the exact sums of D decide whether the bin is the right one (else its neighbour is
-//      taken), the later searches count in 2^-33 units of the bin's weights, or exactly once a
-//      bin is one key.
+//      512 bins: every CTA reads all histograms of the cluster, which at 2048 bins and 16 CTAs took
+//      9.8k cycles.  Tokens whose weight is below (1 - top_p) of the mean are left out of the first
+//      search of masses: together they hold less than the 1 - top_p that is cut.  Its bins hold
+//      masses to 16 bits only: the exact sums of D decide whether the bin is the right one (else its
+//      neighbour is taken), the later searches count in 2^-31 units of the bin's weights, or
+//      exactly once a bin is one key.
 //   D  fp64 sums of the kept weights by 32-vector stretches of a warp, in index order
 //   E  the stretch, lane and element where u * total falls
 #include <cooperative_groups.h>
@@ -32,23 +33,25 @@
 #include <climits>
 
 #include "kernels.cuh"
+#include "tc_sm100.cuh"
 
 namespace kvc {
 namespace cg = cooperative_groups;
 
 constexpr int SP_THREADS = 512;
 constexpr int SP_WARPS = SP_THREADS / 32;
-constexpr int SP_BINS = 2048;
+constexpr int SP_BINS = 512;
 constexpr int SP_MAXC = 16;
 constexpr int SP_LIST = 4096;                   // candidates that one CTA sorts
 constexpr float SP_ONE = 8388608.f;             // 2^23: adding it leaves the rounded integer in a float's low bits
 
 struct alignas(16) SpShared {                   // the slice follows: its vectors are 16-byte aligned
   union {
-    unsigned hist[2][2 * SP_BINS];              // two searches deep: counts or masses; two 17-bit limbs of a mass
+    unsigned hist[2][2 * SP_BINS];              // two searches deep: counts or masses; two 16-bit limbs of a mass
     unsigned long long list[SP_LIST];
   };
   double table[64];                             // 2^(j / 64)
+  double part[2];                               // beside a histogram: the mass of the slice, to fp32
   unsigned long long xch[2][SP_MAXC][4];        // values of every CTA of the cluster, two steps deep
   unsigned long long red[SP_WARPS][4];
   double found[4];
@@ -103,6 +106,19 @@ __device__ __forceinline__ uint4 sp_load(const T* row, int64_t i, int V) {
   return x.u;
 }
 
+// Sum of N values, pairwise.
+template <int N>
+__device__ __forceinline__ double sp_tree(const double (&v)[N]) {
+  double a[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) a[j] = v[j];
+#pragma unroll
+  for (int h = N / 2; h > 0; h >>= 1)
+#pragma unroll
+    for (int j = 0; j < h; ++j) a[j] = a[2 * j] + a[2 * j + 1];
+  return a[0];
+}
+
 template <typename T>
 struct SpRow {
   static constexpr int N = SpVec<T>::N, KS = SpVec<T>::KSHIFT;
@@ -113,6 +129,7 @@ struct SpRow {
   int C, rank, nvec, i0;                        // cluster size, rank, vectors of the slice, its first index
   int step, search;
   float zmax, ybin;                             // bins below the maximum: (zmax - z) * ybin
+  float zlow;                                   // weights below this one's, 2^-64 of the largest, are nothing
   double c;                                     // log2(e) / T
   bool cut;                                     // top-k left: key > ck, or key == ck and index <= ci
   uint32_t ck;
@@ -156,9 +173,9 @@ struct SpRow {
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      V s = V(0);
+      V s = *reinterpret_cast<V*>(&sh.red[lane & (SP_WARPS - 1)][k]);
 #pragma unroll
-      for (int w = 0; w < SP_WARPS; ++w) s += *reinterpret_cast<V*>(&sh.red[w][k]);
+      for (int o = SP_WARPS / 2; o > 0; o >>= 1) s += __shfl_xor_sync(FULL, s, o);
       v[k] = s;
     }
   }
@@ -169,10 +186,9 @@ struct SpRow {
     const float r = fmaf(zmax - z, ybin, SP_ONE);
     return min(__float_as_int(r) - 0x4B000000, SP_BINS - 1);
   }
-  __device__ __forceinline__ double weight(float z) const {
-    double t = ((double)z - (double)zmax) * c;
-    const bool none = !(t > -64.0);             // -infinity at an infinite temperature (NaN) too
-    t = none ? -64.0 : t;
+  // For z >= zlow: weights of the others are nothing.
+  __device__ __forceinline__ double raw_weight(float z) const {
+    const double t = ((double)z - (double)zmax) * c;
     const double magic = 6755399441055744.0 / 64;   // 1.5 * 2^52 / 64: rounds t to a multiple of 1/64
     const double r = t + magic;
     const int k = __double2loint(r);
@@ -183,8 +199,9 @@ struct SpRow {
     p = fma(f, p, 6.931471805599453e-1);
     p = fma(f, p, 1.0);
     p *= sh.table[k & 63];
-    return none ? 0.0 : __hiloint2double(__double2hiint(p) + ((k >> 6) << 20), __double2loint(p));
+    return __hiloint2double(__double2hiint(p) + ((k >> 6) << 20), __double2loint(p));
   }
+  __device__ __forceinline__ double weight(float z) const { return z >= zlow ? raw_weight(z) : 0.0; }
   __device__ __forceinline__ bool left(float z, int idx) const {
     if (!cut) return z > -INFINITY;
     const uint32_t key = sp_key(z, KS);
@@ -209,37 +226,32 @@ struct SpRow {
     __syncthreads();
     return h;
   }
-  // The first bin at which the sum over the cluster's histograms reaches `target`, or the last that
-  // holds something; the sum before it and the bin's own value.  A bin's value is val(bin, words
-  // summed over the cluster); LIMBS: the histogram has a second half, 2^17 times the first's unit.
-  // Every CTA reads all histograms (a thread four bins, all its loads in flight) and scans them for
-  // itself: one cluster barrier a search.  The next search uses the other buffer, so a slow reader is
-  // not overtaken.
+  // The first bin at which the sum over the cluster's histograms reaches `target` (frac > 0: that
+  // share of the cluster's `part`), or the last that holds something; the sum before it and the bin's
+  // own value.  A bin's value is val(bin, words summed over the cluster); LIMBS: the histogram has a
+  // second half, 2^16 times the first's unit.  Every CTA reads all histograms (a thread one bin, its
+  // loads all in flight) and scans them for itself: one cluster barrier a search.  The next search
+  // uses the other buffer, so a slow reader is not overtaken.
   template <bool LIMBS, typename F>
-  __device__ __forceinline__ void border(double target, F&& val, int& b, double& above, double& value) {
-    static_assert(SP_BINS == 4 * SP_THREADS, "four bins a thread");
+  __device__ __forceinline__ void border(double frac, double target, F&& val, int& b, double& above, double& value) {
+    static_assert(SP_BINS == SP_THREADS, "a bin a thread");
     cl.sync();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    unsigned long long h[4] = {0, 0, 0, 0};
+    unsigned long long h = 0;
 #pragma unroll 8
     for (int r = 0; r < C; ++r) {
-      const uint4* o = reinterpret_cast<const uint4*>(cl.map_shared_rank(&sh.hist[search & 1][0], r));
-      const uint4 x = o[threadIdx.x];
-      h[0] += x.x; h[1] += x.y; h[2] += x.z; h[3] += x.w;
-      if (LIMBS) {
-        const uint4 y = o[SP_BINS / 4 + threadIdx.x];
-        h[0] += (unsigned long long)y.x << 17; h[1] += (unsigned long long)y.y << 17;
-        h[2] += (unsigned long long)y.z << 17; h[3] += (unsigned long long)y.w << 17;
-      }
+      const unsigned* o = cl.map_shared_rank(&sh.hist[search & 1][0], r);
+      h += o[threadIdx.x];
+      if (LIMBS) h += (unsigned long long)o[SP_BINS + threadIdx.x] << 16;
+    }
+    if (frac > 0.0 && warp == 0) {
+      double m = lane < C ? *cl.map_shared_rank(&sh.part[search & 1], lane) : 0.0;
+      m = warp_sum_d(m);
+      if (lane == 0) sh.found[3] = frac * m;
     }
     ++search;
-    double v[4], sum = 0.0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[j] = h[j] ? val(4 * (int)threadIdx.x + j, (double)h[j]) : 0.0;
-      sum += v[j];
-    }
-    double inc = sum;
+    const double v = h ? val((int)threadIdx.x, (double)h) : 0.0;
+    double inc = v;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const double y = __shfl_up_sync(FULL, inc, d);
@@ -247,45 +259,28 @@ struct SpRow {
     }
     if (lane == 31) *reinterpret_cast<double*>(&sh.red[warp][0]) = inc;
     __syncthreads();
-    double before = 0.0;
-    for (int w = 0; w < warp; ++w) before += *reinterpret_cast<double*>(&sh.red[w][0]);
-    const unsigned some = __ballot_sync(FULL, sum > 0.0);
-    const unsigned hit = __ballot_sync(FULL, sum > 0.0 && before + inc >= target);
+    if (frac > 0.0) target = sh.found[3];
+    // sum of the warps before (lanes 0 .. 15 hold the warps' sums)
+    double before = (lane & (SP_WARPS - 1)) < warp ? *reinterpret_cast<double*>(&sh.red[lane & (SP_WARPS - 1)][0]) : 0.0;
+#pragma unroll
+    for (int o = SP_WARPS / 2; o > 0; o >>= 1) before += __shfl_xor_sync(FULL, before, o);
+    const unsigned some = __ballot_sync(FULL, v > 0.0);
+    const unsigned hit = __ballot_sync(FULL, v > 0.0 && before + inc >= target);
     if (lane == 0) {
       sh.cand[warp][0] = hit ? warp * 32 + __ffs(hit) - 1 : INT_MAX;
       sh.cand[warp][1] = some ? warp * 32 + 31 - __clz(some) : -1;
     }
     __syncthreads();
-    int at = INT_MAX, end = -1;
-#pragma unroll
-    for (int w = 0; w < SP_WARPS; ++w) {
-      at = min(at, sh.cand[w][0]);
-      end = max(end, sh.cand[w][1]);
-    }
-    if (at == INT_MAX) at = max(end, 0);
-    if ((int)threadIdx.x == at) {
-      double run = before + inc - sum, last_run = run, last_v = 0.0;
-      int last = 0;
-      bool done = false;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (!done && v[j] > 0.0) {
-          last = j;
-          last_run = run;
-          last_v = v[j];
-          done = run + v[j] >= target;
-        }
-        run += v[j];
-      }
-      sh.ifound[0] = 4 * at + last;
-      sh.found[0] = last_run;
-      sh.found[1] = last_v;
+    const int at = __reduce_min_sync(FULL, sh.cand[lane & (SP_WARPS - 1)][0]);
+    const int end = __reduce_max_sync(FULL, sh.cand[lane & (SP_WARPS - 1)][1]);
+    b = at == INT_MAX ? max(end, 0) : at;
+    if ((int)threadIdx.x == b) {
+      sh.found[0] = before + inc - v;
+      sh.found[1] = v;
     }
     __syncthreads();
-    b = sh.ifound[0];
     above = sh.found[0];
     value = sh.found[1];
-    __syncthreads();
   }
 
   // use(value, index) for every element of the slice with lo <= value <= hi; they are few
@@ -306,11 +301,13 @@ struct SpRow {
   }
 
   // Within bin b0 (of the tokens left by top-k), the key at which the count (MASS: the mass, in units
-  // of 2^-(33 + e)) reaches `need`, and the index of the last tie that stays.
+  // of 2^-(31 + e)) reaches `need`, and the index of the last tie that stays.  False if the bin holds
+  // less than that (then nothing else is set).
   template <bool MASS>
-  __device__ __forceinline__ void refine(int b0, double need, int e, uint32_t& tkey, int& tidx) {
+  __device__ __forceinline__ bool refine(int b0, double need, int e, uint32_t& tkey, int& tidx) {
     uint32_t hi = sp_key(edge_high(b0), KS), lo = max(sp_key(edge_low(b0), KS), sp_key(-INFINITY, KS) + 1u);
     double above = 0.0, value = 0.0;
+    bool first_search = true;
     int shift = 0;
     while (((hi - lo) >> shift) >= SP_BINS) ++shift;
     while (true) {
@@ -320,9 +317,9 @@ struct SpRow {
         if (bin(z) != b0 || !left(z, idx)) return;
         const uint32_t hb = (hi - sp_key(z, KS)) >> shift;
         if (limbs) {
-          const unsigned long long q = (unsigned long long)__double2ll_rn(scalbn(weight(z), 33 + e));
-          atomicAdd(hist + hb, (unsigned)(q & 0x1ffffu));
-          atomicAdd(hist + SP_BINS + hb, (unsigned)(q >> 17));
+          const unsigned long long q = (unsigned long long)__double2ll_rn(scalbn(weight(z), 31 + e));
+          atomicAdd(hist + hb, (unsigned)(q & 0xffffu));
+          atomicAdd(hist + SP_BINS + hb, (unsigned)(q >> 16));
         } else {
           atomicAdd(hist + hb, 1u);
         }
@@ -330,15 +327,17 @@ struct SpRow {
       int hb;
       double ab;
       if (limbs) {
-        border<true>(need - above, [](int, double n) { return n; }, hb, ab, value);
+        border<true>(0.0, need - above, [](int, double n) { return n; }, hb, ab, value);
       } else if (MASS) {                        // a bin is one key: its weight times its count
         const uint32_t first = hi;
-        border<false>(need - above,
-                      [&](int i, double n) { return n * scalbn(weight(sp_value<KS>(first - (uint32_t)i)), 33 + e); }, hb, ab,
+        border<false>(0.0, need - above,
+                      [&](int i, double n) { return n * scalbn(weight(sp_value<KS>(first - (uint32_t)i)), 31 + e); }, hb, ab,
                       value);
       } else {
-        border<false>(need - above, [](int, double n) { return n; }, hb, ab, value);
+        border<false>(0.0, need - above, [](int, double n) { return n; }, hb, ab, value);
       }
+      if (MASS && first_search && ab + value < need) return false;
+      first_search = false;
       above += ab;
       const uint32_t top = hi - ((uint32_t)hb << shift);
       const uint32_t span = (1u << shift) - 1u;
@@ -352,13 +351,13 @@ struct SpRow {
     // of the ties of tkey the first `take` in index order stay; `value` tells how many there are
     double take = need - above, ties = value;
     if (MASS) {
-      const double w = scalbn(weight(sp_value<KS>(tkey)), 33 + e);
+      const double w = scalbn(weight(sp_value<KS>(tkey)), 31 + e);
       take = w > 0.0 ? ceil(take / w) : 1.0;
       ties = w > 0.0 ? rint(value / w) : 1.0;
     }
     if (take < 1.0) take = 1.0;
     tidx = INT_MAX;
-    if (take >= ties) return;
+    if (take >= ties) return true;
     // ties of every 32-vector stretch, in the histogram words of the next search
     const int lane = threadIdx.x & 31, nst = (nvec + 31) / 32;
     const float zt = sp_value<KS>(tkey);
@@ -430,6 +429,7 @@ struct SpRow {
     int at = 0;
     exchange<1>(y, [&](int, unsigned long long (&w)[1]) { at = max(at, (int)w[0]); });
     tidx = at - 1;
+    return true;
   }
 };
 
@@ -451,7 +451,7 @@ __device__ __forceinline__ void sp_sort(unsigned long long* a, int n) {
 }
 
 template <typename T, bool ALIGNED>
-__global__ void __launch_bounds__(SP_THREADS) sample_kernel(SampleParams p, int per_cta) {
+__global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, int per_cta) {
   constexpr int N = SpVec<T>::N, KS = SpVec<T>::KSHIFT;
   static_assert(sizeof(SpShared) % 16 == 0, "vectors follow");
   extern __shared__ __align__(16) uint8_t sp_raw[];
@@ -530,7 +530,11 @@ __global__ void __launch_bounds__(SP_THREADS) sample_kernel(SampleParams p, int 
     s.zmax = 0.f;
   }
   s.c = 1.4426950408889634 / (double)T_;
-  s.ybin = fminf((float)(16.0 * s.c), 3e38f);
+  s.ybin = fminf((float)(8.0 * s.c), 3e38f);
+  {
+    const double x = (double)s.zmax - 64.0 / s.c;   // (an infinite temperature: -infinity, held above it)
+    s.zlow = x > -3.4028234663852886e38 ? __double2float_ru(x) : -3.4028234663852886e38f;
+  }
   const double top_p = (double)pf;
   const bool use_p = pf < 1.f;
   // p_i >= min_p max p  <=>  z_i >= max z + T ln(min_p); as the least such value of the dtype's keys
@@ -550,7 +554,7 @@ __global__ void __launch_bounds__(SP_THREADS) sample_kernel(SampleParams p, int 
       unsigned* hist = s.clear_hist(SP_BINS);
       if (best > -INFINITY) atomicAdd(hist + s.bin(best), 1u);
       int far;
-      s.template border<false>((double)k, number, far, above, value);
+      s.template border<false>(0.0, (double)k, number, far, above, value);
       const float low = above + value >= (double)k ? s.edge_low(far) : -INFINITY;
       const float floor_ = fmaxf(low, -3.4028234663852886e38f);   // never -infinity itself
       // what reaches it, first counted
@@ -696,7 +700,7 @@ __global__ void __launch_bounds__(SP_THREADS) sample_kernel(SampleParams p, int 
     if (k < total) {
       int b, ti;
       uint32_t tk;
-      s.template border<false>((double)k, number, b, above, value);
+      s.template border<false>(0.0, (double)k, number, b, above, value);
       s.template refine<false>(b, (double)k - above, 0, tk, ti);
       s.cut = true;
       s.ck = tk;
@@ -707,32 +711,22 @@ __global__ void __launch_bounds__(SP_THREADS) sample_kernel(SampleParams p, int 
   int b = SP_BINS;                              // top-p: kept are the bins before b and a part of b
   double above = 0.0;
   if (use_p && pf > 0.f) {
-    // C: the mass to fp32, which says what can be left out and where the border is about
+    // C: the slice's mass to fp32.  The whole row's is no smaller, so what is below (1 - top_p) of it
+    // over V is below (1 - top_p) of the mean, and each CTA knows by itself what to leave out
     float part = 0.f;
-    int held[1] = {0};
-    const float scale = s.ybin * (-1.f / 16.f);
+    const float scale = s.ybin * (-1.f / 8.f);
     for (int v = tid; v < s.nvec; v += SP_THREADS) {
       float z[N];
       s.unpack(v, z);
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const bool in = s.left(z[j], s.i0 + v * N + j);
-        part += in ? exp2f((s.zmax - z[j]) * scale) : 0.f;
-        held[0] += in;
-      }
+      for (int j = 0; j < N; ++j) part += s.left(z[j], s.i0 + v * N + j) ? tc::ex2((s.zmax - z[j]) * scale) : 0.f;
     }
     double about[1] = {(double)part};
     s.block_sum(about);
-    s.block_sum(held);
-    double mass32 = 0.0, count = 0.0;
-    unsigned long long x[2] = {(unsigned long long)__double_as_longlong(about[0]), (unsigned long long)held[0]};
-    s.exchange(x, [&](int, unsigned long long (&w)[2]) {
-      mass32 += __longlong_as_double((long long)w[0]);
-      count += (double)w[1];
-    });
-    const float mean = (float)(0.99 * (1.0 - top_p) * mass32 / count);
-    // bins up to this one; the last bin is below 2^-127 of the maximum
-    const int far = mean > 0.f ? min((int)(-16.f * log2f(mean)) + 1, SP_BINS - 2) : SP_BINS - 2;
+    if (tid == 0) sh.part[s.search & 1] = about[0];
+    const float mean = (float)(0.99 * (1.0 - top_p) * about[0] / p.V);
+    // bins up to this one; the last bin is below 2^-63 of the maximum
+    const int far = mean > 0.f ? min((int)(-8.f * log2f(mean)) + 1, SP_BINS - 2) : SP_BINS - 2;
     const float low = s.edge_low(far);
     unsigned* hist = s.clear_hist(SP_BINS);
     for (int v = tid; v < s.nvec; v += SP_THREADS) {
@@ -751,15 +745,15 @@ __global__ void __launch_bounds__(SP_THREADS) sample_kernel(SampleParams p, int 
           rb = bb;
           run = 0;
         }
-        // 2^-(distance from the bin's middle, in sixteenths), below 1.022, in 2^-15 units
+        // 2^-(distance from the bin's middle, in eighths), below 1.045, in 2^-15 units
         const float y = fmaf(d, s.ybin, SP_ONE - r);
-        run += (unsigned)__float_as_int(fmaf(exp2f(y * (-1.f / 16.f)), 32768.f, SP_ONE)) - 0x4B000000u;
+        run += (unsigned)__float_as_int(fmaf(tc::ex2(y * (-1.f / 8.f)), 32768.f, SP_ONE)) - 0x4B000000u;
       }
       if (run) atomicAdd(hist + rb, run);
     }
     double value;
-    s.template border<false>(top_p * mass32,
-                             [](int i, double n) { return n * (double)exp2f((float)i * (-1.f / 16.f)) * 0x1p-15; }, b,
+    s.template border<false>(top_p, 0.0,
+                             [](int i, double n) { return n * (double)exp2f((float)i * (-1.f / 8.f)) * 0x1p-15; }, b,
                              above, value);
   } else if (use_p) {
     b = 0;                                      // top_p <= 0: one token
@@ -767,70 +761,68 @@ __global__ void __launch_bounds__(SP_THREADS) sample_kernel(SampleParams p, int 
   // D: the kept mass by stretches of 32 vectors
   const int nst = (s.nvec + 31) / 32;
   int kept = 0;
-  double total = 0.0;
   for (int moved = 0;;) {
-    double sums[3] = {0.0, 0.0, 0.0};           // all that is left, bins before b, bin b
+    double sums[2] = {0.0, 0.0};                // all that is left, bins before b
+    const float rb = SP_ONE + (float)b;         // bin(z) < b  <=>  fma(zmax - z, ybin, 2^23) < 2^23 + b
     kept = 0;
     for (int st = warp; st < nst; st += SP_WARPS) {
       const int v = st * 32 + lane;
       double mine = 0.0;
       if (v < s.nvec) {
         float z[N];
+        double w[N];
         s.unpack(v, z);
-        if (use_p) {
+        unsigned head = 0;                      // kept for certain: in bins before b, above the min-p cut
 #pragma unroll
-          for (int j = 0; j < N; ++j) {         // no branches: the chains of the N weights interleave
-            const bool in = s.left(z[j], s.i0 + v * N + j), over = z[j] >= zcut;
-            const double w = in ? s.weight(z[j]) : 0.0;
-            const int bb = s.bin(z[j]);
-            const bool keep = in && over && bb < b;
-            sums[0] += w;
-            sums[1] += bb < b ? w : 0.0;
-            sums[2] += bb == b ? w : 0.0;
-            mine += keep ? w : 0.0;
-            kept += keep;
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < N; ++j) {
-            const bool in = s.left(z[j], s.i0 + v * N + j) && z[j] >= zcut;
-            const double w = s.weight(z[j]);
-            mine += in ? w : 0.0;
-            kept += in;
-          }
+        for (int j = 0; j < N; ++j) {           // no branches: the chains of the N weights interleave
+          const bool in = s.left(z[j], s.i0 + v * N + j), some = in && z[j] >= s.zlow;
+          const double x = s.raw_weight(some ? z[j] : s.zmax);
+          w[j] = some ? x : 0.0;
+          const bool before = fmaf(s.zmax - z[j], s.ybin, SP_ONE) < rb || !use_p;
+          head |= (in && before && z[j] >= zcut ? 1u : 0u) << j;
+          if (use_p) sums[1] += before ? w[j] : 0.0;
         }
+        if (use_p) sums[0] += sp_tree<N>(w);
+        kept += __popc(head);
+#pragma unroll
+        for (int j = 0; j < N; ++j) w[j] = (head >> j) & 1u ? w[j] : 0.0;
+        mine = sp_tree<N>(w);
       }
       mine = warp_sum_d(mine);
       if (lane == 0) s.wsum[st] = mine;
     }
     if (!use_p) break;
     s.block_sum(sums);
-    unsigned long long x[3];
+    unsigned long long x[2];
 #pragma unroll
-    for (int q = 0; q < 3; ++q) x[q] = (unsigned long long)__double_as_longlong(sums[q]);
-    double in_b = 0.0;
-    total = above = 0.0;
-    s.exchange(x, [&](int, unsigned long long (&w)[3]) {
+    for (int q = 0; q < 2; ++q) x[q] = (unsigned long long)__double_as_longlong(sums[q]);
+    double total = 0.0;
+    above = 0.0;
+    s.exchange(x, [&](int, unsigned long long (&w)[2]) {
       total += __longlong_as_double((long long)w[0]);
       above += __longlong_as_double((long long)w[1]);
-      in_b += __longlong_as_double((long long)w[2]);
     });
-    // the bin is right if the sum passes top_p of the total inside it
-    const double goal = top_p * total;
-    if (!(pf > 0.f)) break;
-    const int way = above >= goal && b > 0 ? -1 : above + in_b < goal && b < SP_BINS - 2 ? 1 : 0;
-    if (way == 0 || way == -moved) break;       // right, or between two bins by the sums' last bits
-    b += way;
-    moved = way;
-  }
-  if (use_p) {
-    // the bin's weights lie within 2^(-(b +- 1/2) / 16) of the maximum: scaled by 2^e they are at most 2^(1/16)
-    const int e = b / 16;
+    // the bin is right if the sum reaches top_p of the total inside it (b == 0: it starts there)
+    const double goal = pf > 0.f ? top_p * total : 0.0;
+    if (above >= goal && b > 0 && moved <= 0) {
+      --b;
+      moved = -1;
+      continue;
+    }
+    // the bin's weights lie within 2^(-(b +- 1/2) / 8) of the maximum: scaled by 2^e they are at most 2^(1/16)
+    const int e = b / 8;
     uint32_t tk;
     int ti;
-    double need = ldexp(top_p * total - above, 33 + e);
-    if (!(need > 0.0)) need = 0.0;
-    s.template refine<true>(b, need, e, tk, ti);
+    if (!s.template refine<true>(b, fmax(ldexp(goal - above, 31 + e), 0.0), e, tk, ti)) {
+      if (moved >= 0 && b < SP_BINS - 2) {
+        ++b;
+        moved = 1;
+        continue;
+      }
+      // between two bins by the sums' last bits: all of this one stays
+      tk = sp_key(s.edge_low(b), KS);
+      ti = INT_MAX;
+    }
     // the part of bin b that stays
     const float zt = sp_value<KS>(tk), top = s.edge_high(b);
     for (int st = warp; st < nst; st += SP_WARPS) {
@@ -860,6 +852,7 @@ __global__ void __launch_bounds__(SP_THREADS) sample_kernel(SampleParams p, int 
     s.ci = s.cut && tk == s.ck ? min(ti, s.ci) : ti;
     s.ck = tk;
     s.cut = true;
+    break;
   }
   int kk[1] = {kept};
   s.block_sum(kk);                              // also orders the stretches' sums before their use
@@ -957,10 +950,13 @@ __global__ void __launch_bounds__(SP_THREADS) sample_kernel(SampleParams p, int 
 
 cudaError_t launch_sample(const SampleParams& p, cudaStream_t st) {
   const int es = p.bf16 ? 2 : 4, vn = 16 / es;
-  // the cluster: slices of at most `most` elements.  Few rows: short slices, for short passes, up to 16
-  // CTAs a row (more than 8 need the non-portable size) while all rows fit the GPU at once
+  // the cluster.  Few rows: short slices, for short passes, up to 16 CTAs a row (more than 8 need the
+  // non-portable size) while all rows fit the GPU at once.  Many rows: slices of up to 40960, two
+  // CTAs an SM, so that a search's barriers are paid by fewer CTAs
+  const bool many = p.n * 8 > 4 * num_sms();
+  const int most = many ? 40960 : 16384;
   int C = 1;
-  while (C < 8 && (p.V + C - 1) / C > 16384) C <<= 1;
+  while (C < 8 && (p.V + C - 1) / C > most) C <<= 1;
   if (C == 8 && p.n * 16 <= num_sms()) C = 16;
   const int unit = 32 * vn;
   const int per = ((p.V + C - 1) / C + unit - 1) / unit * unit;
