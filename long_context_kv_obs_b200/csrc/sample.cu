@@ -52,8 +52,8 @@ struct alignas(16) SpShared {                   // the slice follows: its vector
   };
   double table[64];                             // 2^(j / 64)
   double part[2];                               // beside a histogram: the mass of the slice, to fp32
-  unsigned long long xch[2][SP_MAXC][4];        // values of every CTA of the cluster, two steps deep
-  unsigned long long red[SP_WARPS][4];
+  unsigned long long xch[2][SP_MAXC][2];        // values of every CTA of the cluster, two steps deep
+  double red[SP_WARPS];
   double found[4];
   int ifound[2];
   int cand[SP_WARPS][2];
@@ -74,6 +74,29 @@ template <> struct SpVec<__nv_bfloat16> {
     }
     return u;
   }
+  __device__ __forceinline__ static float largest(uint4 u) {
+    const uint32_t* w = &u.x;
+    __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(w);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) x = __hmax2(x, *reinterpret_cast<const __nv_bfloat162*>(w + i));
+    return fmaxf(__low2float(x), __high2float(x));
+  }
+  // whether any element lies in [lo, hi]; the bounds as the nearest values inside, two to a word
+  struct Range {
+    __nv_bfloat162 lo, hi;
+    __device__ __forceinline__ Range(float l, float h)
+        : lo(__bfloat162bfloat162(__float2bfloat16_ru(l))), hi(__bfloat162bfloat162(__float2bfloat16_rd(h))) {}
+    __device__ __forceinline__ bool any(uint4 u) const {
+      const uint32_t* w = &u.x;
+      unsigned m = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(w + i);
+        m |= __hge2_mask(x, lo) & __hle2_mask(x, hi);
+      }
+      return m != 0;
+    }
+  };
 };
 template <> struct SpVec<float> {
   static constexpr int N = 4, KSHIFT = 0;
@@ -83,6 +106,20 @@ template <> struct SpVec<float> {
     for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(fmaxf(__uint_as_float(w[i]), -INFINITY) + 0.f);
     return u;
   }
+  __device__ __forceinline__ static float largest(uint4 u) {
+    return fmaxf(fmaxf(__uint_as_float(u.x), __uint_as_float(u.y)), fmaxf(__uint_as_float(u.z), __uint_as_float(u.w)));
+  }
+  struct Range {
+    float lo, hi;
+    __device__ __forceinline__ Range(float l, float h) : lo(l), hi(h) {}
+    __device__ __forceinline__ bool any(uint4 u) const {
+      const uint32_t* w = &u.x;
+      bool m = false;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m |= __uint_as_float(w[i]) >= lo && __uint_as_float(w[i]) <= hi;
+      return m;
+    }
+  };
 };
 
 __device__ __forceinline__ uint32_t sp_key(float z, int shift) { return f2key(z) >> shift; }
@@ -106,26 +143,150 @@ __device__ __forceinline__ uint4 sp_load(const T* row, int64_t i, int V) {
   return x.u;
 }
 
-// Sum of N values, pairwise.
-template <int N>
-__device__ __forceinline__ double sp_tree(const double (&v)[N]) {
-  double a[N];
+extern __shared__ __align__(16) uint8_t sp_raw[];   // SpShared, the slice, a double a stretch of it
+__device__ __forceinline__ SpShared& sp_sh() { return *reinterpret_cast<SpShared*>(sp_raw); }
+__device__ __forceinline__ uint4* sp_slice() { return reinterpret_cast<uint4*>(sp_raw + sizeof(SpShared)); }
+
+// Functions of several callers are kept out of line, and their state comes by value or from shared
+// memory: a row runs each pass a few times only, so code that is not there need not be fetched.
+__device__ __forceinline__ double sp_warp_scan(double inc) {   // inclusive
 #pragma unroll
-  for (int j = 0; j < N; ++j) a[j] = v[j];
+  for (int d = 1; d < 32; d <<= 1) {
+    const double y = __shfl_up_sync(FULL, inc, d);
+    if ((int)(threadIdx.x & 31) >= d) inc += y;
+  }
+  return inc;
+}
+__device__ __forceinline__ int sp_warp_scan(int inc) {
 #pragma unroll
-  for (int h = N / 2; h > 0; h >>= 1)
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(FULL, inc, d);
+    if ((int)(threadIdx.x & 31) >= d) inc += y;
+  }
+  return inc;
+}
+// Sum over the CTA, in a fixed order, known to every thread.
+__device__ __noinline__ double sp_block_sum(double v) {
+  SpShared& sh = sp_sh();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  v = warp_sum_d(v);
+  __syncthreads();
+  if (lane == 0) sh.red[warp] = v;
+  __syncthreads();
+  v = sh.red[lane & (SP_WARPS - 1)];
 #pragma unroll
-    for (int j = 0; j < h; ++j) a[j] = a[2 * j] + a[2 * j + 1];
-  return a[0];
+  for (int o = SP_WARPS / 2; o > 0; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
+  return v;
+}
+// Sum of the threads before (x) and of the CTA (y).
+__device__ __noinline__ double2 sp_block_scan(double mine) {
+  SpShared& sh = sp_sh();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const double inc = sp_warp_scan(mine);
+  __syncthreads();
+  if (lane == 31) sh.red[warp] = inc;
+  __syncthreads();
+  const double x = sh.red[lane & (SP_WARPS - 1)];
+  double b = (lane & (SP_WARPS - 1)) < warp ? x : 0.0, t = x;
+#pragma unroll
+  for (int o = SP_WARPS / 2; o > 0; o >>= 1) {
+    b += __shfl_xor_sync(FULL, b, o);
+    t += __shfl_xor_sync(FULL, t, o);
+  }
+  return make_double2(b + inc - mine, t);
+}
+// Two values of every CTA (known to all its threads) to all: each CTA writes its own into every other's
+// shared memory (a store does not wait), and after the cluster barrier the reads are local.  A slot
+// is written again two exchanges later: by then its reader has passed the barrier between.
+__device__ __noinline__ void sp_exchange(int C, int rank, int slot, unsigned long long a, unsigned long long b) {
+  cg::cluster_group cl = cg::this_cluster();
+  if ((int)threadIdx.x < C) {
+    unsigned long long* o = cl.map_shared_rank(&sp_sh().xch[slot][rank][0], threadIdx.x);
+    o[0] = a;
+    o[1] = b;
+  }
+  cl.sync();
+}
+// The weight of logit z: 2^((z - zmax) c), for z within 2^-64 of the largest.
+__device__ __forceinline__ double sp_raw_weight(float z, float zmax, double c) {
+  const double t = ((double)z - (double)zmax) * c;
+  const double magic = 6755399441055744.0 / 64;   // 1.5 * 2^52 / 64: rounds t to a multiple of 1/64
+  const double r = t + magic;
+  const int k = __double2loint(r);
+  const double f = t - (r - magic);
+  // exp(f ln 2) = 1 + f ln2 + (f ln2)^2 / 2 + (f ln2)^3 / 6 + (f ln2)^4 / 24
+  double p = fma(f, 9.618129107628477e-3, 5.550410866482158e-2);
+  p = fma(f, p, 2.402265069591007e-1);
+  p = fma(f, p, 6.931471805599453e-1);
+  p = fma(f, p, 1.0);
+  p *= sp_sh().table[k & 63];
+  return __hiloint2double(__double2hiint(p) + ((k >> 6) << 20), __double2loint(p));
+}
+// The same times 2^e, 0 below zlow.
+__device__ __noinline__ double sp_weight(float z, float zmax, float zlow, double c, int e) {
+  if (!(z >= zlow)) return 0.0;
+  const double w = sp_raw_weight(z, zmax, c);
+  return __hiloint2double(__double2hiint(w) + (e << 20), __double2loint(w));
+}
+
+enum { SP_COUNT, SP_SHARE, SP_LIMBS, SP_KEYS };
+// The first bin at which the sum over the cluster's histograms reaches `target` (SHARE: that share of
+// the cluster's `part`), or the last that holds something: returned, with the sum before it in
+// found[0] and the bin's own value in found[1].  What a word of bin i stands for: COUNT, 1; SHARE, 2^-15
+// of the weight at the bin's middle; LIMBS, 1, and a word of the histogram's second half 2^16; KEYS,
+// the weight of key first - i in 2^-(31 + e) units.  Every CTA reads all histograms (a thread one bin,
+// its loads all in flight) and scans them for itself: one cluster barrier a search.  The next search
+// uses the other buffer, so a slow reader is not overtaken.
+template <int KS>
+__device__ __noinline__ int sp_border(int kind, double target, int C, int rank, int buf, uint32_t first, int e, float zmax,
+                                      float zlow, double c) {
+  static_assert(SP_BINS == SP_THREADS, "a bin a thread");
+  cg::cluster_group cl = cg::this_cluster();
+  SpShared& sh = sp_sh();
+  cl.sync();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  unsigned long long h = 0;
+  if (kind == SP_LIMBS) {
+#pragma unroll
+    for (int r = 0; r < SP_MAXC; ++r)
+      if (r < C)
+        h += (unsigned long long)cl.map_shared_rank(&sh.hist[buf][SP_BINS], (rank + r) & (C - 1))[threadIdx.x] << 16;
+  }
+#pragma unroll
+  for (int r = 0; r < SP_MAXC; ++r)             // each CTA begins with its own: no one is asked by all at once
+    if (r < C) h += cl.map_shared_rank(&sh.hist[buf][0], (rank + r) & (C - 1))[threadIdx.x];
+  if (kind == SP_SHARE && warp == 0) {
+    double m = lane < C ? *cl.map_shared_rank(&sh.part[buf], lane) : 0.0;
+    m = warp_sum_d(m);
+    if (lane == 0) sh.found[3] = target * m;
+  }
+  double v = (double)h;
+  if (kind == SP_SHARE) v *= (double)(tc::ex2((float)threadIdx.x * (-1.f / 8.f)) * 0x1p-15f);
+  if (kind == SP_KEYS && h) v *= sp_weight(sp_value<KS>(first - threadIdx.x), zmax, zlow, c, 31 + e);
+  const double2 sc = sp_block_scan(v);
+  const double inc = sc.x + v;
+  if (kind == SP_SHARE) target = sh.found[3];
+  const unsigned some = __ballot_sync(FULL, v > 0.0);
+  const unsigned hit = __ballot_sync(FULL, v > 0.0 && inc >= target);
+  if (lane == 0) {
+    sh.cand[warp][0] = hit ? warp * 32 + __ffs(hit) - 1 : INT_MAX;
+    sh.cand[warp][1] = some ? warp * 32 + 31 - __clz(some) : -1;
+  }
+  __syncthreads();
+  const int at = __reduce_min_sync(FULL, sh.cand[lane & (SP_WARPS - 1)][0]);
+  const int end = __reduce_max_sync(FULL, sh.cand[lane & (SP_WARPS - 1)][1]);
+  const int b = at == INT_MAX ? max(end, 0) : at;
+  if ((int)threadIdx.x == b) {
+    sh.found[0] = sc.x;
+    sh.found[1] = v;
+  }
+  __syncthreads();
+  return b;
 }
 
 template <typename T>
 struct SpRow {
   static constexpr int N = SpVec<T>::N, KS = SpVec<T>::KSHIFT;
-  cg::cluster_group cl;
-  SpShared& sh;
-  uint4* slice;                                 // this CTA's vectors; thread t owns t, t + SP_THREADS, ...
-  double* wsum;                                 // kept mass of every 32-vector stretch
   int C, rank, nvec, i0;                        // cluster size, rank, vectors of the slice, its first index
   int step, search;
   float zmax, ybin;                             // bins below the maximum: (zmax - z) * ybin
@@ -135,73 +296,54 @@ struct SpRow {
   uint32_t ck;
   int ci;
 
-  __device__ __forceinline__ SpRow(SpShared& s) : cl(cg::this_cluster()), sh(s) {}
-
-  // The values v of every CTA, which all its threads know: each CTA writes its own into every other's
-  // shared memory (a store does not wait), and after the cluster barrier the reads are local.  A slot
-  // is written again two steps later: by then its reader has passed the barrier between.
-  template <int K, typename F>
-  __device__ __forceinline__ void exchange(const unsigned long long (&v)[K], F&& use) {
-    if ((int)threadIdx.x < C) {
-      unsigned long long* o = cl.map_shared_rank(&sh.xch[step & 1][rank][0], threadIdx.x);
-#pragma unroll
-      for (int k = 0; k < K; ++k) o[k] = v[k];
-    }
-    cl.sync();
-    for (int r = 0; r < C; ++r) {
-      unsigned long long w[K];
-#pragma unroll
-      for (int k = 0; k < K; ++k) w[k] = sh.xch[step & 1][r][k];
-      use(r, w);
-    }
+  __device__ __forceinline__ void exchange(unsigned long long a, unsigned long long b) {
+    sp_exchange(C, rank, step & 1, a, b);
     ++step;
   }
-  // Sums over the CTA, in a fixed order, known to every thread.
-  template <int K, typename V>
-  __device__ __forceinline__ void block_sum(V (&v)[K]) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(FULL, v[k], o);
+  __device__ __forceinline__ void exchange(double a, double b) {
+    exchange((unsigned long long)__double_as_longlong(a), (unsigned long long)__double_as_longlong(b));
+  }
+  __device__ __forceinline__ unsigned long long got(int r, int k) const { return sp_sh().xch[(step - 1) & 1][r][k]; }
+  __device__ __forceinline__ double got_d(int r, int k) const { return __longlong_as_double((long long)got(r, k)); }
+  // The sum of a value of every CTA, in their order; `before` the sum of the lower ranks'.
+  __device__ __forceinline__ double cluster_sum(double x, double& before) {
+    exchange(x, 0.0);
+    double all = 0.0;
+    before = 0.0;
+#pragma unroll 1
+    for (int r = 0; r < C; ++r) {
+      if (r == rank) before = all;
+      all += got_d(r, 0);
     }
-    __syncthreads();
-    if (lane == 0) {
-#pragma unroll
-      for (int k = 0; k < K; ++k) *reinterpret_cast<V*>(&sh.red[warp][k]) = v[k];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      V s = *reinterpret_cast<V*>(&sh.red[lane & (SP_WARPS - 1)][k]);
-#pragma unroll
-      for (int o = SP_WARPS / 2; o > 0; o >>= 1) s += __shfl_xor_sync(FULL, s, o);
-      v[k] = s;
+    return all;
+  }
+  __device__ __forceinline__ int border(int kind, double target, uint32_t first, int e) {
+    const int b = sp_border<KS>(kind, target, C, rank, search & 1, first, e, zmax, zlow, c);
+    ++search;
+    return b;
+  }
+  __device__ __forceinline__ double weight(float z, int e = 0) const { return sp_weight(z, zmax, zlow, c, e); }
+
+  // use(value, index) for the elements of vector v, in order, U of its four words at a time.
+  template <int U, typename F>
+  __device__ __forceinline__ void each(int v, F&& use) const {
+#pragma unroll U
+    for (int w = 0; w < 4; ++w) {
+      const uint32_t x = reinterpret_cast<const uint32_t*>(sp_slice() + v)[w];
+      const int idx = i0 + v * N + w * (N / 4);
+      if (N == 8) {
+        use(bf_lo(x), idx);
+        use(bf_hi(x), idx + 1);
+      } else {
+        use(__uint_as_float(x), idx);
+      }
     }
   }
-
-  __device__ __forceinline__ void unpack(int v, float (&z)[N]) const { Vec<T>::unpack(slice[v], z); }
   // Monotone in z; the maximum is in bin 0, the last bin holds all that is farther.
   __device__ __forceinline__ int bin(float z) const {
     const float r = fmaf(zmax - z, ybin, SP_ONE);
     return min(__float_as_int(r) - 0x4B000000, SP_BINS - 1);
   }
-  // For z >= zlow: weights of the others are nothing.
-  __device__ __forceinline__ double raw_weight(float z) const {
-    const double t = ((double)z - (double)zmax) * c;
-    const double magic = 6755399441055744.0 / 64;   // 1.5 * 2^52 / 64: rounds t to a multiple of 1/64
-    const double r = t + magic;
-    const int k = __double2loint(r);
-    const double f = t - (r - magic);
-    // exp(f ln 2) = 1 + f ln2 + (f ln2)^2 / 2 + (f ln2)^3 / 6 + (f ln2)^4 / 24
-    double p = fma(f, 9.618129107628477e-3, 5.550410866482158e-2);
-    p = fma(f, p, 2.402265069591007e-1);
-    p = fma(f, p, 6.931471805599453e-1);
-    p = fma(f, p, 1.0);
-    p *= sh.table[k & 63];
-    return __hiloint2double(__double2hiint(p) + ((k >> 6) << 20), __double2loint(p));
-  }
-  __device__ __forceinline__ double weight(float z) const { return z >= zlow ? raw_weight(z) : 0.0; }
   __device__ __forceinline__ bool left(float z, int idx) const {
     if (!cut) return z > -INFINITY;
     const uint32_t key = sp_key(z, KS);
@@ -221,122 +363,54 @@ struct SpRow {
 
   // The histogram of this search, cleared for use (its words are used again two searches on).
   __device__ __forceinline__ unsigned* clear_hist(int words) {
-    unsigned* h = sh.hist[search & 1];
+    unsigned* h = sp_sh().hist[search & 1];
+#pragma unroll 1
     for (int j = threadIdx.x; j < words / 4; j += SP_THREADS) reinterpret_cast<uint4*>(h)[j] = make_uint4(0, 0, 0, 0);
     __syncthreads();
     return h;
   }
-  // The first bin at which the sum over the cluster's histograms reaches `target` (frac > 0: that
-  // share of the cluster's `part`), or the last that holds something; the sum before it and the bin's
-  // own value.  A bin's value is val(bin, words summed over the cluster); LIMBS: the histogram has a
-  // second half, 2^16 times the first's unit.  Every CTA reads all histograms (a thread one bin, its
-  // loads all in flight) and scans them for itself: one cluster barrier a search.  The next search
-  // uses the other buffer, so a slow reader is not overtaken.
-  template <bool LIMBS, typename F>
-  __device__ __forceinline__ void border(double frac, double target, F&& val, int& b, double& above, double& value) {
-    static_assert(SP_BINS == SP_THREADS, "a bin a thread");
-    cl.sync();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    unsigned long long h = 0;
-#pragma unroll 8
-    for (int r = 0; r < C; ++r) {
-      const unsigned* o = cl.map_shared_rank(&sh.hist[search & 1][0], r);
-      h += o[threadIdx.x];
-      if (LIMBS) h += (unsigned long long)o[SP_BINS + threadIdx.x] << 16;
-    }
-    if (frac > 0.0 && warp == 0) {
-      double m = lane < C ? *cl.map_shared_rank(&sh.part[search & 1], lane) : 0.0;
-      m = warp_sum_d(m);
-      if (lane == 0) sh.found[3] = frac * m;
-    }
-    ++search;
-    const double v = h ? val((int)threadIdx.x, (double)h) : 0.0;
-    double inc = v;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const double y = __shfl_up_sync(FULL, inc, d);
-      if (lane >= d) inc += y;
-    }
-    if (lane == 31) *reinterpret_cast<double*>(&sh.red[warp][0]) = inc;
-    __syncthreads();
-    if (frac > 0.0) target = sh.found[3];
-    // sum of the warps before (lanes 0 .. 15 hold the warps' sums)
-    double before = (lane & (SP_WARPS - 1)) < warp ? *reinterpret_cast<double*>(&sh.red[lane & (SP_WARPS - 1)][0]) : 0.0;
-#pragma unroll
-    for (int o = SP_WARPS / 2; o > 0; o >>= 1) before += __shfl_xor_sync(FULL, before, o);
-    const unsigned some = __ballot_sync(FULL, v > 0.0);
-    const unsigned hit = __ballot_sync(FULL, v > 0.0 && before + inc >= target);
-    if (lane == 0) {
-      sh.cand[warp][0] = hit ? warp * 32 + __ffs(hit) - 1 : INT_MAX;
-      sh.cand[warp][1] = some ? warp * 32 + 31 - __clz(some) : -1;
-    }
-    __syncthreads();
-    const int at = __reduce_min_sync(FULL, sh.cand[lane & (SP_WARPS - 1)][0]);
-    const int end = __reduce_max_sync(FULL, sh.cand[lane & (SP_WARPS - 1)][1]);
-    b = at == INT_MAX ? max(end, 0) : at;
-    if ((int)threadIdx.x == b) {
-      sh.found[0] = before + inc - v;
-      sh.found[1] = v;
-    }
-    __syncthreads();
-    above = sh.found[0];
-    value = sh.found[1];
-  }
 
-  // use(value, index) for every element of the slice with lo <= value <= hi; they are few
+  // use(value, index) for every element of the slice with lo <= value <= hi: two instructions an
+  // element where there are none
   template <typename F>
   __device__ __forceinline__ void in_range(float lo, float hi, F&& use) {
-    for (int v = threadIdx.x; v < nvec; v += SP_THREADS) {
-      float z[N];
-      unpack(v, z);
-      unsigned in = 0;
-#pragma unroll
-      for (int j = 0; j < N; ++j) in |= (z[j] >= lo && z[j] <= hi ? 1u : 0u) << j;
-      while (in) {
-        const int j = __ffs(in) - 1;
-        in &= in - 1;
-        use((float)reinterpret_cast<const T*>(slice + v)[j], i0 + v * N + j);
-      }
-    }
+    const typename SpVec<T>::Range range(lo, hi);
+#pragma unroll 1
+    for (int v = threadIdx.x; v < nvec; v += SP_THREADS)
+      if (range.any(sp_slice()[v]))
+        each<1>(v, [&](float z, int idx) {
+          if (z >= lo && z <= hi) use(z, idx);
+        });
   }
 
-  // Within bin b0 (of the tokens left by top-k), the key at which the count (MASS: the mass, in units
+  // Within bin b0 (of the tokens left by top-k), the key at which the count (mass: the mass, in units
   // of 2^-(31 + e)) reaches `need`, and the index of the last tie that stays.  False if the bin holds
   // less than that (then nothing else is set).
-  template <bool MASS>
-  __device__ __forceinline__ bool refine(int b0, double need, int e, uint32_t& tkey, int& tidx) {
+  __device__ __forceinline__ bool refine(bool mass, int b0, double need, int e, uint32_t& tkey, int& tidx) {
+    SpShared& sh = sp_sh();
     uint32_t hi = sp_key(edge_high(b0), KS), lo = max(sp_key(edge_low(b0), KS), sp_key(-INFINITY, KS) + 1u);
     double above = 0.0, value = 0.0;
     bool first_search = true;
     int shift = 0;
     while (((hi - lo) >> shift) >= SP_BINS) ++shift;
     while (true) {
-      const bool limbs = MASS && shift > 0;
+      const bool limbs = mass && shift > 0;
       unsigned* hist = clear_hist(limbs ? 2 * SP_BINS : SP_BINS);
       in_range(sp_value<KS>(lo), sp_value<KS>(hi), [&](float z, int idx) {
         if (bin(z) != b0 || !left(z, idx)) return;
         const uint32_t hb = (hi - sp_key(z, KS)) >> shift;
         if (limbs) {
-          const unsigned long long q = (unsigned long long)__double2ll_rn(scalbn(weight(z), 31 + e));
+          const unsigned long long q = (unsigned long long)__double2ll_rn(weight(z, 31 + e));
           atomicAdd(hist + hb, (unsigned)(q & 0xffffu));
           atomicAdd(hist + SP_BINS + hb, (unsigned)(q >> 16));
         } else {
           atomicAdd(hist + hb, 1u);
         }
       });
-      int hb;
-      double ab;
-      if (limbs) {
-        border<true>(0.0, need - above, [](int, double n) { return n; }, hb, ab, value);
-      } else if (MASS) {                        // a bin is one key: its weight times its count
-        const uint32_t first = hi;
-        border<false>(0.0, need - above,
-                      [&](int i, double n) { return n * scalbn(weight(sp_value<KS>(first - (uint32_t)i)), 31 + e); }, hb, ab,
-                      value);
-      } else {
-        border<false>(0.0, need - above, [](int, double n) { return n; }, hb, ab, value);
-      }
-      if (MASS && first_search && ab + value < need) return false;
+      const int hb = border(limbs ? SP_LIMBS : mass ? SP_KEYS : SP_COUNT, need - above, hi, e);
+      const double ab = sh.found[0];
+      value = sh.found[1];
+      if (mass && first_search && ab + value < need) return false;
       first_search = false;
       above += ab;
       const uint32_t top = hi - ((uint32_t)hb << shift);
@@ -350,8 +424,8 @@ struct SpRow {
     tkey = hi;
     // of the ties of tkey the first `take` in index order stay; `value` tells how many there are
     double take = need - above, ties = value;
-    if (MASS) {
-      const double w = scalbn(weight(sp_value<KS>(tkey)), 31 + e);
+    if (mass) {
+      const double w = weight(sp_value<KS>(tkey), 31 + e);
       take = w > 0.0 ? ceil(take / w) : 1.0;
       ties = w > 0.0 ? rint(value / w) : 1.0;
     }
@@ -362,39 +436,29 @@ struct SpRow {
     const int lane = threadIdx.x & 31, nst = (nvec + 31) / 32;
     const float zt = sp_value<KS>(tkey);
     unsigned* count = sh.hist[search & 1];
-    int mine[1] = {0};
+    double mine = 0.0;
+    const typename SpVec<T>::Range range(zt, zt);
+#pragma unroll 1
     for (int v0 = threadIdx.x - lane; v0 < nvec; v0 += SP_THREADS) {
       const int v = v0 + lane;
       int n = 0;
-      if (v < nvec) {
-        float z[N];
-        unpack(v, z);
-#pragma unroll
-        for (int j = 0; j < N; ++j) n += z[j] == zt && left(z[j], i0 + v * N + j);
-      }
+      if (v < nvec && range.any(sp_slice()[v])) each<1>(v, [&](float z, int idx) { n += z == zt && left(z, idx); });
       n = __reduce_add_sync(FULL, n);
       if (lane == 0) {
         count[v0 >> 5] = (unsigned)n;
-        mine[0] += n;
+        mine += n;
       }
     }
-    block_sum<1>(mine);
-    double before = 0.0;
-    {
-      unsigned long long x[1] = {(unsigned long long)mine[0]};
-      exchange<1>(x, [&](int r, unsigned long long (&w)[1]) { before += r < rank ? (double)w[0] : 0.0; });
-    }
-    const bool here = before < take && take <= before + (double)mine[0];
+    mine = sp_block_sum(mine);
+    double before;
+    cluster_sum(mine, before);
+    const bool here = before < take && take <= before + mine;
     if (here && threadIdx.x < 32) {             // this slice holds the last tie that stays
       int want = (int)(take - before), st = 0;
+#pragma unroll 1
       for (int s0 = 0; s0 < nst; s0 += 32) {
         const int n = s0 + lane < nst ? (int)count[s0 + lane] : 0;
-        int inc = n;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const int y = __shfl_up_sync(FULL, inc, d);
-          if (lane >= d) inc += y;
-        }
+        const int inc = sp_warp_scan(n);
         const unsigned hit = __ballot_sync(FULL, inc >= want);
         if (hit) {
           st = s0 + __ffs(hit) - 1;
@@ -404,40 +468,26 @@ struct SpRow {
         want -= __shfl_sync(FULL, inc, 31);
       }
       const int v = st * 32 + lane;
-      unsigned in = 0;
-      if (v < nvec) {
-        float z[N];
-        unpack(v, z);
-#pragma unroll
-        for (int j = 0; j < N; ++j) in |= (z[j] == zt && left(z[j], i0 + v * N + j) ? 1u : 0u) << j;
-      }
-      int inc = __popc(in);
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int y = __shfl_up_sync(FULL, inc, d);
-        if (lane >= d) inc += y;
-      }
-      int k = inc - __popc(in);
-      while (in) {
-        const int j = __ffs(in) - 1;
-        in &= in - 1;
-        if (++k == want) sh.ifound[1] = i0 + v * N + j;
-      }
+      int n = 0;
+      if (v < nvec) each<1>(v, [&](float z, int idx) { n += z == zt && left(z, idx); });
+      int k = sp_warp_scan(n) - n;
+      if (k < want && want <= k + n)
+        each<1>(v, [&](float z, int idx) {
+          if (z == zt && left(z, idx) && ++k == want) sh.ifound[1] = idx;
+        });
     }
     __syncthreads();
-    unsigned long long y[1] = {(unsigned long long)(here ? sh.ifound[1] + 1 : 0)};
-    int at = 0;
-    exchange<1>(y, [&](int, unsigned long long (&w)[1]) { at = max(at, (int)w[0]); });
-    tidx = at - 1;
+    tidx = (int)cluster_sum(here ? (double)sh.ifound[1] : 0.0, before);   // one CTA's
     return true;
   }
 };
 
 // a[0, n) sorted downwards, n a power of two (bitonic merges).
-__device__ __forceinline__ void sp_sort(unsigned long long* a, int n) {
+__device__ __noinline__ void sp_sort(unsigned long long* a, int n) {
   for (int k = 2; k <= n; k <<= 1)
     for (int j = k >> 1; j > 0; j >>= 1) {
       __syncthreads();
+#pragma unroll 1
       for (int p = threadIdx.x; p < n / 2; p += SP_THREADS) {
         const int i = 2 * p - (p & (j - 1)), q = i + j;
         const unsigned long long x = a[i], y = a[q];
@@ -454,16 +504,15 @@ template <typename T, bool ALIGNED>
 __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, int per_cta) {
   constexpr int N = SpVec<T>::N, KS = SpVec<T>::KSHIFT;
   static_assert(sizeof(SpShared) % 16 == 0, "vectors follow");
-  extern __shared__ __align__(16) uint8_t sp_raw[];
-  SpShared& sh = *reinterpret_cast<SpShared*>(sp_raw);
-  uint4* slice = reinterpret_cast<uint4*>(sp_raw + sizeof(SpShared));
-  SpRow<T> s(sh);
-  s.cl.barrier_arrive();                        // every CTA of the cluster runs before its shared memory is written
-  s.C = (int)s.cl.num_blocks();
-  s.rank = (int)s.cl.block_rank();
+  SpShared& sh = sp_sh();
+  uint4* slice = sp_slice();
+  double* wsum = reinterpret_cast<double*>(slice + per_cta / N);   // kept mass of every 32-vector stretch
+  cg::cluster_group cl = cg::this_cluster();
+  SpRow<T> s;
+  cl.barrier_arrive();                          // every CTA of the cluster runs before its shared memory is written
+  s.C = (int)cl.num_blocks();
+  s.rank = (int)cl.block_rank();
   const int row = blockIdx.x / s.C, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  s.slice = slice;
-  s.wsum = reinterpret_cast<double*>(slice + per_cta / N);
   s.i0 = s.rank * per_cta;
   s.nvec = max(0, min(per_cta, p.V - s.i0) + N - 1) / N;
   s.step = s.search = 0;
@@ -472,14 +521,11 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
 
   // A: the slice into shared memory and the maximum
   float best = -INFINITY;
-#pragma unroll 4
+#pragma unroll 2
   for (int v = tid; v < s.nvec; v += SP_THREADS) {
     const uint4 u = SpVec<T>::clean(sp_load<T, ALIGNED>(z0, s.i0 + (int64_t)v * N, p.V));
     slice[v] = u;
-    float z[N];
-    Vec<T>::unpack(u, z);
-#pragma unroll
-    for (int j = 0; j < N; ++j) best = fmaxf(best, z[j]);
+    best = fmaxf(best, SpVec<T>::largest(u));
   }
   if (tid < 64) sh.table[tid] = exp2((double)tid / 64.0);
   const float T_ = p.temperature ? p.temperature[row] : 1.f;
@@ -487,15 +533,15 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
   const float pf = p.top_p ? p.top_p[row] : 1.f, mf = p.min_p ? p.min_p[row] : 0.f;
   {
     const float m = warp_max(best);
-    if (lane == 0) sh.red[warp][0] = f2key(m);
+    if (lane == 0) sh.red[warp] = (double)m;
     __syncthreads();
-    unsigned long long x[1] = {0};
-#pragma unroll
-    for (int w = 0; w < SP_WARPS; ++w) x[0] = max(x[0], sh.red[w][0]);
-    s.cl.barrier_wait();
-    unsigned long long top = 0;
-    s.exchange(x, [&](int, unsigned long long (&w)[1]) { top = max(top, w[0]); });
-    s.zmax = key2f((uint32_t)top);
+    double x = sh.red[lane & (SP_WARPS - 1)];
+    x = (double)warp_max((float)x);
+    cl.barrier_wait();
+    s.exchange(x, 0.0);
+    s.zmax = -INFINITY;
+#pragma unroll 1
+    for (int r = 0; r < s.C; ++r) s.zmax = fmaxf(s.zmax, (float)s.got_d(r, 0));
   }
   if (s.zmax == -INFINITY || !(T_ > 0.f)) {
     // nothing to take, or the first token of the order
@@ -504,13 +550,13 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
       s.in_range(s.zmax, s.zmax, [&](float, int idx) { at = min(at, idx); });
     at = __reduce_min_sync(FULL, at);
     __syncthreads();
-    if (lane == 0) sh.red[warp][0] = (unsigned long long)at;
+    if (lane == 0) sh.cand[warp][0] = at;
     __syncthreads();
-    unsigned long long x[1] = {INT_MAX};
-#pragma unroll
-    for (int w = 0; w < SP_WARPS; ++w) x[0] = min(x[0], sh.red[w][0]);
+    at = __reduce_min_sync(FULL, sh.cand[lane & (SP_WARPS - 1)][0]);
+    s.exchange((unsigned long long)at, 0ull);
     unsigned long long first = INT_MAX;
-    s.exchange(x, [&](int, unsigned long long (&w)[1]) { first = min(first, w[0]); });
+#pragma unroll 1
+    for (int r = 0; r < s.C; ++r) first = min(first, s.got(r, 0));
     if (s.rank == 0 && tid == 0) {
       const bool any = s.zmax > -INFINITY;
       p.token[row] = any ? (int)first : -1;
@@ -521,9 +567,10 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
   }
   if (s.zmax == INFINITY) {
     // infinite logits share the mass: they become 0, all others -infinity
+#pragma unroll 1
     for (int v = tid; v < s.nvec; v += SP_THREADS) {
       T* e = reinterpret_cast<T*>(slice + v);
-#pragma unroll
+#pragma unroll 1
       for (int j = 0; j < N; ++j) e[j] = (float)e[j] == INFINITY ? T(0.f) : T(-INFINITY);
     }
     best = best == INFINITY ? 0.f : -INFINITY;
@@ -547,110 +594,76 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
   u = u > 0.f ? fminf(u, 1.f - 0x1p-24f) : 0.f;   // NaN and negatives: 0
 
   if (k > 0 && k < p.V) {
-    double above, value;
-    auto number = [](int, double n) { return n; };
     if (k <= s.C * (SP_THREADS / 4)) {
       // B: a bin that the k-th largest cannot lie beyond, from the threads' own maxima
       unsigned* hist = s.clear_hist(SP_BINS);
       if (best > -INFINITY) atomicAdd(hist + s.bin(best), 1u);
-      int far;
-      s.template border<false>(0.0, (double)k, number, far, above, value);
-      const float low = above + value >= (double)k ? s.edge_low(far) : -INFINITY;
+      const int far = s.border(SP_COUNT, (double)k, 0, 0);
+      const float low = sh.found[0] + sh.found[1] >= (double)k ? s.edge_low(far) : -INFINITY;
       const float floor_ = fmaxf(low, -3.4028234663852886e38f);   // never -infinity itself
       // what reaches it, first counted
-      int n[1] = {0};
-      s.in_range(floor_, INFINITY, [&](float, int) { ++n[0]; });
-      s.block_sum(n);
-      unsigned long long x[1] = {(unsigned long long)n[0]};
-      int off = 0, m = 0;
-      s.exchange(x, [&](int r, unsigned long long (&w)[1]) {
-        off += r < s.rank ? (int)w[0] : 0;
-        m += (int)w[0];
-      });
+      double n = 0.0, off;
+      s.in_range(floor_, INFINITY, [&](float, int) { n += 1.0; });
+      n = sp_block_sum(n);
+      const int m = (int)s.cluster_sum(n, off);
       if (m <= SP_LIST) {
         // the candidates, to the first CTA (its histograms are read no more: all have passed the exchange)
-        if (tid == 0) sh.nlist = off;
+        if (tid == 0) sh.nlist = (int)off;
         __syncthreads();
-        unsigned long long* list = s.cl.map_shared_rank(&sh.list[0], 0);
+        unsigned long long* list = cl.map_shared_rank(&sh.list[0], 0);
         s.in_range(floor_, INFINITY, [&](float z, int idx) {
           list[atomicAdd(&sh.nlist, 1)] = ((unsigned long long)f2key(z) << 32) | (unsigned)~idx;
         });
-        s.cl.sync();
+        cl.sync();
         if (s.rank != 0) return;                // the rest is the first CTA's own
         int np = 2;
         while (np < m) np <<= 1;
+#pragma unroll 1
         for (int i = m + tid; i < np; i += SP_THREADS) sh.list[i] = 0ull;
         sp_sort(sh.list, np);
         const int kk = min(k, m);
-        // weights in the order, eight a thread, and their running sum
-        constexpr int Q = SP_LIST / SP_THREADS;
-        double w[Q], sum = 0.0;
-#pragma unroll
-        for (int j = 0; j < Q; ++j) {
-          const int i = tid * Q + j;
-          w[j] = i < kk ? s.weight(key2f((uint32_t)(sh.list[i] >> 32))) : 0.0;
-          sum += w[j];
+        // weights in the order, a stretch a thread, and their running sum
+        const int Q = (np + SP_THREADS - 1) / SP_THREADS;
+        auto value = [&](int i) { return key2f((uint32_t)(sh.list[i] >> 32)); };
+        double sum = 0.0, nkeep = 0.0;
+#pragma unroll 1
+        for (int i = tid * Q; i < min(kk, tid * Q + Q); ++i) sum += s.weight(value(i));
+        double2 sc = sp_block_scan(sum);
+        double run = sc.x;
+#pragma unroll 1
+        for (int i = tid * Q; i < min(kk, tid * Q + Q); ++i) {
+          // kept: a head of the order, both conditions only turn false
+          nkeep += i == 0 || ((!use_p || run < top_p * sc.y) && value(i) >= zcut);
+          run += s.weight(value(i));
         }
-        auto scan = [&](double mine, double& total) {   // sum of the threads before
-          double inc = mine;
-#pragma unroll
-          for (int d = 1; d < 32; d <<= 1) {
-            const double y = __shfl_up_sync(FULL, inc, d);
-            if (lane >= d) inc += y;
-          }
-          __syncthreads();
-          if (lane == 31) *reinterpret_cast<double*>(&sh.red[warp][0]) = inc;
-          __syncthreads();
-          double b = 0.0;
-          total = 0.0;
-#pragma unroll
-          for (int q = 0; q < SP_WARPS; ++q) {
-            const double y = *reinterpret_cast<double*>(&sh.red[q][0]);
-            b += q < warp ? y : 0.0;
-            total += y;
-          }
-          return b + inc - mine;
-        };
-        double total;
-        double run = scan(sum, total);
-        int keep[1] = {0};
-#pragma unroll
-        for (int j = 0; j < Q; ++j) {
-          const int i = tid * Q + j;
-          if (i < kk) {
-            const bool in = i == 0 || ((!use_p || run < top_p * total) && key2f((uint32_t)(sh.list[i] >> 32)) >= zcut);
-            keep[0] += in;                      // a head of the order: both conditions only turn false
-          }
-          run += w[j];
-        }
-        s.block_sum(keep);
+        const int keep = (int)sp_block_sum(nkeep);
         // the kept ones in index order
         int nk = 2;
-        while (nk < keep[0]) nk <<= 1;
+        while (nk < keep) nk <<= 1;
+#pragma unroll 1
         for (int i = tid; i < nk; i += SP_THREADS) {
           const unsigned long long x = sh.list[i];
           // sorted downwards: index up is ~index down; what is cut sinks
-          sh.list[i] = i < keep[0] ? (x << 32) | (x >> 32) : 0ull;
+          sh.list[i] = i < keep ? (x << 32) | (x >> 32) : 0ull;
         }
         sp_sort(sh.list, nk);
         sum = 0.0;
-#pragma unroll
-        for (int j = 0; j < Q; ++j) {
-          const int i = tid * Q + j;
-          w[j] = i < keep[0] ? s.weight(key2f((uint32_t)sh.list[i])) : 0.0;
-          sum += w[j];
-        }
-        run = scan(sum, total);
-        const double goal = (double)u * total;
+        const int Qk = (nk + SP_THREADS - 1) / SP_THREADS;
+#pragma unroll 1
+        for (int i = tid * Qk; i < min(keep, tid * Qk + Qk); ++i) sum += s.weight(key2f((uint32_t)sh.list[i]));
+        sc = sp_block_scan(sum);
+        run = sc.x;
+        const double goal = (double)u * sc.y;
         // the first whose running sum passes the goal (else, by rounding, the last with mass)
         int at = INT_MAX, last = -1;
-#pragma unroll
-        for (int j = 0; j < Q; ++j) {
-          if (w[j] > 0.0) {
-            last = tid * Q + j;
-            if (at == INT_MAX && run + w[j] > goal) at = last;
+#pragma unroll 1
+        for (int i = tid * Qk; i < min(keep, tid * Qk + Qk); ++i) {
+          const double w = s.weight(key2f((uint32_t)sh.list[i]));
+          if (w > 0.0) {
+            last = i;
+            if (at == INT_MAX && run + w > goal) at = i;
           }
-          run += w[j];
+          run += w;
         }
         at = __reduce_min_sync(FULL, at);
         last = __reduce_max_sync(FULL, last);
@@ -666,42 +679,38 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
           }
           const unsigned long long x = sh.list[at == INT_MAX ? last : at];
           p.token[row] = (int)~(unsigned)(x >> 32);
-          if (p.logprob) p.logprob[row] = (float)log(s.weight(key2f((uint32_t)x)) / total);
-          if (p.kept) p.kept[row] = keep[0];
+          if (p.logprob) p.logprob[row] = (float)log(s.weight(key2f((uint32_t)x)) / sc.y);
+          if (p.kept) p.kept[row] = keep;
         }
         return;
       }
     }
     // C: the k-th key by counts
     unsigned* hist = s.clear_hist(SP_BINS);
-    int have[1] = {0};
+    double have = 0.0;
+#pragma unroll 1
     for (int v = tid; v < s.nvec; v += SP_THREADS) {
-      float z[N];
-      s.unpack(v, z);
       int run = 0, rb = -1;                     // equal neighbours in one atomic
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        if (!(z[j] > -INFINITY)) continue;
-        ++have[0];
-        const int bb = s.bin(z[j]);
+      s.template each<1>(v, [&](float z, int) {
+        if (!(z > -INFINITY)) return;
+        have += 1.0;
+        const int bb = s.bin(z);
         if (bb != rb) {
           if (run) atomicAdd(hist + rb, (unsigned)run);
           rb = bb;
           run = 0;
         }
         ++run;
-      }
+      });
       if (run) atomicAdd(hist + rb, (unsigned)run);
     }
-    s.block_sum(have);
-    int total = 0;
-    unsigned long long x[1] = {(unsigned long long)have[0]};
-    s.exchange(x, [&](int, unsigned long long (&w)[1]) { total += (int)w[0]; });
-    if (k < total) {
-      int b, ti;
+    double lower;
+    have = s.cluster_sum(sp_block_sum(have), lower);
+    if ((double)k < have) {
+      int ti;
       uint32_t tk;
-      s.template border<false>(0.0, (double)k, number, b, above, value);
-      s.template refine<false>(b, (double)k - above, 0, tk, ti);
+      const int b = s.border(SP_COUNT, (double)k, 0, 0);
+      s.refine(false, b, (double)k - sh.found[0], 0, tk, ti);
       s.cut = true;
       s.ck = tk;
       s.ci = ti;
@@ -711,35 +720,32 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
   int b = SP_BINS;                              // top-p: kept are the bins before b and a part of b
   double above = 0.0;
   if (use_p && pf > 0.f) {
-    // C: the slice's mass to fp32.  The whole row's is no smaller, so what is below (1 - top_p) of it
-    // over V is below (1 - top_p) of the mean, and each CTA knows by itself what to leave out
-    float part = 0.f;
+    // C: a part of the slice's mass to fp32 (every fourth vector).  The whole row's is no smaller, so
+    // what is below (1 - top_p) of it over V is below (1 - top_p) of the mean, and each CTA knows by
+    // itself what to leave out
+    float some = 0.f, part = 0.f;
     const float scale = s.ybin * (-1.f / 8.f);
-    for (int v = tid; v < s.nvec; v += SP_THREADS) {
-      float z[N];
-      s.unpack(v, z);
-#pragma unroll
-      for (int j = 0; j < N; ++j) part += s.left(z[j], s.i0 + v * N + j) ? tc::ex2((s.zmax - z[j]) * scale) : 0.f;
-    }
-    double about[1] = {(double)part};
-    s.block_sum(about);
-    if (tid == 0) sh.part[s.search & 1] = about[0];
-    const float mean = (float)(0.99 * (1.0 - top_p) * about[0] / p.V);
+#pragma unroll 1
+    for (int v = tid; v < s.nvec; v += 4 * SP_THREADS)
+      s.template each<4>(v, [&](float z, int idx) { some += s.left(z, idx) ? tc::ex2((s.zmax - z) * scale) : 0.f; });
+    const double about = sp_block_sum((double)some);
+    const float mean = (float)(0.99 * (1.0 - top_p) * about / p.V);
     // bins up to this one; the last bin is below 2^-63 of the maximum
     const int far = mean > 0.f ? min((int)(-8.f * log2f(mean)) + 1, SP_BINS - 2) : SP_BINS - 2;
     const float low = s.edge_low(far);
     unsigned* hist = s.clear_hist(SP_BINS);
+#pragma unroll 1
     for (int v = tid; v < s.nvec; v += SP_THREADS) {
-      float z[N];
-      s.unpack(v, z);
       unsigned run = 0;                         // equal neighbours in one atomic
       int rb = -1;
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        if (!(z[j] >= low) || !s.left(z[j], s.i0 + v * N + j)) continue;
-        const float d = s.zmax - z[j], r = fmaf(d, s.ybin, SP_ONE);
+      s.template each<4>(v, [&](float z, int idx) {
+        const bool in = s.left(z, idx);
+        const float d = s.zmax - z;
+        part += in ? tc::ex2(d * scale) : 0.f;
+        if (!(z >= low) || !in) return;
+        const float r = fmaf(d, s.ybin, SP_ONE);
         const int bb = __float_as_int(r) - 0x4B000000;
-        if (bb > far) continue;
+        if (bb > far) return;
         if (bb != rb) {
           if (run) atomicAdd(hist + rb, run);
           rb = bb;
@@ -748,13 +754,12 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
         // 2^-(distance from the bin's middle, in eighths), below 1.045, in 2^-15 units
         const float y = fmaf(d, s.ybin, SP_ONE - r);
         run += (unsigned)__float_as_int(fmaf(tc::ex2(y * (-1.f / 8.f)), 32768.f, SP_ONE)) - 0x4B000000u;
-      }
+      });
       if (run) atomicAdd(hist + rb, run);
     }
-    double value;
-    s.template border<false>(top_p, 0.0,
-                             [](int i, double n) { return n * (double)exp2f((float)i * (-1.f / 8.f)) * 0x1p-15; }, b,
-                             above, value);
+    const double whole = sp_block_sum((double)part);
+    if (tid == 0) sh.part[s.search & 1] = whole;
+    b = s.border(SP_SHARE, top_p, 0, 0);
   } else if (use_p) {
     b = 0;                                      // top_p <= 0: one token
   }
@@ -763,45 +768,53 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
   int kept = 0;
   for (int moved = 0;;) {
     double sums[2] = {0.0, 0.0};                // all that is left, bins before b
-    const float rb = SP_ONE + (float)b;         // bin(z) < b  <=>  fma(zmax - z, ybin, 2^23) < 2^23 + b
+    // bin(z) < b  <=>  not fma(zmax - z, ybin, 2^23) >= 2^23 + b; without top-p (NaN) everything is before
+    const float rb = use_p ? SP_ONE + (float)b : __int_as_float(0x7fffffff);
+    const bool plain = !s.cut && zcut == -INFINITY;
     kept = 0;
+#pragma unroll 1
     for (int st = warp; st < nst; st += SP_WARPS) {
       const int v = st * 32 + lane;
       double mine = 0.0;
       if (v < s.nvec) {
-        float z[N];
-        double w[N];
-        s.unpack(v, z);
-        unsigned head = 0;                      // kept for certain: in bins before b, above the min-p cut
-#pragma unroll
-        for (int j = 0; j < N; ++j) {           // no branches: the chains of the N weights interleave
-          const bool in = s.left(z[j], s.i0 + v * N + j), some = in && z[j] >= s.zlow;
-          const double x = s.raw_weight(some ? z[j] : s.zmax);
-          w[j] = some ? x : 0.0;
-          const bool before = fmaf(s.zmax - z[j], s.ybin, SP_ONE) < rb || !use_p;
-          head |= (in && before && z[j] >= zcut ? 1u : 0u) << j;
-          if (use_p) sums[1] += before ? w[j] : 0.0;
+        if (plain) {
+          s.template each<4>(v, [&](float z, int) {
+            const bool some = z >= s.zlow;
+            const double x = sp_raw_weight(some ? z : s.zmax, s.zmax, s.c), w = some ? x : 0.0;
+            sums[0] += w;
+            if (!(fmaf(s.zmax - z, s.ybin, SP_ONE) >= rb)) {
+              mine += w;
+              kept += z > -INFINITY;
+            }
+          });
+        } else {
+          s.template each<4>(v, [&](float z, int idx) {
+            const bool in = s.left(z, idx), some = in && z >= s.zlow;
+            const double x = sp_raw_weight(some ? z : s.zmax, s.zmax, s.c), w = some ? x : 0.0;
+            const bool before = !(fmaf(s.zmax - z, s.ybin, SP_ONE) >= rb);
+            const bool head = in && before && z >= zcut;   // kept for certain: before bin b, above the min-p cut
+            kept += head;
+            sums[0] += w;
+            sums[1] += before ? w : 0.0;
+            mine += head ? w : 0.0;
+          });
         }
-        if (use_p) sums[0] += sp_tree<N>(w);
-        kept += __popc(head);
-#pragma unroll
-        for (int j = 0; j < N; ++j) w[j] = (head >> j) & 1u ? w[j] : 0.0;
-        mine = sp_tree<N>(w);
       }
+      if (plain) sums[1] += mine;
       mine = warp_sum_d(mine);
-      if (lane == 0) s.wsum[st] = mine;
+      if (lane == 0) wsum[st] = mine;
     }
     if (!use_p) break;
-    s.block_sum(sums);
-    unsigned long long x[2];
-#pragma unroll
-    for (int q = 0; q < 2; ++q) x[q] = (unsigned long long)__double_as_longlong(sums[q]);
+    sums[0] = sp_block_sum(sums[0]);
+    sums[1] = sp_block_sum(sums[1]);
+    s.exchange(sums[0], sums[1]);
     double total = 0.0;
     above = 0.0;
-    s.exchange(x, [&](int, unsigned long long (&w)[2]) {
-      total += __longlong_as_double((long long)w[0]);
-      above += __longlong_as_double((long long)w[1]);
-    });
+#pragma unroll 1
+    for (int r = 0; r < s.C; ++r) {
+      total += s.got_d(r, 0);
+      above += s.got_d(r, 1);
+    }
     // the bin is right if the sum reaches top_p of the total inside it (b == 0: it starts there)
     const double goal = pf > 0.f ? top_p * total : 0.0;
     if (above >= goal && b > 0 && moved <= 0) {
@@ -813,7 +826,7 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
     const int e = b / 8;
     uint32_t tk;
     int ti;
-    if (!s.template refine<true>(b, fmax(ldexp(goal - above, 31 + e), 0.0), e, tk, ti)) {
+    if (!s.refine(true, b, fmax(ldexp(goal - above, 31 + e), 0.0), e, tk, ti)) {
       if (moved >= 0 && b < SP_BINS - 2) {
         ++b;
         moved = 1;
@@ -825,28 +838,20 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
     }
     // the part of bin b that stays
     const float zt = sp_value<KS>(tk), top = s.edge_high(b);
+    const typename SpVec<T>::Range part(zt, top);
+#pragma unroll 1
     for (int st = warp; st < nst; st += SP_WARPS) {
       const int v = st * 32 + lane;
-      unsigned in = 0;
-      float z[N];
-      if (v < s.nvec) {
-        s.unpack(v, z);
-#pragma unroll
-        for (int j = 0; j < N; ++j) in |= (z[j] >= zt && z[j] <= top && z[j] >= zcut ? 1u : 0u) << j;
-      }
-      if (!__any_sync(FULL, in != 0)) continue;
       double mine = 0.0;
-      if (in) {
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-          const int idx = s.i0 + v * N + j;
-          if (!((in >> j) & 1u) || (z[j] == zt && idx > ti) || s.bin(z[j]) != b || !s.left(z[j], idx)) continue;
-          mine += s.weight(z[j]);
+      if (v < s.nvec && part.any(slice[v]))
+        s.template each<1>(v, [&](float z, int idx) {
+          if (!(z >= zt && z <= top && z >= zcut) || (z == zt && idx > ti) || s.bin(z) != b || !s.left(z, idx)) return;
+          mine += s.weight(z);
           ++kept;
-        }
-      }
+        });
+      if (!__any_sync(FULL, mine > 0.0)) continue;
       mine = warp_sum_d(mine);
-      if (lane == 0) s.wsum[st] += mine;
+      if (lane == 0) wsum[st] += mine;
     }
     // from here on `left` is the final cut
     s.ci = s.cut && tk == s.ck ? min(ti, s.ci) : ti;
@@ -854,40 +859,35 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
     s.cut = true;
     break;
   }
-  int kk[1] = {kept};
-  s.block_sum(kk);                              // also orders the stretches' sums before their use
+  const double kk = sp_block_sum((double)kept);                              // also orders the stretches' sums before their use
   // E: the slices' masses, the slice, the stretch, the element
   const int q = (nst + 31) / 32;                // stretches a lane of the first warp
   double lane_sum = 0.0, lane_inc = 0.0;
   if (warp == 0) {
-    for (int j = lane * q; j < min(nst, (lane + 1) * q); ++j) lane_sum += s.wsum[j];
-    lane_inc = lane_sum;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const double y = __shfl_up_sync(FULL, lane_inc, d);
-      if (lane >= d) lane_inc += y;
-    }
+#pragma unroll 1
+    for (int j = lane * q; j < min(nst, (lane + 1) * q); ++j) lane_sum += wsum[j];
+    lane_inc = sp_warp_scan(lane_sum);
     if (lane == 31) sh.found[2] = lane_inc;
   }
   __syncthreads();
   double mass = 0.0, before = 0.0, chosen_before = 0.0;
-  int chosen = -1, kept_all = 0;
-  {
-    // twice over the slices' masses: the total, then the first slice whose running sum passes u of it
-    unsigned long long x[2] = {(unsigned long long)__double_as_longlong(sh.found[2]), (unsigned long long)kk[0]};
-    s.exchange(x, [&](int, unsigned long long (&w)[2]) {
-      mass += __longlong_as_double((long long)w[0]);
-      kept_all += (int)w[1];
-    });
-    for (int r = 0; r < s.C; ++r) {
-      const double m = __longlong_as_double((long long)sh.xch[(s.step - 1) & 1][r][0]);
-      if (m > 0.0 && (chosen < 0 || chosen_before + __longlong_as_double((long long)sh.xch[(s.step - 1) & 1][chosen][0]) <=
-                                        (double)u * mass)) {
-        chosen = r;                             // (else, by rounding, the last slice with mass)
-        chosen_before = before;
-      }
-      before += m;
+  double kept_all = 0.0;
+  int chosen = -1;
+  s.exchange(sh.found[2], kk);
+#pragma unroll 1
+  for (int r = 0; r < s.C; ++r) {
+    mass += s.got_d(r, 0);
+    kept_all += s.got_d(r, 1);
+  }
+  // the first slice whose running sum passes u of the total (else, by rounding, the last with mass)
+#pragma unroll 1
+  for (int r = 0; r < s.C; ++r) {
+    const double m = s.got_d(r, 0);
+    if (m > 0.0 && (chosen < 0 || chosen_before + s.got_d(chosen, 0) <= (double)u * mass)) {
+      chosen = r;
+      chosen_before = before;
     }
+    before += m;
   }
   const double goal = (double)u * mass;
   if (s.rank == chosen && warp == 0) {
@@ -898,8 +898,9 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
     double run = chosen_before + __shfl_sync(FULL, lane_inc - lane_sum, l);
     int st = -1;
     double st_run = 0.0;
+#pragma unroll 1
     for (int j = l * q; j < min(nst, (l + 1) * q); ++j) {
-      const double w = s.wsum[j];
+      const double w = wsum[j];
       if (w > 0.0) {
         st = j;
         st_run = run;
@@ -908,56 +909,40 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
       run += w;
     }
     const int v = st * 32 + lane;
-    double w[N], mine = 0.0;
-#pragma unroll
-    for (int j = 0; j < N; ++j) w[j] = 0.0;
-    if (v < s.nvec) {
-      float z[N];
-      s.unpack(v, z);
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        if (s.left(z[j], s.i0 + v * N + j) && z[j] >= zcut) w[j] = s.weight(z[j]);
-        mine += w[j];
-      }
-    }
-    double inc = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const double y = __shfl_up_sync(FULL, inc, d);
-      if (lane >= d) inc += y;
-    }
+    double mine = 0.0;
+    auto mass_of = [&](float z, int idx) { return s.left(z, idx) && z >= zcut ? s.weight(z) : 0.0; };
+    if (v < s.nvec) s.template each<1>(v, [&](float z, int idx) { mine += mass_of(z, idx); });
+    const double inc = sp_warp_scan(mine);
     const unsigned hit2 = __ballot_sync(FULL, st_run + inc > goal && mine > 0.0);
     const unsigned any2 = __ballot_sync(FULL, mine > 0.0);
     const int l2 = hit2 ? __ffs(hit2) - 1 : 31 - __clz(any2);
     if (lane == l2) {
-      double r2 = st_run + inc - mine;
+      double r2 = st_run + inc - mine, tw = 1.0;
       int tok = -1;
-      double tw = 1.0;
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        if (w[j] > 0.0 && (tok < 0 || r2 <= goal)) {
-          tok = s.i0 + v * N + j;
-          tw = w[j];
+      s.template each<1>(v, [&](float z, int idx) {
+        const double w = mass_of(z, idx);
+        if (w > 0.0 && (tok < 0 || r2 <= goal)) {
+          tok = idx;
+          tw = w;
         }
-        r2 += w[j];
-      }
+        r2 += w;
+      });
       p.token[row] = tok;
       if (p.logprob) p.logprob[row] = (float)log(tw / mass);
-      if (p.kept) p.kept[row] = kept_all;
+      if (p.kept) p.kept[row] = (int)kept_all;
     }
   }
 }
 
 cudaError_t launch_sample(const SampleParams& p, cudaStream_t st) {
   const int es = p.bf16 ? 2 : 4, vn = 16 / es;
-  // the cluster.  Few rows: short slices, for short passes, up to 16 CTAs a row (more than 8 need the
-  // non-portable size) while all rows fit the GPU at once.  Many rows: slices of up to 40960, two
+  // the cluster.  Few rows: slices down to 4096, for short passes, up to 16 CTAs a row (more than 8 need
+  // the non-portable size) while all rows fit the GPU at once.  Many rows: slices of up to 40960, two
   // CTAs an SM, so that a search's barriers are paid by fewer CTAs
-  const bool many = p.n * 8 > 4 * num_sms();
-  const int most = many ? 40960 : 16384;
+  const int most = p.n * 8 > 4 * num_sms() ? 40960 : 16384;
   int C = 1;
   while (C < 8 && (p.V + C - 1) / C > most) C <<= 1;
-  if (C == 8 && p.n * 16 <= num_sms()) C = 16;
+  while (C < SP_MAXC && p.V / C > 4096 && p.n * 2 * C <= num_sms()) C <<= 1;
   const int unit = 32 * vn;
   const int per = ((p.V + C - 1) / C + unit - 1) / unit * unit;
   const size_t smem = sizeof(SpShared) + (size_t)per * es + (size_t)(per / unit) * sizeof(double);
