@@ -4,28 +4,35 @@
 // head of it, so the outcome is one cut (key, index), and the token is found where the kept
 // mass, summed in index order, passes u times its total.  No sort of the row.
 //
-// Masses.  A vocabulary of 10^5 flat probabilities puts borders 10^-5 apart, so fp32 sums
-// (errors near 10^-7) would move a border once in a hundred rows.  Weights are formed in fp64:
-// 2^t with t = (z - max) log2(e) / T split as t = k / 64 + f, |f| <= 1/128; 2^(k mod 64 / 64) from a
-// table that the CUDA function exp2 fills, 2^f by the Taylor series of exp(f ln 2) to degree 4
-// (relative error below 4e-14), and the exponent added.  Weights below 2^-64 of the largest count
-// as nothing: all of them together are below 2^-46 of the mass.  Sums run in a fixed order.
+// Masses.  A vocabulary of 10^5 flat probabilities puts borders 10^-5 apart, and a sum of n weights
+// w that carry independent errors e is off by e w sqrt(n): fp32 weights (e = 2^-24, 2e-5 w at n =
+// 10^5; worse where equal logits repeat one error) with fp32 sums (3e-3 w) would move a border once in
+// a hundred rows.  So weights carry 31 bits and are summed in fp64.  2^t, t = (z - max) log2(e) / T:
+// t in fp64 is rounded to 32 fraction bits, whose upper 8 pick 2^(j / 256) from a table that the CUDA
+// function exp2 fills (an integer in 2^-30 units) and whose lower 24 give x = r ln 2 < 2.8e-3 and
+// 2^r - 1 = x + x^2 / 2 + x^3 / 6 in fp32 (2^-24 of it, 2^-32 of the weight); integer and product
+// add up to the mantissa, and exponent and mantissa are put together as an fp64.  That is 4 fp64
+// operations an element where the Taylor series in fp64 took 13, which bound pass D.  The largest
+// logit's weight is 1 exactly.  Weights below 2^-64 of it count as nothing: all of them together are
+// below 2^-46 of the mass.  Sums run in a fixed order.
 //
 // A row is a cluster of CTAs, each with a slice of it in shared memory, read from HBM once.
 //   A  the maximum
 //   B  top-k, few: the k-th largest of the threads' own maxima is a bound that k elements reach; what
 //      reaches it goes to one CTA, which sorts it, sums it in that order for top-p, and again in
 //      index order for the token
-//   C  else the cut is searched: counts (top-k) or masses (top-p) by bins of 1/8 octave of weight below
-//      the maximum (shared-memory integer atomics: order does not matter), summed over the
-//      cluster through distributed shared memory; the bin that holds the border is searched
-//      again by ranges of the key, until one key is left; of its ties the lowest indices stay.
-//      512 bins: every CTA reads all histograms of the cluster, which at 2048 bins and 16 CTAs took
-//      9.8k cycles.  Tokens whose weight is below (1 - top_p) of the mean are left out of the first
-//      search of masses: together they hold less than the 1 - top_p that is cut.  Its bins hold
-//      masses to 16 bits only: the exact sums of D decide whether the bin is the right one (else its
-//      neighbour is taken), the later searches count in 2^-31 units of the bin's weights, or
-//      exactly once a bin is one key.
+//   C  else the cut is searched: counts (top-k) or masses (top-p) by 512 bins of the distance below the
+//      maximum (shared-memory integer atomics: order does not matter), summed over the cluster
+//      through distributed shared memory; the bin that holds the border is searched again by
+//      ranges of the key, until one key is left; of its ties the lowest indices stay.  Every CTA
+//      reads all histograms of the cluster: with 2048 bins and 16 CTAs that took 9.8k cycles.
+//      For masses a quarter of the row is summed first, in fp32.  That is a lower bound S of the
+//      mass, and tokens below (1 - top_p) S / V together hold less than the 1 - top_p that is cut:
+//      they stay out, and the bins spread over what is left (atomics that meet in a bin wait for one
+//      another: bins of 1/8 octave cost a flat row 26k cycles).  The bins hold masses to 16 bits
+//      only: the exact sums of D decide whether the bin is the right one (else its neighbour is
+//      taken), the later searches count in 2^-31 units of the bin's weights, or exactly once a bin is
+//      one key.
 //   D  fp64 sums of the kept weights by 32-vector stretches of a warp, in index order
 //   E  the stretch, lane and element where u * total falls
 #include <cooperative_groups.h>
@@ -50,7 +57,7 @@ struct alignas(16) SpShared {                   // the slice follows: its vector
     unsigned hist[2][2 * SP_BINS];              // two searches deep: counts or masses; two 16-bit limbs of a mass
     unsigned long long list[SP_LIST];
   };
-  double table[64];                             // 2^(j / 64)
+  uint2 table[256];                             // 2^(j / 256): in 2^-30 units, and as an fp32
   double part[2];                               // beside a histogram: the mass of the slice, to fp32
   unsigned long long xch[2][SP_MAXC][2];        // values of every CTA of the cluster, two steps deep
   double red[SP_WARPS];
@@ -209,18 +216,16 @@ __device__ __noinline__ void sp_exchange(int C, int rank, int slot, unsigned lon
 }
 // The weight of logit z: 2^((z - zmax) c), for z within 2^-64 of the largest.
 __device__ __forceinline__ double sp_raw_weight(float z, float zmax, double c) {
-  const double t = ((double)z - (double)zmax) * c;
-  const double magic = 6755399441055744.0 / 64;   // 1.5 * 2^52 / 64: rounds t to a multiple of 1/64
-  const double r = t + magic;
-  const int k = __double2loint(r);
-  const double f = t - (r - magic);
-  // exp(f ln 2) = 1 + f ln2 + (f ln2)^2 / 2 + (f ln2)^3 / 6 + (f ln2)^4 / 24
-  double p = fma(f, 9.618129107628477e-3, 5.550410866482158e-2);
-  p = fma(f, p, 2.402265069591007e-1);
-  p = fma(f, p, 6.931471805599453e-1);
-  p = fma(f, p, 1.0);
-  p *= sp_sh().table[k & 63];
-  return __hiloint2double(__double2hiint(p) + ((k >> 6) << 20), __double2loint(p));
+  const double r = ((double)z - (double)zmax) * c + 1572864.0;   // 1.5 * 2^20: 32 fraction bits, the low word
+  const uint32_t f = (uint32_t)__double2loint(r);
+  const uint2 tab = sp_sh().table[f >> 24];
+  // r in 2^-24 units, without its last bit, and 2^r - 1
+  const float x = (__uint_as_float(0x4B000000u | ((f & 0xffffffu) >> 1)) - SP_ONE) * (float)(0.6931471805599453 / 2147483648.0);
+  const float q = fmaf(x * x, fmaf(x, 1.f / 6.f, 0.5f), x);
+  const uint32_t m = tab.x + (uint32_t)(__float_as_int(fmaf(__uint_as_float(tab.y) * q, 1073741824.f, SP_ONE)) - 0x4B000000);
+  // m 2^(k - 30), 2^30 <= m < 2^31, k = high word - 0x41380000: exponent field k + 1023 over m's low 30 bits
+  const uint32_t hi = ((uint32_t)__double2hiint(r) << 20) + (uint32_t)((1022u - 0x41380000u) << 20) + (m >> 10);
+  return __hiloint2double((int)hi, (int)(m << 22));
 }
 // The same times 2^e, 0 below zlow.
 __device__ __noinline__ double sp_weight(float z, float zmax, float zlow, double c, int e) {
@@ -233,13 +238,13 @@ enum { SP_COUNT, SP_SHARE, SP_LIMBS, SP_KEYS };
 // The first bin at which the sum over the cluster's histograms reaches `target` (SHARE: that share of
 // the cluster's `part`), or the last that holds something: returned, with the sum before it in
 // found[0] and the bin's own value in found[1].  What a word of bin i stands for: COUNT, 1; SHARE, 2^-15
-// of the weight at the bin's middle; LIMBS, 1, and a word of the histogram's second half 2^16; KEYS,
+// of the weight at the bin's middle (bins `octaves` wide); LIMBS, 1, and a word of the histogram's second half 2^16; KEYS,
 // the weight of key first - i in 2^-(31 + e) units.  Every CTA reads all histograms (a thread one bin,
 // its loads all in flight) and scans them for itself: one cluster barrier a search.  The next search
 // uses the other buffer, so a slow reader is not overtaken.
 template <int KS>
 __device__ __noinline__ int sp_border(int kind, double target, int C, int rank, int buf, uint32_t first, int e, float zmax,
-                                      float zlow, double c) {
+                                      float zlow, double c, float octaves) {
   static_assert(SP_BINS == SP_THREADS, "a bin a thread");
   cg::cluster_group cl = cg::this_cluster();
   SpShared& sh = sp_sh();
@@ -261,7 +266,7 @@ __device__ __noinline__ int sp_border(int kind, double target, int C, int rank, 
     if (lane == 0) sh.found[3] = target * m;
   }
   double v = (double)h;
-  if (kind == SP_SHARE) v *= (double)(tc::ex2((float)threadIdx.x * (-1.f / 8.f)) * 0x1p-15f);
+  if (kind == SP_SHARE) v *= (double)(tc::ex2((float)threadIdx.x * -octaves) * 0x1p-15f);
   if (kind == SP_KEYS && h) v *= sp_weight(sp_value<KS>(first - threadIdx.x), zmax, zlow, c, 31 + e);
   const double2 sc = sp_block_scan(v);
   const double inc = sc.x + v;
@@ -318,10 +323,11 @@ struct SpRow {
     return all;
   }
   __device__ __forceinline__ int border(int kind, double target, uint32_t first, int e) {
-    const int b = sp_border<KS>(kind, target, C, rank, search & 1, first, e, zmax, zlow, c);
+    const int b = sp_border<KS>(kind, target, C, rank, search & 1, first, e, zmax, zlow, c, octaves());
     ++search;
     return b;
   }
+  __device__ __forceinline__ float octaves() const { return ybin > 0.f ? (float)(c / (double)ybin) : 0.f; }   // a bin's width
   __device__ __forceinline__ double weight(float z, int e = 0) const { return sp_weight(z, zmax, zlow, c, e); }
 
   // use(value, index) for the elements of vector v, in order, U of its four words at a time.
@@ -521,13 +527,16 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
 
   // A: the slice into shared memory and the maximum
   float best = -INFINITY;
-#pragma unroll 2
+#pragma unroll 4
   for (int v = tid; v < s.nvec; v += SP_THREADS) {
     const uint4 u = SpVec<T>::clean(sp_load<T, ALIGNED>(z0, s.i0 + (int64_t)v * N, p.V));
     slice[v] = u;
     best = fmaxf(best, SpVec<T>::largest(u));
   }
-  if (tid < 64) sh.table[tid] = exp2((double)tid / 64.0);
+  if (tid < 256) {
+    const double x = exp2((double)tid / 256.0);
+    sh.table[tid] = make_uint2((unsigned)__double2uint_rn(x * 1073741824.0), __float_as_uint((float)x));
+  }
   const float T_ = p.temperature ? p.temperature[row] : 1.f;
   const int k = p.top_k ? p.top_k[row] : 0;
   const float pf = p.top_p ? p.top_p[row] : 1.f, mf = p.min_p ? p.min_p[row] : 0.f;
@@ -720,19 +729,20 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
   int b = SP_BINS;                              // top-p: kept are the bins before b and a part of b
   double above = 0.0;
   if (use_p && pf > 0.f) {
-    // C: a part of the slice's mass to fp32 (every fourth vector).  The whole row's is no smaller, so
-    // what is below (1 - top_p) of it over V is below (1 - top_p) of the mean, and each CTA knows by
-    // itself what to leave out
+    // C: every fourth vector's mass, to fp32: a lower bound of the row's
     float some = 0.f, part = 0.f;
-    const float scale = s.ybin * (-1.f / 8.f);
+    const float scale = -(float)s.c;
 #pragma unroll 1
     for (int v = tid; v < s.nvec; v += 4 * SP_THREADS)
       s.template each<4>(v, [&](float z, int idx) { some += s.left(z, idx) ? tc::ex2((s.zmax - z) * scale) : 0.f; });
-    const double about = sp_block_sum((double)some);
-    const float mean = (float)(0.99 * (1.0 - top_p) * about / p.V);
-    // bins up to this one; the last bin is below 2^-63 of the maximum
-    const int far = mean > 0.f ? min((int)(-8.f * log2f(mean)) + 1, SP_BINS - 2) : SP_BINS - 2;
-    const float low = s.edge_low(far);
+    double lower;
+    const double bound = s.cluster_sum(sp_block_sum((double)some), lower);
+    // what is lighter than `mean` stays out; the bins before the last cover the rest, with a bin to spare
+    const float mean = (float)fmin(0.99 * (1.0 - top_p) * bound / p.V, 0.99);
+    const float range = mean > 0x1p-63f ? -log2f(mean) : 63.f;   // octaves
+    s.ybin = fminf((float)((SP_BINS - 3) * s.c) / range, 3e38f);
+    const int far = SP_BINS - 2;
+    const float low = s.edge_low(far), oct = s.octaves();
     unsigned* hist = s.clear_hist(SP_BINS);
 #pragma unroll 1
     for (int v = tid; v < s.nvec; v += SP_THREADS) {
@@ -751,9 +761,9 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
           rb = bb;
           run = 0;
         }
-        // 2^-(distance from the bin's middle, in eighths), below 1.045, in 2^-15 units
+        // 2^-(distance from the bin's middle), at most 2^(1/16), in 2^-15 units
         const float y = fmaf(d, s.ybin, SP_ONE - r);
-        run += (unsigned)__float_as_int(fmaf(tc::ex2(y * (-1.f / 8.f)), 32768.f, SP_ONE)) - 0x4B000000u;
+        run += (unsigned)__float_as_int(fmaf(tc::ex2(y * -oct), 32768.f, SP_ONE)) - 0x4B000000u;
       });
       if (run) atomicAdd(hist + rb, run);
     }
@@ -822,8 +832,8 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
       moved = -1;
       continue;
     }
-    // the bin's weights lie within 2^(-(b +- 1/2) / 8) of the maximum: scaled by 2^e they are at most 2^(1/16)
-    const int e = b / 8;
+    // the bin's weights lie within 2^(-(b +- 1/2) octaves) of the maximum: scaled by 2^e they are at most 2^(1/16)
+    const int e = (int)((float)b * s.octaves());
     uint32_t tk;
     int ti;
     if (!s.refine(true, b, fmax(ldexp(goal - above, 31 + e), 0.0), e, tk, ti)) {
