@@ -715,11 +715,42 @@ def _flat(t: Optional[torch.Tensor], name: str, dtype, n: int) -> Optional[int]:
     """Address of a contiguous tensor of n elements."""
     if t is None:
         return None
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}")
     if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous with {n} elements")
     return t.data_ptr()
+
+
+_DTYPE = {torch.bfloat16: KVC_BF16, torch.float32: KVC_F32}
+
+
+def _cache(t: torch.Tensor, lead: tuple, d: int, name: str) -> KV:
+    """KV descriptor of a cache whose leading sizes must be `lead` (None: any), then tokens, then rows of
+    d contiguous elements.  A dimension of one element gets the stride its inner neighbour implies."""
+    sh, st = t.shape, t.stride()
+    n = len(lead)
+    ok = len(sh) == n + 2 and sh[n + 1] == d and st[n + 1] == 1
+    if ok:
+        for i in range(n):
+            if lead[i] is not None and sh[i] != lead[i]:
+                ok = False
+    if not ok:
+        raise ValueError(f"{name} must be {''.join('[any]' if x is None else f'[{x}]' for x in lead)}[tokens][{d}] with "
+                         "contiguous rows")
+    if 1 in sh[:n + 1]:
+        st = list(st)
+        for i in range(n, -1, -1):
+            if sh[i] == 1:
+                st[i] = d if i == n else st[i + 1] * sh[i + 1]
+    code = _DTYPE.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    if n == 3:                                # [B][L][Hkv]
+        return KV(t.data_ptr(), code, st[0], st[1], st[2], st[3])
+    if lead[0] is None:                       # [pages][Hkv]
+        return KV(t.data_ptr(), code, st[0], 0, st[1], st[2])
+    return KV(t.data_ptr(), code, 0, st[0], st[1], st[2])   # [L][Hkv]
 
 
 def _own_ws(op, m, args, workspace, device, stream):
@@ -736,18 +767,6 @@ def _own_ws(op, m, args, workspace, device, stream):
     if stream is not None:
         workspace.record_stream(stream)
     return workspace, need
-
-
-def _pool(t: torch.Tensor, H: int, d: int, name: str) -> KV:
-    """KV descriptor of a page pool [n_pages][Hkv][page][d] in any strides with contiguous rows."""
-    if t.dim() != 4 or t.shape[1] != H or t.shape[3] != d or t.stride(3) != 1:
-        raise ValueError(f"{name} must be [n_pages][{H}][page][{d}] with contiguous rows")
-    sp, sh, st = t.stride()[:3]
-    if t.shape[0] == 1:
-        sp = t.shape[1] * t.shape[2] * d
-    if H == 1:
-        sh = t.shape[2] * d
-    return KV(t.data_ptr(), _dt(t), sp, 0, sh, st)
 
 
 def page_tables_args(*, lens, lens_new, table, ring, state, page: int, state_out=None, lens_out=None, slots=None,
@@ -801,20 +820,9 @@ def kvc_page_append(m: Model, *, k, v, K, V, slots, stream=None):
 
     if T == 0:
         return
-    a.k, a.v, a.K, a.V = src(k), src(v), _pool(K, H, d, "K"), _pool(V, H, d, "V")
+    a.k, a.v, a.K, a.V = src(k), src(v), _cache(K, (None, H), d, "K"), _cache(V, (None, H), d, "V")
     a.slots = _flat(slots, "slots", torch.int32, T)
     _check(lib().kvc_page_append(C.byref(m), C.byref(a), _raw_stream(stream)))
-
-
-def _strides_of(t: torch.Tensor, shape, d: int, name: str):
-    """Strides of a cache tensor whose leading sizes must be `shape` (tokens free), rows contiguous."""
-    if t.dim() != len(shape) + 2 or tuple(t.shape[:-2]) != tuple(shape) or t.shape[-1] != d or t.stride(-1) != 1:
-        raise ValueError(f"{name} must be {''.join(f'[{x}]' for x in shape)}[tokens][{d}] with contiguous rows")
-    st = list(t.stride()[:-1])
-    for i in range(len(st) - 1, -1, -1):      # a dimension of one element gets the stride its neighbour implies
-        if t.shape[i] == 1:
-            st[i] = d if i == len(st) - 1 else st[i + 1] * t.shape[i + 1]
-    return st
 
 
 def prefix_decode_args(m: Model, *, q, o, K_prefix=None, V_prefix=None, lens_prefix=None, max_len_prefix: int = 0,
@@ -823,46 +831,51 @@ def prefix_decode_args(m: Model, *, q, o, K_prefix=None, V_prefix=None, lens_pre
     """Argument struct of kvc_prefix_decode_attn."""
     _one_device(q, o, K_prefix, V_prefix, lens_prefix, R, K, V, lens, table, lse)
     L, Hq, H, d = m.n_layers, m.n_q_heads, m.n_kv_heads, m.head_dim
-    if q.dim() != 4 or tuple(q.shape[1:]) != (L, Hq, d) or not q.is_contiguous():
+    qs = q.shape
+    if len(qs) != 4 or qs[1] != L or qs[2] != Hq or qs[3] != d or not q.is_contiguous():
         raise ValueError(f"q must be contiguous [B][{L}][{Hq}][{d}]")
     a = PrefixDecodeArgs()
-    B_ = q.shape[0]
+    B_ = qs[0]
     a.batch, a.q, a.q_dtype = B_, q.data_ptr(), _dt(q)
-    a.o = _flat(o, "o", torch.float32, q.numel())
+    a.o = _flat(o, "o", torch.float32, B_ * L * Hq * d)
     a.alpha_c, a.scale = alpha_c, scale
     if K_prefix is not None:
-        sk, sv = _strides_of(K_prefix, (L, H), d, "K_prefix"), _strides_of(V_prefix, (L, H), d, "V_prefix")
-        if max_len_prefix > min(K_prefix.shape[2], V_prefix.shape[2]):
+        a.K_prefix, a.V_prefix = _cache(K_prefix, (L, H), d, "K_prefix"), _cache(V_prefix, (L, H), d, "V_prefix")
+        if max_len_prefix > K_prefix.shape[2] or max_len_prefix > V_prefix.shape[2]:
             raise ValueError("max_len_prefix above the prompt cache's rows")
-        a.K_prefix = KV(K_prefix.data_ptr(), _dt(K_prefix), 0, *sk)
-        a.V_prefix = KV(V_prefix.data_ptr(), _dt(V_prefix), 0, *sv)
         a.len_prefix, a.max_len_prefix = _flat(lens_prefix, "lens_prefix", torch.int32, L), max_len_prefix
         if R is not None:
-            if R.dtype != torch.float32 or R.dim() != 3 or tuple(R.shape[:2]) != (L, H) or R.shape[2] < max_len_prefix \
-                    or R.stride(2) != 1:
+            rs, rt = R.shape, R.stride()
+            if R.dtype is not torch.float32 or len(rs) != 3 or rs[0] != L or rs[1] != H or rs[2] < max_len_prefix \
+                    or (rt[2] != 1 and rs[2] > 1):
                 raise ValueError(f"R must be fp32 [{L}][{H}][>= max_len_prefix] with contiguous rows")
-            a.R, a.R_s_layer, a.R_s_head = R.data_ptr(), R.stride(0), R.stride(1)
+            a.R, a.R_s_layer, a.R_s_head = R.data_ptr(), rt[0], rt[1]
     elif R is not None:
         raise ValueError("R belongs to a prompt")
     if K is not None:
         if table is None:
-            sk, sv = _strides_of(K, (B_, L, H), d, "K"), _strides_of(V, (B_, L, H), d, "V")
-            if max_len > min(K.shape[3], V.shape[3]):
+            a.K, a.V = _cache(K, (B_, L, H), d, "K"), _cache(V, (B_, L, H), d, "V")
+            if max_len > K.shape[3] or max_len > V.shape[3]:
                 raise ValueError("max_len above the cache's rows")
-            a.K, a.V = KV(K.data_ptr(), _dt(K), *sk), KV(V.data_ptr(), _dt(V), *sv)
         else:
             if K.shape != V.shape:
                 raise ValueError("K and V must have one shape")
-            a.K, a.V, a.page, a.n_pages = _pool(K, H, d, "K"), _pool(V, H, d, "V"), K.shape[2], K.shape[0]
-            if table.dtype != torch.int32 or table.dim() != 3 or tuple(table.shape[:2]) != (B_, L) \
-                    or table.stride(2) != 1 or table.shape[2] * a.page < max_len:
+            a.K, a.V = _cache(K, (None, H), d, "K"), _cache(V, (None, H), d, "V")
+            a.n_pages, a.page = K.shape[0], K.shape[2]
+            ts, tt = table.shape, table.stride()
+            if table.dtype is not torch.int32 or len(ts) != 3 or ts[0] != B_ or ts[1] != L or (tt[2] != 1 and ts[2] > 1) \
+                    or ts[2] * a.page < max_len:
                 raise ValueError(f"table must be int32 [{B_}][{L}][>= max_len / page] with contiguous rows")
-            a.table, a.table_s_batch, a.table_s_layer = table.data_ptr(), table.stride(0), table.stride(1)
+            a.table, a.table_s_batch, a.table_s_layer = table.data_ptr(), tt[0], tt[1]
         a.len, a.max_len = _flat(lens, "lens", torch.int32, B_ * L), max_len
     if lse is not None:
-        if tuple(lse.shape) != (B_, L, Hq):
+        ls = lse.shape
+        if len(ls) != 3 or ls[0] != B_ or ls[1] != L or ls[2] != Hq:
             raise ValueError(f"lse must be [{B_}][{L}][{Hq}]")
-        a.lse, a.lse_stride = _lse(lse)
+        if lse.dtype is torch.float32 and lse.is_contiguous():
+            a.lse, a.lse_stride = lse.data_ptr(), 1
+        else:
+            a.lse, a.lse_stride = _lse(lse)
     return a
 
 

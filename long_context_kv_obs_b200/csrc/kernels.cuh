@@ -261,7 +261,46 @@ struct PrefixParams {
   int nsp, spl, rgp;                        // generic: splits, keys a split, groups of 8 query rows
   int nso, slo;                             // own rows: splits and keys a split
   PartialBuf pp, po;
+  int* counter;                             // own items drawn so far (one word of the workspace)
+  int own_mma, counter_zeroed;              // the tensor-core own kernel; the prompt's kernel zeroes its counter
 };
+constexpr int PREFIX_TC_LAYERS = 128;       // layers whose tile sums fit the shared arrays
+
+__device__ __forceinline__ int prefix_len(const PrefixParams& p, int l) {
+  const int n = p.len_p[l];
+  return n < 0 ? 0 : n > p.max_p ? p.max_p : n;
+}
+// One warp: cum[l] = 128-key tiles of all items of the layers before l, l <= L <= PREFIX_TC_LAYERS.
+__device__ __forceinline__ void prefix_tile_sums(const PrefixParams& p, int* cum) {
+  const int lane = threadIdx.x & 31;
+  int run = 0;
+  for (int l0 = 0; l0 < p.L; l0 += 32) {
+    const int l = l0 + lane;
+    int t = l < p.L ? (prefix_len(p, l) + 127) / 128 * p.Hkv * p.mp : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(FULL, t, o);
+      if (lane >= o) t += x;
+    }
+    if (l < p.L) cum[l + 1] = run + t;
+    run += __shfl_sync(FULL, t, 31);
+  }
+  if (lane == 0) cum[0] = 0;
+}
+// The tensor-core prompt kernel's records of query row r = b * G + head of (layer l, KV head g): their
+// number, the first one and the step between them.  before, all, T: tiles of the layers before, of
+// all layers, of one item of this one.
+__device__ __forceinline__ int prefix_records(const PrefixParams& p, int before, int all, int T, int l, int g, int r,
+                                              int64_t& first, int& step) {
+  if (T == 0) return 0;
+  const int W = max(1, (all + p.grid - 1) / p.grid), blk = p.mt * 128, mp = r / blk, rr = r - mp * blk;
+  const int it = g * p.mp + mp, start = before + it * T, c0 = start / W, c1 = (start + T - 1) / W;
+  // a run and an item it touches have two groups of 128 rows: mt 1, one a warpgroup and both hold the
+  // row; mt 2, the second holds the next 128 rows
+  step = p.mt == 1 ? 128 : 256;
+  first = 2 * ((int64_t)l * p.Hkv * p.mp + it + c0) * 128 + rr;
+  return (c1 - c0 + 1) * (p.mt == 1 ? 2 : 1);
+}
 bool prefix_tc_supported(const PrefixParams& p);
 cudaError_t launch_prefix_tc(const PrefixParams& p, cudaStream_t st);
 bool prefix_own_mma_supported(const PrefixParams& p);

@@ -173,93 +173,128 @@ __global__ void __launch_bounds__(PG_THREADS) prefix_generic_kernel(const __grid
   }
 }
 
-// One warp a (sequence, layer, query head): merge its records, prompt first, in a fixed order.
-// Records without weight (nothing seen) are not read.
-template <int D>
-__global__ void __launch_bounds__(256) prefix_combine_kernel(const __grid_constant__ PrefixParams p) {
-  constexpr int EPL = D / 32;
-  const int wid = (int)((blockIdx.x * 256 + threadIdx.x) >> 5), lane = threadIdx.x & 31;
-  if (wid >= p.B * p.L * p.Hq) return;
-  const int h = wid % p.Hq, bl = wid / p.Hq, l = bl % p.L, b = bl / p.L;
-  const int g = h / p.G, gg = h - g * p.G;
-  int np = 0;                                   // prompt records, `pstep` apart from prec
-  int64_t prec = 0, pstep = 0;
+// Merge of the records, in a fixed order: CTAs of a (sequence, layer) and some of its heads.  Where the
+// prompt's runs lie depends on every layer's length: the CTA sums them once.  Eight lanes share a
+// record, D / 8 dimensions each, so it is D / 32 loads a lane, all in flight.  Many heads: eight lanes
+// a head (65536 heads of 3 records 30 us; with a warp a head, and its chain of lengths, maxima and
+// outputs, 57 us).  Few heads, whose prompt is cut into many runs: a warp a head, its four groups
+// of lanes a quarter of the records each (512 heads of 35 records: 9 us against 21).  Records without
+// weight (nothing seen) are not read, they may hold anything.
+constexpr int PC_THREADS = 256;
+constexpr int PC_MANY = 4096;                   // heads from which eight lanes a head are faster (6272: 13 us against 19)
+template <int D, int GR>
+__global__ void __launch_bounds__(PC_THREADS) prefix_combine_kernel(const __grid_constant__ PrefixParams p) {
+  constexpr int Q = D / 32;                     // float4s a lane
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane & 7, grp = GR == 1 ? 0 : lane >> 3;
+  const int bl = blockIdx.x, l = bl % p.L, b = bl / p.L;
+  const int h0 = blockIdx.y * (PC_THREADS / (8 * GR)) + (int)threadIdx.x / (8 * GR);
+  __shared__ int sums[3];                       // tiles of the layers before, of all, of this one
   if (p.Kp && p.tc) {
-    // the runs that touch this row's item (see prefix_tc.cu)
-    const int per = p.Hkv * p.mp;
-    int before = 0, all = 0, T = 0;
-    for (int x = lane; x < p.L; x += 32) {
-      const int n0 = p.len_p[x], n = n0 < 0 ? 0 : min(n0, p.max_p), t = (n + 127) / 128;
-      all += t * per;
-      if (x < l) before += t * per;
-      if (x == l) T = t;
+    if (warp == 0) {
+      const int per = p.Hkv * p.mp;
+      int before = 0, all = 0, T = 0;
+      for (int x = lane; x < p.L; x += 32) {
+        const int t = (prefix_len(p, x) + 127) / 128;
+        all += t * per;
+        if (x < l) before += t * per;
+        if (x == l) T = t;
+      }
+      before = __reduce_add_sync(FULL, before);
+      all = __reduce_add_sync(FULL, all);
+      T = __reduce_add_sync(FULL, T);
+      if (lane == 0) {
+        sums[0] = before;
+        sums[1] = all;
+        sums[2] = T;
+      }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      before += __shfl_xor_sync(FULL, before, o);
-      all += __shfl_xor_sync(FULL, all, o);
-      T += __shfl_xor_sync(FULL, T, o);
-    }
-    if (T > 0) {
-      const int W = max(1, (all + p.grid - 1) / p.grid);
-      const int r = b * p.G + gg, blk = p.mt * 128, mp = r / blk, rr = r - mp * blk;
-      const int it = g * p.mp + mp, start = before + it * T, c0 = start / W, c1 = (start + T - 1) / W;
-      const int64_t item = (int64_t)l * per + it;
-      // mt 1: both warpgroups' records of a run hold the row; mt 2: one of them
-      np = (c1 - c0 + 1) * (p.mt == 1 ? 2 : 1);
-      pstep = p.mt == 1 ? 128 : 256;
-      prec = 2 * (item + c0) * 128 + rr;        // mt 2: the second group of 128 rows follows the first
-    }
+    __syncthreads();
+  }
+  const bool live = h0 < p.Hq;
+  const int h = live ? h0 : p.Hq - 1;           // lanes past the last head repeat it and write nothing
+  const int g = h / p.G, gg = h - g * p.G;
+  int np = 0, pstep = 0;                        // prompt records, `pstep` apart from prec
+  int64_t prec = 0;
+  if (p.Kp && p.tc) {
+    np = prefix_records(p, sums[0], sums[1], sums[2], l, g, b * p.G + gg, prec, pstep);
   } else if (p.Kp) {
     const int r = b * p.G + gg;
     np = p.nsp;
     pstep = PG_ROWS;
     prec = (((int64_t)l * p.Hkv + g) * p.rgp + r / PG_ROWS) * p.nsp * PG_ROWS + r % PG_ROWS;
   }
-  const int no = p.K ? p.nso : 0;
+  const int nall = np + (p.K ? p.nso : 0);
   const int64_t orec = ((int64_t)bl * p.Hkv + g) * p.nso * p.G + gg;
-  const int nall = np + no;
-  float M = -INFINITY;
-  for (int i = lane; i < nall; i += 32) {
-    const float2 x = i < np ? p.pp.ml[prec + i * pstep] : p.po.ml[orec + (int64_t)(i - np) * p.G];
-    M = fmaxf(M, x.x);
-  }
-  M = warp_max(M);
-  float acc[EPL], lsum = 0.f;
+  const int most = __reduce_max_sync(FULL, nall);
+  float M = -INFINITY, lsum = 0.f;
+  float4 acc[Q];
 #pragma unroll
-  for (int e = 0; e < EPL; ++e) acc[e] = 0.f;
-  for (int i0 = 0; i0 < nall; i0 += 32) {
-    const int i = i0 + lane;
-    float w = 0.f, s = 0.f;
-    if (i < nall) {
-      const float2 x = i < np ? p.pp.ml[prec + i * pstep] : p.po.ml[orec + (int64_t)(i - np) * p.G];
-      w = x.x == -INFINITY ? 0.f : tc::ex2(x.x - M);
-      s = w * x.y;
-    }
-    lsum += warp_sum(s);
-    const int nn = min(32, nall - i0);
-    for (int j = 0; j < nn; ++j) {
-      const float wj = __shfl_sync(FULL, w, j);
-      if (wj == 0.f) continue;
-      const int k = i0 + j;
-      const float* r = k < np ? p.pp.o + (prec + k * pstep) * D : p.po.o + (orec + (int64_t)(k - np) * p.G) * D;
-      float v[EPL];
-      if constexpr (EPL == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(r + lane * 4);
-        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-      } else {
-        const float2 x = *reinterpret_cast<const float2*>(r + lane * 2);
-        v[0] = x.x; v[1] = x.y;
+  for (int q = 0; q < Q; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = grp * 8; i0 - grp * 8 < most; i0 += 8 * GR) {
+    const int i = i0 + sub;
+    float2 x = make_float2(-INFINITY, 0.f);
+    if (i < nall) x = i < np ? p.pp.ml[prec + (int64_t)i * pstep] : p.po.ml[orec + (int64_t)(i - np) * p.G];
+    float Mn = fmaxf(M, x.x);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) Mn = fmaxf(Mn, __shfl_xor_sync(FULL, Mn, o));
+    const float ref = Mn == -INFINITY ? 0.f : Mn;
+    const float old = tc::ex2(M - ref);         // 0 while nothing was seen
+    M = Mn;
+    const float w = tc::ex2(x.x - ref);         // 0 for a record without weight
+    float s = w * x.y;
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(FULL, s, o);
+    lsum = fmaf(lsum, old, s);
+#pragma unroll
+    for (int q = 0; q < Q; ++q) acc[q] = make_float4(acc[q].x * old, acc[q].y * old, acc[q].z * old, acc[q].w * old);
+    const int nn = min(8, most - (i0 - grp * 8));   // the same in all groups: the shuffles want every lane
+    for (int j0 = 0; j0 < nn; j0 += 2) {        // two records at a time
+      float4 v[2][Q];
+      float wj[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        wj[j] = __shfl_sync(FULL, w, (lane & 24) + ((j0 + j) & 7));
+        const int k = i0 + j0 + j;
+        const float4* r = reinterpret_cast<const float4*>(k < np ? p.pp.o + (prec + (int64_t)k * pstep) * D
+                                                                 : p.po.o + (orec + (int64_t)(k - np) * p.G) * D);
+#pragma unroll
+        for (int q = 0; q < Q; ++q) v[j][q] = wj[j] > 0.f ? r[q * 8 + sub] : make_float4(0.f, 0.f, 0.f, 0.f);
       }
 #pragma unroll
-      for (int e = 0; e < EPL; ++e) acc[e] = fmaf(v[e], wj, acc[e]);
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+          acc[q].x = fmaf(v[j][q].x, wj[j], acc[q].x);
+          acc[q].y = fmaf(v[j][q].y, wj[j], acc[q].y);
+          acc[q].z = fmaf(v[j][q].z, wj[j], acc[q].z);
+          acc[q].w = fmaf(v[j][q].w, wj[j], acc[q].w);
+        }
     }
   }
-  const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
-  float* o = p.o + (int64_t)wid * D + lane * EPL;
+  if (GR > 1) {                                 // the groups' parts
 #pragma unroll
-  for (int e = 0; e < EPL; ++e) o[e] = acc[e] * inv;
-  if (p.lse && lane == 0) p.lse[(int64_t)wid * p.lse_stride] = lsum > 0.f ? (M + log2f(lsum)) * PF_LN2 : -INFINITY;
+    for (int o = 8; o < 32; o <<= 1) {
+      const float Mo = __shfl_xor_sync(FULL, M, o), Mn = fmaxf(M, Mo), ref = Mn == -INFINITY ? 0.f : Mn;
+      const float a0 = tc::ex2(M - ref), a1 = tc::ex2(Mo - ref);
+      lsum = lsum * a0 + __shfl_xor_sync(FULL, lsum, o) * a1;
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        acc[q].x = acc[q].x * a0 + __shfl_xor_sync(FULL, acc[q].x, o) * a1;
+        acc[q].y = acc[q].y * a0 + __shfl_xor_sync(FULL, acc[q].y, o) * a1;
+        acc[q].z = acc[q].z * a0 + __shfl_xor_sync(FULL, acc[q].z, o) * a1;
+        acc[q].w = acc[q].w * a0 + __shfl_xor_sync(FULL, acc[q].w, o) * a1;
+      }
+      M = Mn;
+    }
+    if (grp > 0) return;
+  }
+  if (!live) return;
+  const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
+  const int64_t out = (int64_t)bl * p.Hq + h;
+  float4* o = reinterpret_cast<float4*>(p.o + out * D);
+#pragma unroll
+  for (int q = 0; q < Q; ++q) o[q * 8 + sub] = make_float4(acc[q].x * inv, acc[q].y * inv, acc[q].z * inv, acc[q].w * inv);
+  if (p.lse && sub == 0) p.lse[out * p.lse_stride] = lsum > 0.f ? (M + log2f(lsum)) * PF_LN2 : -INFINITY;
 }
 
 static size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -306,7 +341,13 @@ size_t plan_prefix(PrefixParams& p, void* ws) {
     // (whole 64-key stages: a stage starts on a page's first token or a multiple of 64 inside it)
     p.slo = (int)(((p.max_len + ns - 1) / ns + 63) / 64 * 64);
     p.nso = (p.max_len + p.slo - 1) / p.slo;
+    p.own_mma = prefix_own_mma_supported(p);
     place(p.po, rows * p.nso * p.G);
+    if (p.own_mma) {
+      p.counter = ws ? reinterpret_cast<int*>((char*)ws + off) : nullptr;
+      off += 256;
+      p.counter_zeroed = p.Kp && p.tc;
+    }
   }
   return off;
 }
@@ -325,7 +366,7 @@ cudaError_t launch_prefix(const PrefixParams& p, cudaStream_t st) {
     }
   }
   if (p.K) {
-    if (prefix_own_mma_supported(p)) {
+    if (p.own_mma) {
       if ((e = launch_prefix_own_mma(p, st)) != cudaSuccess) return e;
     } else {
       const dim3 grid(p.B * p.L * p.Hkv, p.nso);
@@ -335,10 +376,12 @@ cudaError_t launch_prefix(const PrefixParams& p, cudaStream_t st) {
       count_launch();
     }
   }
-  const int64_t warps = (int64_t)p.B * p.L * p.Hq;
-  const unsigned blocks = (unsigned)((warps + 7) / 8);
-  if (p.d == 128) prefix_combine_kernel<128><<<blocks, 256, 0, st>>>(p);
-  else prefix_combine_kernel<64><<<blocks, 256, 0, st>>>(p);
+  const bool many = (int64_t)p.B * p.L * p.Hq >= PC_MANY;
+  const int per = PC_THREADS / (many ? 8 : 32);   // heads a CTA
+  const dim3 grid(p.B * p.L, (p.Hq + per - 1) / per);
+  auto kern = p.d == 128 ? (many ? prefix_combine_kernel<128, 1> : prefix_combine_kernel<128, 4>)
+                         : (many ? prefix_combine_kernel<64, 1> : prefix_combine_kernel<64, 4>);
+  kern<<<grid, PC_THREADS, 0, st>>>(p);
   if ((e = cudaGetLastError()) == cudaSuccess) count_launch();
   return e;
 }

@@ -38,7 +38,6 @@ using namespace tc;
 constexpr int PX_KEYS = 128;                    // keys a tile
 constexpr int PX_THREADS = 384;                 // warps 10 and 11 only complete the third warpgroup
 constexpr int PX_ATOM = PX_KEYS * 128;          // 128 rows x 64 bf16, 128B-swizzled (16 KB)
-constexpr int PX_MAXL = 128;                    // layers whose tile sums fit the shared array
 template <int D> constexpr int px_tile() { return (D / 64) * PX_ATOM; }
 template <int D, int MT> constexpr int px_nk() { return D == 64 ? 4 : (MT == 1 ? 3 : 2); }
 template <int D, int MT> constexpr int px_nv() { return D == 64 ? 4 : 3; }
@@ -48,15 +47,10 @@ struct PxCtl {
   uint32_t tmem;
   int abort;
   float bias[2][2][PX_KEYS];                    // [warpgroup][buffer]
-  int cum[PX_MAXL + 1];                         // tiles of the layers before
+  int cum[PREFIX_TC_LAYERS + 1];                         // tiles of the layers before
 };
 template <int D, int MT> constexpr size_t px_smem() {
   return (size_t)MT * px_tile<D>() + (size_t)(px_nk<D, MT>() + px_nv<D, MT>()) * px_tile<D>() + sizeof(PxCtl);
-}
-
-__device__ __forceinline__ int px_len(const PrefixParams& p, int l) {
-  const int n = p.len_p[l];
-  return n < 0 ? 0 : n > p.max_p ? p.max_p : n;
 }
 
 // A run's next piece: tiles [t0, t0 + n) of item (l, g, mp).
@@ -166,24 +160,12 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
       prefetch_map(&mapK);
       prefetch_map(&mapV);
     }
-    // tiles of the layers before each layer
-    int run = 0;
-    for (int l0 = 0; l0 < p.L; l0 += 32) {
-      const int l = l0 + lane;
-      int t = 0;
-      if (l < p.L) {
-        t = (px_len(p, l) + PX_KEYS - 1) / PX_KEYS * p.Hkv * p.mp;
-        if (blockIdx.x == 0 && px_len(p, l) != p.len_p[l]) flag(p.status, ST_BOUNDS);
-      }
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(FULL, t, o);
-        if (lane >= o) t += x;
-      }
-      if (l < p.L) c->cum[l + 1] = run + t;
-      run += __shfl_sync(FULL, t, 31);
+    prefix_tile_sums(p, c->cum);
+    if (blockIdx.x == 0) {
+      for (int l = lane; l < p.L; l += 32)
+        if (prefix_len(p, l) != p.len_p[l]) flag(p.status, ST_BOUNDS);
+      if (lane == 0 && p.counter) *p.counter = 0;   // for the own rows' kernel, next on the stream
     }
-    if (lane == 0) c->cum[0] = 0;
   }
   fence_before();
   __syncthreads();
@@ -318,7 +300,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
     uint32_t steps = 0, tc = 0, nseg = 0;
     bool ok = true;
     while (ok && run.next(p, c->cum, sg)) {
-      const int len = px_len(p, sg.l);
+      const int len = prefix_len(p, sg.l);
       const int r0 = sg.mp * (MT * 128);
       // Q of the piece: all S products of the piece before are done (both warpgroups waited for theirs)
       if (nseg > 0) {
@@ -564,7 +546,7 @@ static bool px_map(CUtensorMap* m, const char* base, int64_t sl, int64_t sh, int
 
 // bf16 queries and keys, at most 128 layers, and cache layouts a TMA map can describe.
 bool prefix_tc_supported(const PrefixParams& p) {
-  if (!p.qbf16 || !p.kbf16 || (p.d != 64 && p.d != 128) || p.L > PX_MAXL) return false;
+  if (!p.qbf16 || !p.kbf16 || (p.d != 64 && p.d != 128) || p.L > PREFIX_TC_LAYERS) return false;
   if (((uintptr_t)p.q | (uintptr_t)p.Kp | (uintptr_t)p.Vp) % 16) return false;
   int64_t s[3];
   return px_strides(s, p.Kpl, p.Kph, p.Kpt, p) && px_strides(s, p.Vpl, p.Vph, p.Vpt, p);
