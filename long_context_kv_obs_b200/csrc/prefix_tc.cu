@@ -311,18 +311,17 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
       }
       ++nseg;
       {
-        constexpr int CH = D / 8;                // 16-byte chunks a row
-        const int qr = MT == 2 ? threadIdx.x : wt;
-        const int R = r0 + qr;
-        const int c0 = MT == 2 ? 0 : w * (CH / 2), c1 = MT == 2 ? CH : c0 + CH / 2;
-        const int b = R / p.G, gg = R - b * p.G;
-        const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(p.q) +
-                                 (((int64_t)b * p.L + sg.l) * p.Hq + sg.g * p.G + gg) * D;
-        uint8_t* dst = Qs + (MT == 2 ? (qr >> 7) * TILE : 0) + (qr & 127) * 128;
+        // a warp fills 32 (MT 1: 16) of its rows, whole rows by consecutive lanes
+        constexpr int CH = D / 8, WR = 16 * MT;  // 16-byte chunks a row, rows a warp
 #pragma unroll
-        for (int ch = c0; ch < c1; ++ch) {
+        for (int x = lane; x < WR * CH; x += 32) {
+          const int qr = warp * WR + x / CH, ch = x % CH, R = r0 + qr;
+          const int b = R / p.G, gg = R - b * p.G;
+          const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(p.q) +
+                                   (((int64_t)b * p.L + sg.l) * p.Hq + sg.g * p.G + gg) * D;
           const uint4 v = R < rows ? ldg16(q + ch * 8) : make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(dst + (ch >> 3) * PX_ATOM + (((ch & 7) ^ (qr & 7)) << 4)) = v;
+          *reinterpret_cast<uint4*>(Qs + (qr >> 7) * TILE + (ch >> 3) * PX_ATOM + (qr & 127) * 128 +
+                                    (((ch & 7) ^ (qr & 7)) << 4)) = v;
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
@@ -489,9 +488,26 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
         if (live) {
           p.pp.ml[rec] = make_float2(m, lsum);
           px_add_o<D>(tO, acc);
+          // rows to memory through the Q area, whose products are all done (this warpgroup's last o_ready
+          // came behind them): a lane storing its own row, 16 bytes here and there, took 40k cycles a piece
+          constexpr int CC = D / 4;              // dimensions at a time
+          uint8_t* stage = Qs + warp * (32 * CC * 4);
+          float* dst = p.pp.o + group * 128 * D + (int64_t)((warp & 3) * 32) * D;
 #pragma unroll
-          for (int k = 0; k < D; k += 4)
-            *reinterpret_cast<float4*>(p.pp.o + rec * D + k) = make_float4(acc[k], acc[k + 1], acc[k + 2], acc[k + 3]);
+          for (int d0 = 0; d0 < D; d0 += CC) {
+#pragma unroll
+            for (int k = 0; k < CC / 4; ++k)
+              *reinterpret_cast<float4*>(stage + lane * CC * 4 + ((k ^ (lane & (CC / 4 - 1))) << 4)) =
+                  make_float4(acc[d0 + 4 * k], acc[d0 + 4 * k + 1], acc[d0 + 4 * k + 2], acc[d0 + 4 * k + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int x = lane; x < 32 * (CC / 4); x += 32) {
+              const int r = x / (CC / 4), k = x % (CC / 4);
+              const float4 v = *reinterpret_cast<const float4*>(stage + r * CC * 4 + ((k ^ (r & (CC / 4 - 1))) << 4));
+              *reinterpret_cast<float4*>(dst + (int64_t)r * D + d0 + 4 * k) = v;
+            }
+            __syncwarp();
+          }
         }
         fence_before();
       } else if (live) {
