@@ -36,7 +36,7 @@ constexpr int PO_ATOM = PO_KEYS * 128;          // 64 rows x 64 bf16 (8 KB)
 constexpr int PO_PER_SM = 2;
 template <int D> constexpr int po_stage() { return 2 * (D / 64) * PO_ATOM; }
 
-constexpr int PO_Q = 4;                         // items handed on at a time
+constexpr int PO_Q = 2;                         // items handed on at a time
 
 struct PoArgs {
   PrefixParams p;
@@ -44,8 +44,8 @@ struct PoArgs {
 };
 struct PoCtl {
   uint64_t full[6], empty[6];
-  uint64_t q_full[PO_Q], q_empty[PO_Q], merge_ready, merge_done;
-  int item[PO_Q];
+  uint64_t q_full[PO_Q], q_empty[PO_Q], upper, second, merged;
+  int item[PO_Q], len[PO_Q];                    // an item and its row's length; its queries lie behind
   int abort;
 };
 
@@ -59,7 +59,8 @@ prefix_own_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
   extern __shared__ __align__(1024) uint8_t po_raw[];
   uint8_t* ring = po_raw;
   PoCtl* c = reinterpret_cast<PoCtl*>(ring + (size_t)NST * STAGE);
-  float* dsm = reinterpret_cast<float*>(c + 1);   // [CW][G][REC]
+  uint8_t* qbuf = ring + (size_t)NST * STAGE + ((sizeof(PoCtl) + 127) & ~(size_t)127);   // [PO_Q][G][D]
+  float* dsm = reinterpret_cast<float*>(qbuf + (size_t)PO_Q * p.G * D * 2);              // [2][G][REC]
   uint64_t *full = c->full, *empty = c->empty;
   volatile int* abort = &c->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -72,8 +73,9 @@ prefix_own_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
       mbar_init(&c->q_full[q], 1);
       mbar_init(&c->q_empty[q], PO_CW);
     }
-    mbar_init(&c->merge_ready, PO_CW);
-    mbar_init(&c->merge_done, PO_CW);
+    mbar_init(&c->upper, 2);
+    mbar_init(&c->second, 1);
+    mbar_init(&c->merged, 1);
     c->abort = 0;
     fence_mbar_init();
   }
@@ -96,19 +98,31 @@ prefix_own_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
     int drawn = lane == 0 ? atomicAdd(p.counter, 1) : 0;
     while (ok) {
       const int item = __shfl_sync(FULL, drawn, 0);
+      const bool last = item >= a.nitems;
+      const int row = last ? 0 : item / p.nso, split = item - row * p.nso;
+      const int bl = row / p.Hkv, g = row - bl * p.Hkv, b = bl / p.L, l = bl - b * p.L;
+      const int n = row_len(bl);
       if (lane == 0) {
+        // the item, its length and its queries (G rows, one after the other) to the consumers
         const int q = nq % PO_Q;
         ok = mbar_wait(&c->q_empty[q], ((nq / PO_Q) & 1) ^ 1, abort, p.status);
-        c->item[q] = item;
-        if (ok) mbar_arrive(&c->q_full[q]);
+        if (ok) {
+          const uint32_t bytes = p.G * D * 2;
+          c->item[q] = item;
+          c->len[q] = n;
+          if (last) {
+            mbar_arrive(&c->q_full[q]);
+          } else {
+            drawn = atomicAdd(p.counter, 1);    // the next one, while this one is loaded
+            mbar_expect_tx(&c->q_full[q], bytes);
+            bulk_load(qbuf + q * bytes, reinterpret_cast<const char*>(p.q) + ((int64_t)bl * p.Hq + g * p.G) * D * 2, bytes,
+                      &c->q_full[q]);
+          }
+        }
       }
       ++nq;
       ok = __shfl_sync(FULL, (int)ok, 0) != 0;
-      if (!ok || item >= a.nitems) break;
-      if (lane == 0) drawn = atomicAdd(p.counter, 1);   // the next one, while this one is loaded
-      const int row = item / p.nso, split = item - row * p.nso;
-      const int bl = row / p.Hkv, g = row - bl * p.Hkv, b = bl / p.L, l = bl - b * p.L;
-      const int n = row_len(bl);
+      if (!ok || last) break;
       const int s0 = split * p.slo, s1 = min(n, s0 + p.slo);
       const int32_t* trow = paged ? p.table + b * p.tsb + l * p.tsl : nullptr;
       int ent = 0, ent0 = -1;                   // entries ent0 .. ent0 + 31 of the table, one a lane
@@ -151,7 +165,9 @@ prefix_own_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
     }
     if (*abort && lane == 0) {                  // copies in flight end before shared memory is given up
       int none = 0;
-      const uint32_t issued = chunk;
+      const uint32_t issued = chunk, sent = nq;
+      for (uint32_t j = sent > PO_Q ? sent - PO_Q : 0; j < sent; ++j)
+        mbar_wait(&c->q_full[j % PO_Q], (j / PO_Q) & 1, &none, p.status);
       for (uint32_t j = issued > (uint32_t)NST ? issued - NST : 0; j < issued; ++j)
         mbar_wait(&full[j % NST], (j / NST) & 1, &none, p.status);
     }
@@ -166,28 +182,26 @@ prefix_own_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
     const int q = nq % PO_Q;
     bool fine = mbar_wait(&c->q_full[q], (nq / PO_Q) & 1, abort, p.status);
     if (!__all_sync(FULL, fine)) break;
-    const int item = c->item[q];
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&c->q_empty[q]);
+    const int item = c->item[q], n = c->len[q];
     if (item >= a.nitems) break;
-    const int row = item / p.nso, split = item - row * p.nso;
-    const int bl = row / p.Hkv, g = row - bl * p.Hkv;
-    const int n = row_len(bl);
-    const int s0 = split * p.slo, s1 = min(n, s0 + p.slo);
-    if (cw == 0 && lane == 0 && split == 0 && n != p.len[bl]) flag(p.status, ST_BOUNDS);
-    const int64_t rec0 = ((int64_t)row * p.nso + split) * G;
-    if (s0 >= s1) {                  // nothing here: records of no weight
-      if (cw == 0 && lane < G) p.po.ml[rec0 + lane] = make_float2(-INFINITY, 0.f);
-      continue;
-    }
     uint32_t qa[D / 16][2];
     {
-      const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(p.q) + ((int64_t)bl * p.Hq + g * G + gid) * D;
+      const uint8_t* qr = qbuf + (size_t)q * G * D * 2 + (size_t)gid * D * 2;
 #pragma unroll
       for (int kc = 0; kc < D / 16; ++kc) {
-        qa[kc][0] = gid < G ? __ldg(reinterpret_cast<const uint32_t*>(q + kc * 16 + 2 * tig)) : 0u;
-        qa[kc][1] = gid < G ? __ldg(reinterpret_cast<const uint32_t*>(q + kc * 16 + 8 + 2 * tig)) : 0u;
+        qa[kc][0] = gid < G ? *reinterpret_cast<const uint32_t*>(qr + (kc * 16 + 2 * tig) * 2) : 0u;
+        qa[kc][1] = gid < G ? *reinterpret_cast<const uint32_t*>(qr + (kc * 16 + 8 + 2 * tig) * 2) : 0u;
       }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&c->q_empty[q]);
+    const int row = item / p.nso, split = item - row * p.nso;
+    const int s0 = split * p.slo, s1 = min(n, s0 + p.slo);
+    if (cw == 0 && lane == 0 && split == 0 && n != p.len[row / p.Hkv]) flag(p.status, ST_BOUNDS);
+    const int64_t rec0 = ((int64_t)row * p.nso + split) * G;
+    if (s0 >= s1) {                             // nothing here: records of no weight
+      if (cw == 0 && lane < G) p.po.ml[rec0 + lane] = make_float2(-INFINITY, 0.f);
+      continue;
     }
     float O[D / 8][4];
 #pragma unroll
@@ -278,41 +292,60 @@ prefix_own_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
     if (!fine) break;
     lsum += __shfl_xor_sync(FULL, lsum, 1);
     lsum += __shfl_xor_sync(FULL, lsum, 2);
-    // the records of the item before have been read
-    if (merges > 0) fine = mbar_wait(&c->merge_done, (merges - 1) & 1, abort, p.status);
-    if (!__all_sync(FULL, fine)) break;
-    if (gid < G) {
-      float* r = dsm + ((size_t)cw * G + gid) * REC;
-      if (tig == 0) {
-        r[D] = m;
-        r[D + 1] = lsum;
-      }
+    // warps 2 and 3 hand their state to 0 and 1, warp 1 its own to 0, which writes the record; the
+    // others go on to the next item
+    auto hand = [&](int slot) {
+      if (gid < G) {
+        float* r = dsm + ((size_t)slot * G + gid) * REC;
+        if (tig == 0) *reinterpret_cast<float2*>(r + D) = make_float2(m, lsum);
 #pragma unroll
-      for (int t = 0; t < D / 8; ++t)
-        *reinterpret_cast<float2*>(r + t * 8 + 2 * tig) = make_float2(O[t][0], O[t][1]);
+        for (int t = 0; t < D / 8; ++t) *reinterpret_cast<float2*>(r + t * 8 + 2 * tig) = make_float2(O[t][0], O[t][1]);
+      }
+      __syncwarp();
+    };
+    auto take = [&](int slot) {
+      if (gid < G) {
+        const float* r = dsm + ((size_t)slot * G + gid) * REC;
+        const float2 x = *reinterpret_cast<const float2*>(r + D);
+        const float M = fmaxf(m, x.x), ref = M == -INFINITY ? 0.f : M, a0 = ex2(m - ref), a1 = ex2(x.x - ref);
+        m = M;
+        lsum = lsum * a0 + x.y * a1;
+#pragma unroll
+        for (int t = 0; t < D / 8; ++t) {
+          const float2 y = *reinterpret_cast<const float2*>(r + t * 8 + 2 * tig);
+          O[t][0] = O[t][0] * a0 + y.x * a1;
+          O[t][1] = O[t][1] * a0 + y.y * a1;
+        }
+      }
+      __syncwarp();
+    };
+    if (cw >= 2) {
+      // the slots of the item before have been read
+      if (merges > 0) fine = mbar_wait(&c->merged, (merges - 1) & 1, abort, p.status);
+      if (!__all_sync(FULL, fine)) break;
+      hand(cw - 2);
+      if (lane == 0) mbar_arrive(&c->upper);
+    } else {
+      fine = mbar_wait(&c->upper, merges & 1, abort, p.status);
+      if (!__all_sync(FULL, fine)) break;
+      take(cw);
+      if (cw == 1) {
+        hand(1);
+        if (lane == 0) mbar_arrive(&c->second);
+      } else {
+        fine = mbar_wait(&c->second, merges & 1, abort, p.status);
+        if (!__all_sync(FULL, fine)) break;
+        take(1);
+        if (lane == 0) mbar_arrive(&c->merged);
+        if (gid < G) {
+          if (tig == 0) p.po.ml[rec0 + gid] = make_float2(m, lsum);
+          float* o = p.po.o + (rec0 + gid) * D + 2 * tig;
+#pragma unroll
+          for (int t = 0; t < D / 8; ++t) *reinterpret_cast<float2*>(o + t * 8) = make_float2(O[t][0], O[t][1]);
+        }
+      }
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&c->merge_ready);
-    fine = mbar_wait(&c->merge_ready, merges & 1, abort, p.status);
-    if (!__all_sync(FULL, fine)) break;
     ++merges;
-    for (int t = threadIdx.x - 32; t < G * D; t += PO_CW * 32) {
-      const int gg = t / D, e = t % D;
-      float M = -INFINITY, v = 0.f, ls = 0.f;
-#pragma unroll
-      for (int w = 0; w < PO_CW; ++w) M = fmaxf(M, dsm[((size_t)w * G + gg) * REC + D]);
-#pragma unroll
-      for (int w = 0; w < PO_CW; ++w) {
-        const float* r = dsm + ((size_t)w * G + gg) * REC;
-        const float sc = M == -INFINITY ? 0.f : ex2(r[D] - M);
-        v += r[e] * sc;
-        ls += r[D + 1] * sc;
-      }
-      p.po.o[(rec0 + gg) * D + e] = v;
-      if (e == 0) p.po.ml[rec0 + gg] = make_float2(M, ls);
-    }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&c->merge_done);
   }
 }
 
@@ -329,10 +362,7 @@ static PFN_cuTensorMapEncodeTiled_v12000 po_encode() {
   return fn;
 }
 
-static int po_box(const PrefixParams& p) {
-  const int page = 1 << p.shift;
-  return p.table && page < PO_KEYS ? page : PO_KEYS;
-}
+static int po_box(const PrefixParams&) { return 16; }
 
 // Byte strides of the 5-D map below; a dimension of extent 1 gets its inner neighbour's.
 static bool po_strides(int64_t (&s)[4], int64_t sb, int64_t sl, int64_t sh, int64_t st, const PrefixParams& p) {
@@ -379,8 +409,9 @@ static cudaError_t launch_po(const PrefixParams& p, const CUtensorMap& mk, const
   int dev = 0, smem_sm = 0;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&smem_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev);
-  // two CTAs an SM, as many stages (at most 6) as fit beside the merge records (1 KB a CTA is the runtime's)
-  const size_t fixed = sizeof(PoCtl) + (size_t)PO_CW * p.G * (D + 2) * 4;
+  // two CTAs an SM, as many stages (at most 6) as fit beside the queries and merge records (1 KB a CTA is
+  // the runtime's)
+  const size_t fixed = ((sizeof(PoCtl) + 127) & ~(size_t)127) + (size_t)PO_Q * p.G * D * 2 + (size_t)2 * p.G * (D + 2) * 4;
   const long long room = (long long)smem_sm / PO_PER_SM - 1024 - (long long)fixed;
   a.nst = (int)(room / po_stage<D>());
   if (a.nst > 6) a.nst = 6;
