@@ -1,4 +1,4 @@
-"""Host orchestration of the six libkvc calls for the two workloads.
+"""Host orchestration of the libkvc calls for the workloads.
 
 * ``PrefillCompressor``: one-shot compression after prefill - kvc_score ->
   kvc_select -> kvc_compact (optionally kvc_merge), all buffers and
@@ -7,12 +7,15 @@
   sequences - every step appends one token (K, V and its H / D signals) and
   attends with kvc_decode_attn; every ``period`` generated tokens the batch is
   recompressed with kvc_recompress into a ping-pong buffer.
+* ``SharedPromptBatch``: a batch that answers from one compressed prompt - page
+  tables, append into pages, shared-prompt attention and sampling per step.
 
 Nothing here computes on the host: it sizes buffers and launches the calls in
 order on the current stream.
 """
 from __future__ import annotations
 
+import contextlib
 import math
 from typing import Optional
 
@@ -317,3 +320,72 @@ class DecodeTimeCompressor:
         self.len = keep
         self.lse_streak = 0          # the ring's statistics describe the cache before this call
         return keep
+
+
+class SharedPromptBatch:
+    """A batch of sequences that answer from one compressed prompt.
+
+    The prompt's cache K, V [L][Hkv][k_cap][d] with k [L] rows in use (kvc_select's k_out, e.g. a
+    PrefillCompressor's Kc, Vc, k and R) is held once; what a sequence generates lives in pages of
+    `page` tokens of one (sequence, layer) row, out of a pool of n_pages.  A step is
+    kvc_page_tables -> kvc_page_append -> kvc_prefix_decode_attn, and kvc_sample takes the next token
+    from the step's logits.  Every buffer is allocated here, so a step only enqueues kernels and can be
+    captured into a graph (after one step outside of it).
+    """
+
+    def __init__(self, m, K_prompt, V_prompt, k, *, batch: int, n_pages: int, max_len: int, page: int = 16,
+                 max_len_prompt: Optional[int] = None, R=None, alpha_c: float = 1.0, scale: float = 0.0):
+        dev, dt = K_prompt.device, K_prompt.dtype
+        L, Hq, Hkv, d = m.n_layers, m.n_q_heads, m.n_kv_heads, m.head_dim
+        i32, f32 = torch.int32, torch.float32
+        self.m, self.batch, self.page, self.max_len = m, batch, page, max_len
+        self.Kp, self.Vp, self.k, self.R, self.alpha_c, self.scale = K_prompt, V_prompt, k, R, alpha_c, scale
+        self.max_len_prompt = K_prompt.shape[2] if max_len_prompt is None else max_len_prompt
+        self.K = torch.zeros(n_pages, Hkv, page, d, dtype=dt, device=dev)
+        self.V = torch.zeros(n_pages, Hkv, page, d, dtype=dt, device=dev)
+        self.table = torch.full((batch, L, -(-max_len // page)), -1, dtype=i32, device=dev)
+        self.lens = torch.zeros(batch, L, dtype=i32, device=dev)
+        self.lens_next = torch.zeros_like(self.lens)
+        self.ring = torch.arange(n_pages, dtype=i32, device=dev)
+        self.state = torch.tensor([0, n_pages], dtype=i32, device=dev)     # head, free pages
+        self.slots = torch.empty(batch * L, dtype=i32, device=dev)
+        self.slot_start = torch.empty(batch * L + 1, dtype=i32, device=dev)
+        self.o = torch.empty(batch, L, Hq, d, dtype=f32, device=dev)
+        self.lse = torch.empty(batch, L, Hq, dtype=f32, device=dev)
+        self.token = torch.empty(batch, dtype=i32, device=dev)
+        self.logprob = torch.empty(batch, dtype=f32, device=dev)
+        self.ws_tables = torch.empty(256, dtype=torch.uint8, device=dev)
+        self.ws_attn = None
+
+    def resize(self, lens_new, slots=None, slot_start=None, stream=None):
+        """The rows go from their lengths to lens_new [batch][L]: pages are taken from or given back to
+        the ring (a sequence that ends: 0), slots receives the new tokens' slots."""
+        B.kvc_page_tables(lens=self.lens, lens_new=lens_new, table=self.table, ring=self.ring, state=self.state,
+                          page=self.page, lens_out=self.lens, slots=slots, slot_start=slot_start,
+                          workspace=self.ws_tables, stream=stream)
+
+    def append(self, k, v, stream=None):
+        """One generated token per sequence, k and v [batch][L][Hkv][d], into every layer's pages."""
+        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+            torch.add(self.lens, 1, out=self.lens_next)
+        self.resize(self.lens_next, self.slots, self.slot_start, stream)
+        B.kvc_page_append(self.m, k=k.flatten(0, 1), v=v.flatten(0, 1), K=self.K, V=self.V, slots=self.slots, stream=stream)
+
+    def attend(self, q, stream=None):
+        """o [batch][L][Hq][d] (and self.lse) of q over the prompt and the sequences' own rows."""
+        self.ws_attn = B.kvc_prefix_decode_attn(
+            self.m, q=q, K_prefix=self.Kp, V_prefix=self.Vp, lens_prefix=self.k, max_len_prefix=self.max_len_prompt,
+            R=self.R, alpha_c=self.alpha_c, scale=self.scale, K=self.K, V=self.V, table=self.table, lens=self.lens,
+            max_len=self.max_len, o=self.o, lse=self.lse, workspace=self.ws_attn, stream=stream)
+        return self.o
+
+    def step(self, q, k, v, stream=None):
+        """append, then attend."""
+        self.append(k, v, stream)
+        return self.attend(q, stream)
+
+    def sample(self, logits, u, stream=None, **par):
+        """The sequences' next tokens [batch] from their logits [batch][V] (par: temperature, top_k,
+        top_p, min_p, each [batch])."""
+        B.kvc_sample(logits=logits, u=u, token=self.token, logprob=self.logprob, stream=stream, **par)
+        return self.token
