@@ -774,20 +774,21 @@ def page_tables_args(*, lens, lens_new, table, ring, state, page: int, state_out
     """Argument struct of kvc_page_tables."""
     _one_device(lens, lens_new, table, ring, state, state_out, lens_out, slots, slot_start)
     rows = lens.numel()
-    tb = table.flatten(0, -2) if table.dim() > 2 and table.is_contiguous() else table
-    if tb.dtype != torch.int32 or tb.dim() != 2 or tb.shape[0] != rows or tb.stride(1) != 1:
+    sh = table.shape
+    if len(sh) > 2 and table.is_contiguous():
+        n, s_row, one = table.numel() // sh[-1] if sh[-1] else 0, sh[-1], True
+    else:
+        st = table.stride()
+        n, s_row, one = (sh[0], st[0], st[1] == 1) if len(sh) == 2 else (-1, 0, False)
+    if table.dtype is not torch.int32 or n != rows or not one:
         raise ValueError("table must be int32 with one row of entries per length (more than two dimensions: contiguous)")
-    a = PageTablesArgs()
-    a.rows, a.page, a.n_pages, a.max_pages = rows, page, ring.numel(), tb.shape[1]
-    a.len, a.len_new = _flat(lens, "lens", torch.int32, rows), _flat(lens_new, "lens_new", torch.int32, rows)
-    a.table, a.table_s_row = tb.data_ptr(), tb.stride(0) if rows > 1 else tb.shape[1]
-    a.ring, a.state = _flat(ring, "ring", torch.int32, ring.numel()), _flat(state, "state", torch.int32, 2)
-    a.state_out = a.state if state_out is None else _flat(state_out, "state_out", torch.int32, 2)
-    a.len_out = _flat(lens_out, "lens_out", torch.int32, rows)
-    if slots is not None:
-        a.slots, a.slots_cap = _flat(slots, "slots", torch.int32, slots.numel()), slots.numel()
-    a.slot_start = _flat(slot_start, "slot_start", torch.int32, rows + 1)
-    return a
+    i32, n_pages, n_slots = torch.int32, ring.numel(), slots.numel() if slots is not None else 0
+    at = _flat(state, "state", i32, 2)
+    return PageTablesArgs(
+        rows, page, n_pages, sh[-1], _flat(lens, "lens", i32, rows), _flat(lens_new, "lens_new", i32, rows),
+        table.data_ptr(), s_row if rows > 1 else sh[-1], _flat(ring, "ring", i32, n_pages), at,
+        at if state_out is None else _flat(state_out, "state_out", i32, 2), _flat(lens_out, "lens_out", i32, rows),
+        _flat(slots, "slots", i32, n_slots), n_slots, _flat(slot_start, "slot_start", i32, rows + 1))
 
 
 def kvc_page_tables(*, workspace=None, stream=None, **kw):
@@ -797,7 +798,10 @@ def kvc_page_tables(*, workspace=None, stream=None, **kw):
     unless state_out is given, lens_out (may be lens) receives lens_new, slots the new tokens'
     slots, slot_start [rows + 1] where each row's begin.  Returns the workspace (None out of place)."""
     a = page_tables_args(**kw)
-    ws, need = _own_ws(OP_PAGE_TABLES, None, a, workspace, kw["lens"].device, stream)
+    if workspace is None and a.state_out != a.state and a.len_out not in (a.len, a.len_new):
+        ws, need = None, 0                    # out of place (the library has the last word)
+    else:
+        ws, need = _own_ws(OP_PAGE_TABLES, None, a, workspace, kw["lens"].device, stream)
     _check(lib().kvc_page_tables(C.byref(a), ws.data_ptr() if ws is not None else None, need, _raw_stream(stream)))
     return ws
 

@@ -216,7 +216,6 @@ struct PageTablesParams {
   const int32_t* state; int32_t* state_out;
   int32_t* len_out; int32_t* slots; int slots_cap; int32_t* slot_start;
   int32_t* commit;                          // [3] verdict, head, count for page_commit_kernel; NULL: out of place
-  int rows_per_cta;                         // set by the launcher
   unsigned* status;
 };
 cudaError_t launch_page_tables(const PageTablesParams& p, cudaStream_t st);
