@@ -48,13 +48,18 @@ namespace cg = cooperative_groups;
 constexpr int SP_THREADS = 512;
 constexpr int SP_WARPS = SP_THREADS / 32;
 constexpr int SP_BINS = 512;
+constexpr int SP_WIDE = 2048;                   // bins of a count by bf16 keys
 constexpr int SP_MAXC = 16;
 constexpr int SP_LIST = 4096;                   // candidates that one CTA sorts
 constexpr float SP_ONE = 8388608.f;             // 2^23: adding it leaves the rounded integer in a float's low bits
 
 struct alignas(16) SpShared {                   // the slice follows: its vectors are 16-byte aligned
   union {
-    unsigned hist[2][2 * SP_BINS];              // two searches deep: counts or masses; two 16-bit limbs of a mass
+    struct {
+      unsigned hist[2][2 * SP_BINS];            // two searches deep: counts or masses; two 16-bit limbs of a mass
+      unsigned wide[2][SP_WIDE];                // two searches deep: counts by key
+      unsigned total[SP_WIDE];                  // the cluster's, of the last such search
+    };
     unsigned long long list[SP_LIST];
   };
   uint2 table[256];                             // 2^(j / 256): in 2^-30 units, and as an fp32
@@ -289,6 +294,108 @@ __device__ __noinline__ int sp_border(int kind, double target, int C, int rank, 
   return b;
 }
 
+// Bins of the bf16 values from a row's maximum down to `low`, one to a value: bin o(max) - o(z), where o
+// is the value's bits below the sign, signed.  Values near zero have the most bits for the least
+// difference: where the span is more than SP_WIDE, magnitudes up to `k0` bits share the bin o = 0.
+struct SpWide {
+  int k0, omax, n;
+  __device__ __forceinline__ int order(float z) const {
+    const int b = (int)(__float_as_uint(z) >> 16), m = max((b & 0x7fff) - k0, 0);
+    return b & 0x8000 ? -m : m;
+  }
+  __device__ __forceinline__ SpWide(float zmax, float low) {   // both bf16 values, low <= zmax
+    const int mz = (int)(__float_as_uint(zmax) >> 16) & 0x7fff, ml = (int)(__float_as_uint(low) >> 16) & 0x7fff;
+    const bool across = zmax >= 0.f && low < 0.f;
+    const int big = max(mz, ml), less = min(mz, ml);
+    k0 = 0;
+    if (across && mz + ml + 1 > SP_WIDE) k0 = (mz + ml + 2 - SP_WIDE) / 2;
+    if (across ? k0 > less : big - less + 1 > SP_WIDE) k0 = big + 1 - SP_WIDE;
+    omax = order(zmax);
+    n = omax - order(low) + 1;
+  }
+  __device__ __forceinline__ SpWide() {}
+  __device__ __forceinline__ static float of_order(int o) {    // k0 counted in
+    return __uint_as_float((uint32_t)(o < 0 ? 0x8000 - o : o) << 16);
+  }
+  __device__ __forceinline__ bool single(int b) const { return b != omax || k0 == 0; }
+  __device__ __forceinline__ float high(int b) const {
+    const int o = omax - b;
+    return of_order(o < 0 ? o - k0 : o + k0);
+  }
+  __device__ __forceinline__ float low(int b) const {
+    const int o = omax - b;
+    return of_order(o > 0 ? o + k0 : o - k0);
+  }
+  __device__ __forceinline__ float middle(int b) const { return omax == b ? 0.f : high(b); }
+};
+// The first of these bins at which the cluster's counts (mass: masses, to fp64 except in a bin of several
+// values, taken at its middle) reach `target`, a share of their sum for masses, or the last that holds
+// something: returned, with the sum before it in found[0] and all of them in found[1].  A thread has four bins.
+__device__ __noinline__ int sp_wide_border(bool mass, double target, int C, int rank, int buf, SpWide wd, float zmax,
+                                           float zlow, double c) {
+  static_assert(SP_WIDE == 4 * SP_THREADS, "four bins a thread");
+  cg::cluster_group cl = cg::this_cluster();
+  SpShared& sh = sp_sh();
+  cl.sync();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b0 = 4 * threadIdx.x;
+  uint4 h = make_uint4(0, 0, 0, 0);
+  if (b0 < wd.n) {
+#pragma unroll
+    for (int r = 0; r < SP_MAXC; ++r)
+      if (r < C) {
+        const uint4 x = *reinterpret_cast<const uint4*>(cl.map_shared_rank(&sh.wide[buf][b0], (rank + r) & (C - 1)));
+        h.x += x.x;
+        h.y += x.y;
+        h.z += x.z;
+        h.w += x.w;
+      }
+    *reinterpret_cast<uint4*>(sh.total + b0) = h;
+  }
+  double v[4], sum = 0.0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const unsigned cnt = (&h.x)[i];
+    v[i] = (double)cnt;
+    if (mass && cnt) v[i] *= sp_weight(fminf(wd.middle(b0 + i), zmax), zmax, zlow, c, 0);
+    sum += v[i];
+  }
+  const double2 sc = sp_block_scan(sum);
+  if (mass) target *= sc.y;
+  int at = INT_MAX, end = -1;
+  double run = sc.x, before = 0.0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (v[i] > 0.0) {
+      end = b0 + i;
+      if (at == INT_MAX && run + v[i] >= target) {
+        at = b0 + i;
+        before = run;
+      }
+    }
+    run += v[i];
+  }
+  int first = __reduce_min_sync(FULL, at), last = __reduce_max_sync(FULL, end);
+  if (lane == 0) {
+    sh.cand[warp][0] = first;
+    sh.cand[warp][1] = last;
+  }
+  __syncthreads();
+  first = __reduce_min_sync(FULL, sh.cand[lane & (SP_WARPS - 1)][0]);
+  last = __reduce_max_sync(FULL, sh.cand[lane & (SP_WARPS - 1)][1]);
+  const int b = first == INT_MAX ? max(last, 0) : first;
+  if (b >> 2 == (int)threadIdx.x) {
+    if (first == INT_MAX) {
+      before = sc.x;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) before += b0 + i < b ? v[i] : 0.0;
+    }
+    sh.found[0] = before;
+    sh.found[1] = sc.y;
+  }
+  __syncthreads();
+  return b;
+}
+
 template <typename T>
 struct SpRow {
   static constexpr int N = SpVec<T>::N, KS = SpVec<T>::KSHIFT;
@@ -389,21 +496,65 @@ struct SpRow {
         });
   }
 
-  // Within bin b0 (of the tokens left by top-k), the key at which the count (mass: the mass, in units
-  // of 2^-(31 + e)) reaches `need`, and the index of the last tie that stays.  False if the bin holds
-  // less than that (then nothing else is set).
-  __device__ __forceinline__ bool refine(bool mass, int b0, double need, int e, uint32_t& tkey, int& tidx) {
+  // Counts of the tokens left, by bins of one bf16 value each (of zero's neighbours, see SpWide).
+  __device__ __forceinline__ void wide_hist(const SpWide& wd) const {
+    unsigned* h = sp_sh().wide[search & 1];
+    *reinterpret_cast<uint4*>(h + 4 * threadIdx.x) = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    if (cut) {
+#pragma unroll 1
+      for (int v = threadIdx.x; v < nvec; v += SP_THREADS)
+        each<4>(v, [&](float z, int idx) {
+          const int b = wd.omax - wd.order(z);
+          if (b < wd.n && left(z, idx)) atomicAdd(h + b, 1u);
+        });
+      return;
+    }
+    const uint32_t less = (uint32_t)(-wd.k0 & 0xffff) * 0x10001u;
+    // (-infinity lies beyond the last bin)
+#pragma unroll 1
+    for (int v = threadIdx.x; v < nvec; v += SP_THREADS) {
+      const uint4 u = sp_slice()[v];
+      const bool same = u.x == u.y && u.z == u.w && u.x == u.z && u.x >> 16 == (u.x & 0xffffu);   // flat rows
+      const uint32_t* w = &u.x;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i == 0 || !same) {
+          const uint32_t m = __viaddmax_s16x2_relu(w[i] & 0x7fff7fffu, less, 0u);
+          const int m0 = (int)(m & 0xffffu), m1 = (int)(m >> 16);
+          const int c0 = w[i] & 0x8000u ? wd.omax + m0 : wd.omax - m0, c1 = (int)w[i] < 0 ? wd.omax + m1 : wd.omax - m1;
+          if (c0 < wd.n) atomicAdd(h + c0, same ? 8u : 1u);
+          if (c1 < wd.n && !same) atomicAdd(h + c1, 1u);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ int wide_border(bool mass, double target, const SpWide& wd) {
+    const int b = sp_wide_border(mass, target, C, rank, search & 1, wd, zmax, zlow, c);
+    ++search;
+    return b;
+  }
+
+  // Of the values zl to zh (b0 >= 0: those of bin b0 alone) that top-k left, the key at which the count
+  // (mass: the mass, in units of 2^-(31 + e)) reaches `need`, and the index of the last tie that stays.
+  // False if there is less than that (then nothing else is set).  known >= 0: zl is zh, and so many there are.
+  __device__ __forceinline__ bool refine(bool mass, float zl, float zh, int b0, int known, double need, int e,
+                                         uint32_t& tkey, int& tidx) {
     SpShared& sh = sp_sh();
-    uint32_t hi = sp_key(edge_high(b0), KS), lo = max(sp_key(edge_low(b0), KS), sp_key(-INFINITY, KS) + 1u);
+    uint32_t hi = sp_key(zh, KS), lo = max(sp_key(zl, KS), sp_key(-INFINITY, KS) + 1u);
     double above = 0.0, value = 0.0;
     bool first_search = true;
     int shift = 0;
+    if (known >= 0) {
+      value = mass ? (double)known * weight(zh, 31 + e) : (double)known;
+      if (mass && value < need) return false;
+    }
     while (((hi - lo) >> shift) >= SP_BINS) ++shift;
-    while (true) {
+    while (known < 0) {
       const bool limbs = mass && shift > 0;
       unsigned* hist = clear_hist(limbs ? 2 * SP_BINS : SP_BINS);
       in_range(sp_value<KS>(lo), sp_value<KS>(hi), [&](float z, int idx) {
-        if (bin(z) != b0 || !left(z, idx)) return;
+        if ((b0 >= 0 && bin(z) != b0) || !left(z, idx)) return;
         const uint32_t hb = (hi - sp_key(z, KS)) >> shift;
         if (limbs) {
           const unsigned long long q = (unsigned long long)__double2ll_rn(weight(z, 31 + e));
@@ -695,6 +846,28 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
       }
     }
     // C: the k-th key by counts
+    uint32_t tk = 0;
+    int ti = INT_MAX;
+    if constexpr (N == 8) {
+      // over the positive values, then as far below zero, then to the lowest value, until k are there (the
+      // wider the span, the more values share the bin at zero, and the last span is a few bins only)
+      SpWide wd;
+      int b;
+      for (int span = s.zmax > 0.f && k <= p.V / 2 ? 0 : 1;; ++span) {
+        const float lowest = -3.3895313892515355e38f;
+        wd = SpWide(s.zmax, span == 0 ? s.zmax * 0x1p-15f
+                            : span == 2 ? lowest
+                            : s.zmax > 0.f ? -s.zmax : fmaxf(s.zmax * 0x1p15f, lowest));
+        s.wide_hist(wd);
+        b = s.wide_border(false, (double)k, wd);
+        if ((double)k <= sh.found[1] || span == 2) break;
+      }
+      if ((double)k <= sh.found[1]) {
+        s.refine(false, wd.low(b), fminf(wd.high(b), s.zmax), -1, wd.single(b) ? (int)sh.total[b] : -1,
+                 (double)k - sh.found[0], 0, tk, ti);
+        s.cut = true;
+      }
+    } else {
     unsigned* hist = s.clear_hist(SP_BINS);
     double have = 0.0;
 #pragma unroll 1
@@ -716,11 +889,12 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
     double lower;
     have = s.cluster_sum(sp_block_sum(have), lower);
     if ((double)k < have) {
-      int ti;
-      uint32_t tk;
       const int b = s.border(SP_COUNT, (double)k, 0, 0);
-      s.refine(false, b, (double)k - sh.found[0], 0, tk, ti);
+      s.refine(false, s.edge_low(b), s.edge_high(b), b, -1, (double)k - sh.found[0], 0, tk, ti);
       s.cut = true;
+    }
+    }
+    if (s.cut) {
       s.ck = tk;
       s.ci = ti;
     }
@@ -728,7 +902,15 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
 
   int b = SP_BINS;                              // top-p: kept are the bins before b and a part of b
   double above = 0.0;
-  if (use_p && pf > 0.f) {
+  SpWide wd;
+  if (N == 8 && use_p) {
+    // C: counts by value, down to where V tokens hold less than a 64th of the 1 - top_p of the maximum alone
+    const double x = (double)s.zmax - (6.0 - log2(0.99 * (1.0 - fmax(top_p, 0.0)) / p.V)) / s.c;
+    const float low = x > (double)s.zlow ? __double2float_ru(x) : s.zlow;
+    wd = SpWide(s.zmax, fminf(__bfloat162float(__float2bfloat16_ru(low)), s.zmax));
+    s.wide_hist(wd);
+    b = s.wide_border(true, fmax(top_p, 0.0), wd);
+  } else if (use_p && pf > 0.f) {
     // C: every fourth vector's mass, to fp32: a lower bound of the row's
     float some = 0.f, part = 0.f;
     const float scale = -(float)s.c;
@@ -780,6 +962,8 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
     double sums[2] = {0.0, 0.0};                // all that is left, bins before b
     // bin(z) < b  <=>  not fma(zmax - z, ybin, 2^23) >= 2^23 + b; without top-p (NaN) everything is before
     const float rb = use_p ? SP_ONE + (float)b : __int_as_float(0x7fffffff);
+    const float high = N == 8 && use_p ? fminf(wd.high(b), s.zmax) : -INFINITY;   // bf16: the bin's largest value
+    auto in_front = [&](float z) { return N == 8 ? z > high : !(fmaf(s.zmax - z, s.ybin, SP_ONE) >= rb); };
     const bool plain = !s.cut && zcut == -INFINITY;
     kept = 0;
 #pragma unroll 1
@@ -792,7 +976,7 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
             const bool some = z >= s.zlow;
             const double x = sp_raw_weight(some ? z : s.zmax, s.zmax, s.c), w = some ? x : 0.0;
             sums[0] += w;
-            if (!(fmaf(s.zmax - z, s.ybin, SP_ONE) >= rb)) {
+            if (in_front(z)) {
               mine += w;
               kept += z > -INFINITY;
             }
@@ -801,7 +985,7 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
           s.template each<4>(v, [&](float z, int idx) {
             const bool in = s.left(z, idx), some = in && z >= s.zlow;
             const double x = sp_raw_weight(some ? z : s.zmax, s.zmax, s.c), w = some ? x : 0.0;
-            const bool before = !(fmaf(s.zmax - z, s.ybin, SP_ONE) >= rb);
+            const bool before = in_front(z);
             const bool head = in && before && z >= zcut;   // kept for certain: before bin b, above the min-p cut
             kept += head;
             sums[0] += w;
@@ -828,26 +1012,51 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
     // the bin is right if the sum reaches top_p of the total inside it (b == 0: it starts there)
     const double goal = pf > 0.f ? top_p * total : 0.0;
     if (above >= goal && b > 0 && moved <= 0) {
-      --b;
+      if constexpr (N == 8) {                   // back by the bins' own masses
+        double x = above;
+        do {
+          --b;
+          x -= (double)sh.total[b] * s.weight(fminf(wd.middle(b), s.zmax));
+        } while (b > 0 && (x >= goal || sh.total[b] == 0));
+      } else {
+        --b;
+      }
       moved = -1;
       continue;
     }
-    // the bin's weights lie within 2^(-(b +- 1/2) octaves) of the maximum: scaled by 2^e they are at most 2^(1/16)
-    const int e = (int)((float)b * s.octaves());
+    // weights of the bin scaled by 2^e are at most 2^(1/16): they lie within 2^-(b - 1/2) octaves of the
+    // maximum's (bf16: at or below that of the bin's largest value)
+    const int e = N == 8 ? (int)(((double)s.zmax - (double)high) * s.c) : (int)((float)b * s.octaves());
+    const float zl = N == 8 ? wd.low(b) : s.edge_low(b), top = N == 8 ? high : s.edge_high(b);
+    const int known = N == 8 && wd.single(b) ? (int)sh.total[b] : -1;
     uint32_t tk;
     int ti;
-    if (!s.refine(true, b, fmax(ldexp(goal - above, 31 + e), 0.0), e, tk, ti)) {
-      if (moved >= 0 && b < SP_BINS - 2) {
+    if (!s.refine(true, zl, top, N == 8 ? -1 : b, known, fmax(ldexp(goal - above, 31 + e), 0.0), e, tk, ti)) {
+      bool further = moved >= 0 && (N == 8 ? b + 1 < wd.n : b < SP_BINS - 2);
+      if (N == 8 && further) {                  // on by the bins' own masses, if there is anything
+        double x = above;
+        int to = b, last = b;
+        while (to + 1 < wd.n && (to == b || x < goal)) {
+          x += (double)sh.total[to] * s.weight(fminf(wd.middle(to), s.zmax));
+          ++to;
+          if (sh.total[to]) last = to;
+          if (sh.total[to] && x + (double)sh.total[to] * s.weight(fminf(wd.middle(to), s.zmax)) >= goal) break;
+        }
+        further = last != b;
+        b = last;
+      } else if (further) {
         ++b;
+      }
+      if (further) {
         moved = 1;
         continue;
       }
       // between two bins by the sums' last bits: all of this one stays
-      tk = sp_key(s.edge_low(b), KS);
+      tk = max(sp_key(zl, KS), sp_key(-INFINITY, KS) + 1u);
       ti = INT_MAX;
     }
     // the part of bin b that stays
-    const float zt = sp_value<KS>(tk), top = s.edge_high(b);
+    const float zt = sp_value<KS>(tk);
     const typename SpVec<T>::Range part(zt, top);
 #pragma unroll 1
     for (int st = warp; st < nst; st += SP_WARPS) {
@@ -855,7 +1064,7 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
       double mine = 0.0;
       if (v < s.nvec && part.any(slice[v]))
         s.template each<1>(v, [&](float z, int idx) {
-          if (!(z >= zt && z <= top && z >= zcut) || (z == zt && idx > ti) || s.bin(z) != b || !s.left(z, idx)) return;
+          if (!(z >= zt && z <= top && z >= zcut) || (z == zt && idx > ti) || (N != 8 && s.bin(z) != b) || !s.left(z, idx)) return;
           mine += s.weight(z);
           ++kept;
         });
