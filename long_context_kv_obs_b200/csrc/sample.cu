@@ -21,19 +21,23 @@
 //   B  top-k, few: the k-th largest of the threads' own maxima is a bound that k elements reach; what
 //      reaches it goes to one CTA, which sorts it, sums it in that order for top-p, and again in
 //      index order for the token
-//   C  else the cut is searched: counts (top-k) or masses (top-p) by 512 bins of the distance below the
-//      maximum (shared-memory integer atomics: order does not matter), summed over the cluster
-//      through distributed shared memory; the bin that holds the border is searched again by
-//      ranges of the key, until one key is left; of its ties the lowest indices stay.  Every CTA
-//      reads all histograms of the cluster: with 2048 bins and 16 CTAs that took 9.8k cycles.
-//      For masses a quarter of the row is summed first, in fp32.  That is a lower bound S of the
-//      mass, and tokens below (1 - top_p) S / V together hold less than the 1 - top_p that is cut:
-//      they stay out, and the bins spread over what is left (atomics that meet in a bin wait for one
-//      another: bins of 1/8 octave cost a flat row 26k cycles).  The bins hold masses to 16 bits
-//      only: the exact sums of D decide whether the bin is the right one (else its neighbour is
-//      taken), the later searches count in 2^-31 units of the bin's weights, or exactly once a bin is
-//      one key.
-//   D  fp64 sums of the kept weights by 32-vector stretches of a warp, in index order
+//   C  else the cut is searched: counts or masses by bins below the maximum (shared-memory integer
+//      atomics: order does not matter), summed over the cluster through distributed shared memory.
+//      Every CTA reads all histograms of the cluster, which is why there are no more bins.
+//      bf16: 2048 bins hold one value each (those nearest zero share one), so counts give masses to
+//      fp64, the border's bin is the cut's value, and of its ties the lowest indices stay.  4096 bins
+//      leave fewer rows in doubt (below), but took a row over 16 CTAs from 33 to 62 us.
+//      fp32: 512 bins of the distance below the maximum.  A quarter of the row is summed first, in
+//      fp32: a lower bound S of the mass.  Tokens below (1 - top_p) S / V together hold less than the
+//      1 - top_p that is cut: they stay out, and the bins spread over what is left (atomics that meet in
+//      a bin wait for one another: bins of 1/8 octave cost a flat row 26k cycles).  The bins hold
+//      masses to 16 bits only: the exact sums of D decide whether the bin is the right one (else its
+//      neighbour is taken).
+//      A bin of several values is searched again by ranges of the key, in 2^-31 units of the bin's
+//      weights, or exactly once a bin is one key.
+//   D  fp64 sums of the kept weights by 32-vector stretches of a warp, in index order.  For top-p the
+//      whole mass is summed beside them, 29 instructions an element, unless the counts bound it well
+//      enough to know the cut: then vectors that hold nothing kept cost two instructions an element
 //   E  the stretch, lane and element where u * total falls
 #include <cooperative_groups.h>
 
@@ -330,9 +334,10 @@ struct SpWide {
 };
 // The first of these bins at which the cluster's counts (mass: masses, to fp64 except in a bin of several
 // values, taken at its middle) reach `target`, a share of their sum for masses, or the last that holds
-// something: returned, with the sum before it in found[0] and all of them in found[1].  A thread has four bins.
+// something: returned, with the sum before it in found[0] and all of them in found[1].  For masses found[2] and
+// found[3] bound the mass of the row, of at most V tokens.  A thread has four bins.
 __device__ __noinline__ int sp_wide_border(bool mass, double target, int C, int rank, int buf, SpWide wd, float zmax,
-                                           float zlow, double c) {
+                                           float zlow, double c, int V) {
   static_assert(SP_WIDE == 4 * SP_THREADS, "four bins a thread");
   cg::cluster_group cl = cg::this_cluster();
   SpShared& sh = sp_sh();
@@ -391,6 +396,16 @@ __device__ __noinline__ int sp_wide_border(bool mass, double target, int C, int 
     }
     sh.found[0] = before;
     sh.found[1] = sc.y;
+    if (mass) {
+      double least = sc.y, most = sc.y + (double)V * sp_weight(wd.low(wd.n - 1), zmax, zlow, c, 0);
+      if (wd.k0 > 0 && wd.omax >= 0 && wd.omax < wd.n) {
+        const double cnt = (double)sh.total[wd.omax], mid = sp_weight(fminf(0.f, zmax), zmax, zlow, c, 0);
+        least -= cnt * (mid - sp_weight(wd.low(wd.omax), zmax, zlow, c, 0));
+        most += cnt * (sp_weight(fminf(wd.high(wd.omax), zmax), zmax, zlow, c, 0) - mid);
+      }
+      sh.found[2] = least;
+      sh.found[3] = most;
+    }
   }
   __syncthreads();
   return b;
@@ -529,10 +544,37 @@ struct SpRow {
       }
     }
   }
-  __device__ __forceinline__ int wide_border(bool mass, double target, const SpWide& wd) {
-    const int b = sp_wide_border(mass, target, C, rank, search & 1, wd, zmax, zlow, c);
+  __device__ __forceinline__ int wide_border(bool mass, double target, const SpWide& wd, int V) {
+    const int b = sp_wide_border(mass, target, C, rank, search & 1, wd, zmax, zlow, c, V);
     ++search;
     return b;
+  }
+
+  // The index of tie `want` (from 1) of zt in this slice, by the ties of every stretch: ifound[1], set by one thread.
+  __device__ __forceinline__ void find_tie(const unsigned* count, float zt, int want) const {
+    if (threadIdx.x >= 32) return;
+    const int lane = threadIdx.x, nst = (nvec + 31) / 32;
+    int st = 0;
+#pragma unroll 1
+    for (int s0 = 0; s0 < nst; s0 += 32) {
+      const int n = s0 + lane < nst ? (int)count[s0 + lane] : 0;
+      const int inc = sp_warp_scan(n);
+      const unsigned hit = __ballot_sync(FULL, inc >= want);
+      if (hit) {
+        st = s0 + __ffs(hit) - 1;
+        want -= __shfl_sync(FULL, inc - n, __ffs(hit) - 1);
+        break;
+      }
+      want -= __shfl_sync(FULL, inc, 31);
+    }
+    const int v = st * 32 + lane;
+    int n = 0;
+    if (v < nvec) each<1>(v, [&](float z, int idx) { n += z == zt && left(z, idx); });
+    int k = sp_warp_scan(n) - n;
+    if (k < want && want <= k + n)
+      each<1>(v, [&](float z, int idx) {
+        if (z == zt && left(z, idx) && ++k == want) sp_sh().ifound[1] = idx;
+      });
   }
 
   // Of the values zl to zh (b0 >= 0: those of bin b0 alone) that top-k left, the key at which the count
@@ -590,7 +632,7 @@ struct SpRow {
     tidx = INT_MAX;
     if (take >= ties) return true;
     // ties of every 32-vector stretch, in the histogram words of the next search
-    const int lane = threadIdx.x & 31, nst = (nvec + 31) / 32;
+    const int lane = threadIdx.x & 31;
     const float zt = sp_value<KS>(tkey);
     unsigned* count = sh.hist[search & 1];
     double mine = 0.0;
@@ -610,29 +652,7 @@ struct SpRow {
     double before;
     cluster_sum(mine, before);
     const bool here = before < take && take <= before + mine;
-    if (here && threadIdx.x < 32) {             // this slice holds the last tie that stays
-      int want = (int)(take - before), st = 0;
-#pragma unroll 1
-      for (int s0 = 0; s0 < nst; s0 += 32) {
-        const int n = s0 + lane < nst ? (int)count[s0 + lane] : 0;
-        const int inc = sp_warp_scan(n);
-        const unsigned hit = __ballot_sync(FULL, inc >= want);
-        if (hit) {
-          st = s0 + __ffs(hit) - 1;
-          want -= __shfl_sync(FULL, inc - n, __ffs(hit) - 1);
-          break;
-        }
-        want -= __shfl_sync(FULL, inc, 31);
-      }
-      const int v = st * 32 + lane;
-      int n = 0;
-      if (v < nvec) each<1>(v, [&](float z, int idx) { n += z == zt && left(z, idx); });
-      int k = sp_warp_scan(n) - n;
-      if (k < want && want <= k + n)
-        each<1>(v, [&](float z, int idx) {
-          if (z == zt && left(z, idx) && ++k == want) sh.ifound[1] = idx;
-        });
-    }
+    if (here) find_tie(count, zt, (int)(take - before));        // this slice holds the last tie that stays
     __syncthreads();
     tidx = (int)cluster_sum(here ? (double)sh.ifound[1] : 0.0, before);   // one CTA's
     return true;
@@ -859,7 +879,7 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
                             : span == 2 ? lowest
                             : s.zmax > 0.f ? -s.zmax : fmaxf(s.zmax * 0x1p15f, lowest));
         s.wide_hist(wd);
-        b = s.wide_border(false, (double)k, wd);
+        b = s.wide_border(false, (double)k, wd, p.V);
         if ((double)k <= sh.found[1] || span == 2) break;
       }
       if ((double)k <= sh.found[1]) {
@@ -868,31 +888,31 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
         s.cut = true;
       }
     } else {
-    unsigned* hist = s.clear_hist(SP_BINS);
-    double have = 0.0;
+      unsigned* hist = s.clear_hist(SP_BINS);
+      double have = 0.0;
 #pragma unroll 1
-    for (int v = tid; v < s.nvec; v += SP_THREADS) {
-      int run = 0, rb = -1;                     // equal neighbours in one atomic
-      s.template each<1>(v, [&](float z, int) {
-        if (!(z > -INFINITY)) return;
-        have += 1.0;
-        const int bb = s.bin(z);
-        if (bb != rb) {
-          if (run) atomicAdd(hist + rb, (unsigned)run);
-          rb = bb;
-          run = 0;
-        }
-        ++run;
-      });
-      if (run) atomicAdd(hist + rb, (unsigned)run);
-    }
-    double lower;
-    have = s.cluster_sum(sp_block_sum(have), lower);
-    if ((double)k < have) {
-      const int b = s.border(SP_COUNT, (double)k, 0, 0);
-      s.refine(false, s.edge_low(b), s.edge_high(b), b, -1, (double)k - sh.found[0], 0, tk, ti);
-      s.cut = true;
-    }
+      for (int v = tid; v < s.nvec; v += SP_THREADS) {
+        int run = 0, rb = -1;                     // equal neighbours in one atomic
+        s.template each<1>(v, [&](float z, int) {
+          if (!(z > -INFINITY)) return;
+          have += 1.0;
+          const int bb = s.bin(z);
+          if (bb != rb) {
+            if (run) atomicAdd(hist + rb, (unsigned)run);
+            rb = bb;
+            run = 0;
+          }
+          ++run;
+        });
+        if (run) atomicAdd(hist + rb, (unsigned)run);
+      }
+      double lower;
+      have = s.cluster_sum(sp_block_sum(have), lower);
+      if ((double)k < have) {
+        const int b = s.border(SP_COUNT, (double)k, 0, 0);
+        s.refine(false, s.edge_low(b), s.edge_high(b), b, -1, (double)k - sh.found[0], 0, tk, ti);
+        s.cut = true;
+      }
     }
     if (s.cut) {
       s.ck = tk;
@@ -904,12 +924,12 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
   double above = 0.0;
   SpWide wd;
   if (N == 8 && use_p) {
-    // C: counts by value, down to where V tokens hold less than a 64th of the 1 - top_p of the maximum alone
-    const double x = (double)s.zmax - (6.0 - log2(0.99 * (1.0 - fmax(top_p, 0.0)) / p.V)) / s.c;
+    // C: counts by value, down to where V tokens hold less than 2^-14 of the 1 - top_p of the maximum alone
+    const double x = (double)s.zmax - (14.0 - log2(0.99 * (1.0 - fmax(top_p, 0.0)) / p.V)) / s.c;
     const float low = x > (double)s.zlow ? __double2float_ru(x) : s.zlow;
     wd = SpWide(s.zmax, fminf(__bfloat162float(__float2bfloat16_ru(low)), s.zmax));
     s.wide_hist(wd);
-    b = s.wide_border(true, fmax(top_p, 0.0), wd);
+    b = s.wide_border(true, fmax(top_p, 0.0), wd, p.V);
   } else if (use_p && pf > 0.f) {
     // C: every fourth vector's mass, to fp32: a lower bound of the row's
     float some = 0.f, part = 0.f;
@@ -958,7 +978,92 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
   // D: the kept mass by stretches of 32 vectors
   const int nst = (s.nvec + 31) / 32;
   int kept = 0;
-  for (int moved = 0;;) {
+  bool done = false;
+  if constexpr (N == 8) {
+    // Where the bounds on the row's mass leave no doubt about the cut, only what stays is summed: the
+    // bin is one value of weight w, a number of its ties stays, and few vectors hold any of it
+    // (256 rows of 128256 with filters of all kinds: 164 -> 124 us).
+    const float high = use_p ? fminf(wd.high(b), s.zmax) : 0.f;
+    const double w = use_p ? s.weight(high) : 0.0, share = fmax(top_p, 0.0);
+    const double least = sh.found[2] * (1.0 - 1e-12), most = sh.found[3] * (1.0 + 1e-12);   // beside fp64's own errors
+    if (use_p && wd.single(b) && w > 0.0 && (most - least) * share <= 0.25 * w) {
+      unsigned* count = sh.hist[s.search & 1];
+      double before_b = 0.0, same = 0.0;
+      const typename SpVec<T>::Range front(high, INFINITY);
+#pragma unroll 1
+      for (int st = warp; st < nst; st += SP_WARPS) {
+        const int v = st * 32 + lane;
+        double mine = 0.0;
+        int n = 0;
+        if (v < s.nvec && front.any(slice[v]))
+          s.template each<1>(v, [&](float z, int idx) {
+            if (!(z >= high) || !s.left(z, idx)) return;
+            if (z == high) {
+              ++n;
+              return;
+            }
+            const double x = sp_raw_weight(z, s.zmax, s.c);
+            before_b += x;
+            if (z >= zcut) {
+              mine += x;
+              ++kept;
+            }
+          });
+        if (__any_sync(FULL, mine > 0.0)) mine = warp_sum_d(mine);
+        n = __reduce_add_sync(FULL, n);
+        if (lane == 0) {
+          wsum[st] = mine;
+          count[st] = (unsigned)n;
+          same += n;
+        }
+      }
+      before_b = sp_block_sum(before_b);
+      same = sp_block_sum(same);
+      s.exchange(before_b, same);
+      double ties = 0.0, earlier = 0.0;
+      above = 0.0;
+#pragma unroll 1
+      for (int r = 0; r < s.C; ++r) {
+        if (r == s.rank) earlier = ties;
+        above += s.got_d(r, 0);
+        ties += s.got_d(r, 1);
+      }
+      double take = 1.0;                        // top_p <= 0: one token
+      done = b == 0;
+      if (pf > 0.f) {
+        take = ceil((share * least - above) / w);
+        done = take == ceil((share * most - above) / w) && take >= 1.0 && take <= ties;
+      }
+      if (done) {
+        const int stay = (int)fmin(fmax(take - earlier, 0.0), same), all = (int)same;
+        int ti = stay == all ? INT_MAX : -1;
+        if (stay > 0 && stay < all) {
+          s.find_tie(count, high, stay);
+          __syncthreads();
+          ti = sh.ifound[1];
+        }
+        if (high >= zcut && warp == 0) {
+          int from = 0;
+#pragma unroll 1
+          for (int s0 = 0; s0 < nst; s0 += 32) {
+            const int n = s0 + lane < nst ? (int)count[s0 + lane] : 0;
+            const int inc = sp_warp_scan(n), mine = min(max(stay - from - (inc - n), 0), n);
+            if (mine) wsum[s0 + lane] += (double)mine * w;
+            from += __shfl_sync(FULL, inc, 31);
+          }
+          if (lane == 0) kept += stay;
+        }
+        // from here on `left` is the final cut, in this slice
+        const uint32_t tk = sp_key(high, KS);
+        s.ci = s.cut && tk == s.ck ? min(ti, s.ci) : ti;
+        s.ck = tk;
+        s.cut = true;
+      }
+    }
+  }
+  const float least_kept = use_p ? -INFINITY : fmaxf(zcut, s.cut ? sp_value<KS>(s.ck) : -INFINITY);
+  const typename SpVec<T>::Range may_stay(least_kept, INFINITY);
+  for (int moved = 0; !done;) {
     double sums[2] = {0.0, 0.0};                // all that is left, bins before b
     // bin(z) < b  <=>  not fma(zmax - z, ybin, 2^23) >= 2^23 + b; without top-p (NaN) everything is before
     const float rb = use_p ? SP_ONE + (float)b : __int_as_float(0x7fffffff);
@@ -981,7 +1086,7 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
               kept += z > -INFINITY;
             }
           });
-        } else {
+        } else if (least_kept == -INFINITY || may_stay.any(slice[v])) {
           s.template each<4>(v, [&](float z, int idx) {
             const bool in = s.left(z, idx), some = in && z >= s.zlow;
             const double x = sp_raw_weight(some ? z : s.zmax, s.zmax, s.c), w = some ? x : 0.0;

@@ -1,6 +1,6 @@
 """GPU: token sampling against the fp64 oracle.  Tokens and counts are equal: a border lies within the
-kernel's error (about 10^-11 of the mass) of a random one with a chance of 10^-6 a row.  logprob is
-fp32 of an fp64 value: half a step of fp32 (2^-24 of it) and 10^-9 for the masses."""
+kernel's error (2^-32 of a weight for each of them) of a random one with a chance of 10^-6 a row.  logprob is
+fp32 of an fp64 value: half a step of fp32 (2^-24 of it) and 10^-9 for the masses (2^-30 at most)."""
 import numpy as np
 import pytest
 import torch
@@ -192,3 +192,47 @@ def test_refusals_launch_nothing():
         with pytest.raises((ValueError, TypeError, B.KvcError)):
             B.kvc_sample(**{**dict(logits=z, u=u, token=token), **change})
     assert B.kvc_launch_count() == before
+
+
+def test_bf16_values_of_one_sign_across_zero_and_at_its_borders():
+    """bf16 cuts are searched value by value: spans of one sign, spans that cross zero, more values than bins,
+    values that differ near zero alone, cuts among ties that several slices of the row share."""
+    r = np.random.default_rng(20)
+    V = 90001
+    g = torch.Generator(device=DEV).manual_seed(21)
+    e = torch.rand(12, V, device=DEV, generator=g)
+    z = torch.randn(12, V, device=DEV, generator=g)
+    z[0] = -torch.exp2(-40 * e[0])                                    # negative, 40 octaves
+    z[1] = torch.exp2(-40 * e[1])                                     # positive
+    z[2] = torch.where(e[2] < 0.5, -1.0, 1.0) * torch.exp2(-60 * z[2].abs())
+    z[3] = z[3] * 1e-6                                                # about zero alone
+    z[4] = 9 + z[4] * 0.01
+    z[5] = -9 + z[5] * 0.01
+    z[6] = torch.where(e[6] < 0.999, torch.full_like(z[6], 2.5), z[6])  # one value holds nearly all
+    z[7] = torch.where(e[7] < 0.999, torch.full_like(z[7], -2.5), z[7] * 3)
+    z[8] = z[8] * 1e30
+    z[9] = -z[9].abs() * 1e-30
+    z[10] = z[10].round()                                             # a few values, one of them zero
+    z[11, 0] = 30.0                                                   # one token holds nearly all
+    z = z.to(BF)
+    u = r.random(12).astype(np.float32)
+    for T in (0.05, 0.7, 1.0, 20.0):
+        for p in (0.3, 0.95, 0.9999):
+            check(z, u, temperature=T, top_p=p)
+    for k in (600, 5000, V // 2, V // 2 + 1, V - 1):
+        check(z, u, temperature=0.8, top_k=k)
+        check(z, u, temperature=0.8, top_k=k, top_p=0.8, min_p=1e-4)
+    check(z, u, temperature=0.8, min_p=r.uniform(1e-6, 0.9, 12), top_p=r.uniform(0.01, 0.9999, 12))
+
+
+def test_bf16_border_parameters():
+    z = rows(8, 5003, BF, 22)
+    nan = float("nan")
+    check(z, [0.0, -3.0, 1.0, 7.0, nan, 0.5, 1 - 2 ** -24, 1e-30], temperature=0.9, top_p=0.8)
+    check(z, 0.4, temperature=[0.0, -1.0, nan, 1e-40, 1e-6, 1e6, INF, 30.0], top_p=0.5, top_k=1000)
+    check(z, 0.7, top_p=[0.0, -1.0, nan, 1.0, 2.0, 1e-30, 0.99999994, 0.5])
+    check(z, 0.7, top_p=[0.0, -1.0, nan, 1.0, 2.0, 1e-30, 0.99999994, 0.5], top_k=3000, min_p=0.01)
+    check(z, 0.7, top_k=[0, -5, 1, 2, 5002, 5003, 5004, 2 ** 31 - 1])
+    zi = z.clone()
+    zi[:, 7] = INF
+    check(zi, 0.7, temperature=[1.0, 0.5, 2.0, INF, 1e-40, 30.0, 1.0, 1.0], top_p=0.9, min_p=0.1)
