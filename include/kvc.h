@@ -653,10 +653,10 @@ typedef struct {
  *   token   the smallest index i whose cumulative mass, kept tokens in index order, exceeds
  *           u * the kept mass; u is clamped to [0, 1 - 2^-24], NaN counts as 0
  * temperature <= 0 or NaN takes the first token of the order.  Where logits of +infinity
- * are, only they are kept, all alike; a token of logit -infinity is never kept; a row that holds nothing else gets
- * token -1, kept 0 and logprob -infinity.  Weights are
- * formed in 64 bits and summed in an order that does not depend on timing: equal calls give equal
- * tokens. */
+ * are, only they are kept, all alike; a token of logit -infinity is never kept; a row that
+ * holds nothing else gets token -1, kept 0 and logprob -infinity.  Weights carry 31 bits
+ * (below 2^-64 of the largest they count as nothing) and are summed in fp64, in an order that
+ * does not depend on timing: equal calls give equal tokens. */
 typedef struct {
   int n;                   /* rows */
   int V;                   /* vocabulary, 1 .. 262144 */

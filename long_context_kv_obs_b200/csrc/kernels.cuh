@@ -231,6 +231,24 @@ struct PageAppendParams {
 };
 cudaError_t launch_page_append(const PageAppendParams& p, cudaStream_t st);
 
+// A launch that may begin while the kernel before it on the stream still runs (`early`: that kernel runs
+// griddepcontrol.launch_dependents and this one griddepcontrol.wait before it touches what that one wrote, or ends).
+template <typename... P, typename... A>
+inline cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, bool early,
+                                    const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // Decode attention over a shared prompt and the sequences' own rows (prefix.cu).  Partial
 // results are records of one query row over one stretch of keys: ml = (max in log2 units, sum),
 // o[d] unnormalised.  Records lie in groups of `rows` consecutive query rows.

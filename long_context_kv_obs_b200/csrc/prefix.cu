@@ -78,8 +78,10 @@ __global__ void __launch_bounds__(PG_THREADS) prefix_generic_kernel(const __grid
   const int s0 = split * sl, s1 = min(n, s0 + sl);
   const PartialBuf& out = OWN ? p.po : p.pp;
   const int64_t rec0 = ((int64_t)item * ns + split) * (OWN ? p.G : PG_ROWS);
+  tc::pdl_launch();
   if (s0 >= s1) {
     if ((int)threadIdx.x < nr) out.ml[rec0 + threadIdx.x] = make_float2(-INFINITY, 0.f);
+    if (OWN) tc::pdl_wait();
     return;
   }
   float q[PG_ROWS][4], acc[PG_ROWS][4], m[PG_ROWS], ls[PG_ROWS];
@@ -171,6 +173,7 @@ __global__ void __launch_bounds__(PG_THREADS) prefix_generic_kernel(const __grid
     out.o[(rec0 + r) * D + e] = v;
     if (e == 0) out.ml[rec0 + r] = make_float2(M, s);
   }
+  if (OWN) tc::pdl_wait();                      // done is done: the merge waits for this kernel alone
 }
 
 // Merge of the records, in a fixed order: CTAs of a (sequence, layer) and some of its heads.  Where the
@@ -223,6 +226,7 @@ __global__ void __launch_bounds__(PC_THREADS) prefix_combine_kernel(const __grid
     pstep = PG_ROWS;
     prec = (((int64_t)l * p.Hkv + g) * p.rgp + r / PG_ROWS) * p.nsp * PG_ROWS + r % PG_ROWS;
   }
+  tc::pdl_wait();                               // the records are complete
   const int nall = np + (p.K ? p.nso : 0);
   const int64_t orec = ((int64_t)bl * p.Hkv + g) * p.nso * p.G + gg;
   const int most = __reduce_max_sync(FULL, nall);
@@ -370,9 +374,8 @@ cudaError_t launch_prefix(const PrefixParams& p, cudaStream_t st) {
       if ((e = launch_prefix_own_mma(p, st)) != cudaSuccess) return e;
     } else {
       const dim3 grid(p.B * p.L * p.Hkv, p.nso);
-      if (p.d == 128) prefix_generic_kernel<128, true><<<grid, PG_THREADS, 0, st>>>(p);
-      else prefix_generic_kernel<64, true><<<grid, PG_THREADS, 0, st>>>(p);
-      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+      auto kern = p.d == 128 ? prefix_generic_kernel<128, true> : prefix_generic_kernel<64, true>;
+      if ((e = launch_dependent(kern, grid, PG_THREADS, 0, st, p.Kp != nullptr, p)) != cudaSuccess) return e;
       count_launch();
     }
   }
@@ -381,8 +384,8 @@ cudaError_t launch_prefix(const PrefixParams& p, cudaStream_t st) {
   const dim3 grid(p.B * p.L, (p.Hq + per - 1) / per);
   auto kern = p.d == 128 ? (many ? prefix_combine_kernel<128, 1> : prefix_combine_kernel<128, 4>)
                          : (many ? prefix_combine_kernel<64, 1> : prefix_combine_kernel<64, 4>);
-  kern<<<grid, PC_THREADS, 0, st>>>(p);
-  if ((e = cudaGetLastError()) == cudaSuccess) count_launch();
+  e = launch_dependent(kern, grid, PC_THREADS, 0, st, true, p);
+  if (e == cudaSuccess) count_launch();
   return e;
 }
 

@@ -13,9 +13,11 @@
 // runs ahead across items, so short rows (a few hundred keys) still keep the ring full.  It draws
 // the items from a counter and hands them on through a short queue: rows differ in length, and dealt
 // out in turn the longest share took a quarter more than the mean (0.078 -> 0.063 ms for 896 rows of
-// up to 1400 keys).  Who computes an item does not change it.  Merging the prompt's records here
-// too, in place of a kernel of its own, doubled the time: the consumers wait for those loads while the
-// ring is full.  Every wait is an mbarrier with a time limit.
+// up to 1400 keys).  Who computes an item does not change it.  The first item of a
+// CTA is its number: it is loaded while the prompt's kernel, which zeroes the counter, still runs
+// elsewhere.  Merging the prompt's records here too, in place of a kernel of its own, doubled the
+// time: the consumers wait for those loads while the ring is full.  Every wait is an mbarrier with a
+// time limit.
 // Pages: a stage is 64 / page boxes of `page` tokens (or a part of one page), each at the place its
 // table entry says.  The producer's lanes hold 32 entries of the row's table at a time and each
 // issues one box.  A page id outside the pool becomes a coordinate past the map, whose box reads
@@ -83,6 +85,7 @@ prefix_own_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
     prefetch_map(&mapK);
     prefetch_map(&mapV);
   }
+  pdl_launch();
   __syncthreads();
   auto row_len = [&](int bl) {
     const int n = p.len[bl];
@@ -95,7 +98,7 @@ prefix_own_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
     const int bt = a.bt, nb = PO_KEYS / bt;     // boxes a stage (per K / V atom)
     uint32_t chunk = 0, nq = 0;
     bool ok = true;
-    int drawn = lane == 0 ? atomicAdd(p.counter, 1) : 0;
+    int drawn = blockIdx.x;
     while (ok) {
       const int item = __shfl_sync(FULL, drawn, 0);
       const bool last = item >= a.nitems;
@@ -113,7 +116,8 @@ prefix_own_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
           if (last) {
             mbar_arrive(&c->q_full[q]);
           } else {
-            drawn = atomicAdd(p.counter, 1);    // the next one, while this one is loaded
+            // the next one, while this one is loaded
+            if (nq > 0) drawn = (int)gridDim.x + atomicAdd(p.counter, 1);
             mbar_expect_tx(&c->q_full[q], bytes);
             bulk_load(qbuf + q * bytes, reinterpret_cast<const char*>(p.q) + ((int64_t)bl * p.Hq + g * p.G) * D * 2, bytes,
                       &c->q_full[q]);
@@ -162,7 +166,12 @@ prefix_own_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
           }
         }
       }
+      if (nq == 1) {                            // the first is under way
+        pdl_wait();
+        if (lane == 0) drawn = (int)gridDim.x + atomicAdd(p.counter, 1);
+      }
     }
+    pdl_wait();
     if (*abort && lane == 0) {                  // copies in flight end before shared memory is given up
       int none = 0;
       const uint32_t issued = chunk, sent = nq;
@@ -423,8 +432,7 @@ static cudaError_t launch_po(const PrefixParams& p, const CUtensorMap& mk, const
   int grid = PO_PER_SM * num_sms();
   if (!p.counter_zeroed && (e = cudaMemsetAsync(p.counter, 0, sizeof(int), st)) != cudaSuccess) return e;
   if (grid > a.nitems) grid = a.nitems;
-  kern<<<grid, PO_THREADS, smem, st>>>(mk, mv, a);
-  e = cudaGetLastError();
+  e = launch_dependent(kern, dim3(grid), PO_THREADS, smem, st, p.counter_zeroed != 0, mk, mv, a);
   if (e == cudaSuccess) count_launch();
   return e;
 }

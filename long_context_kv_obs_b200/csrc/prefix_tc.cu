@@ -167,6 +167,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
       if (lane == 0 && p.counter) *p.counter = 0;   // for the own rows' kernel, next on the stream
     }
   }
+  pdl_launch();                                 // it fills the SMs as they fall free
   fence_before();
   __syncthreads();
   fence_after();
@@ -489,7 +490,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
           p.pp.ml[rec] = make_float2(m, lsum);
           px_add_o<D>(tO, acc);
           // rows to memory through the Q area, whose products are all done (this warpgroup's last o_ready
-          // came behind them): a lane storing its own row, 16 bytes here and there, took 40k cycles a piece
+          // came behind them): a lane that stores its own row, 16 bytes here and there, cost one layer 1.8 of 12.3 us
           constexpr int CC = D / 4;              // dimensions at a time
           uint8_t* stage = Qs + warp * (32 * CC * 4);
           float* dst = p.pp.o + group * 128 * D + (int64_t)((warp & 3) * 32) * D;

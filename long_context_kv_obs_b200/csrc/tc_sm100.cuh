@@ -11,6 +11,10 @@ namespace tc {
 
 constexpr uint64_t WAIT_NS = 2000000000ull;   // 2 s: far beyond any legitimate wait
 
+// Programmatic dependent launch: the next kernel may start; the kernel before is done and its writes seen.
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
