@@ -21,7 +21,7 @@
 // are fetched once for 256 rows.
 //
 // Roles: warps 0-3 and 4-7 are the softmax warpgroups (a thread owns a query row, its TMEM lane),
-// warp 8 loads K and V (TMA, 128B swizzle, separate rings), warp 9 issues the products.  TMEM: a
+// warp 8 loads K and V (TMA, 128B swizzle, separate rings), warps 9 and 10 issue the products.  TMEM: a
 // warpgroup has 128 columns of S, overwritten by its P, and 128 of O.  Every wait is an mbarrier
 // with a time limit, those among the softmax warps too, so an abort strands no warp.  While one warpgroup
 // works on its S the tensor cores run the other's products.
@@ -36,17 +36,17 @@ namespace kvc {
 using namespace tc;
 
 constexpr int PX_KEYS = 128;                    // keys a tile
-constexpr int PX_THREADS = 384;                 // warps 10 and 11 only complete the third warpgroup
+constexpr int PX_THREADS = 384;                 // warp 11 only completes the third warpgroup
 constexpr int PX_ATOM = PX_KEYS * 128;          // 128 rows x 64 bf16, 128B-swizzled (16 KB)
 template <int D> constexpr int px_tile() { return (D / 64) * PX_ATOM; }
 template <int D, int MT> constexpr int px_nk() { return D == 64 ? 4 : (MT == 1 ? 3 : 2); }
 template <int D, int MT> constexpr int px_nv() { return D == 64 ? 4 : 3; }
 struct PxCtl {
   uint64_t fullK[4], emptyK[4], fullV[4], emptyV[4];
-  uint64_t s_ready[2], p_ready[2], o_ready[2], b_ready[2], q_ready, q_free, drain;
+  uint64_t s_ready[2], p_ready[2][2], o_ready[2], b_ready[2], q_ready, q_free, s_done, drain;
   uint32_t tmem;
   int abort;
-  float bias[2][2][PX_KEYS];                    // [warpgroup][buffer]
+  alignas(16) float bias[2][2][PX_KEYS];        // [warpgroup][buffer], read as float4
   int cum[PREFIX_TC_LAYERS + 1];                         // tiles of the layers before
 };
 template <int D, int MT> constexpr size_t px_smem() {
@@ -138,19 +138,21 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
   if (threadIdx.x == 0) {
     for (int i = 0; i < 4; ++i) {
       mbar_init(&c->fullK[i], 1);
-      mbar_init(&c->emptyK[i], 1);
+      mbar_init(&c->emptyK[i], MT);
       mbar_init(&c->fullV[i], 1);
-      mbar_init(&c->emptyV[i], 1);
+      mbar_init(&c->emptyV[i], MT);
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(&c->s_ready[w], 1);
-      mbar_init(&c->p_ready[w], 4);
+      mbar_init(&c->p_ready[w][0], 4);
+      mbar_init(&c->p_ready[w][1], 4);
       mbar_init(&c->o_ready[w], 1);
       mbar_init(&c->b_ready[w], 4);
     }
     mbar_init(&c->q_ready, 8);
     mbar_init(&c->q_free, 8);
-    mbar_init(&c->drain, 1);
+    mbar_init(&c->s_done, 8);
+    mbar_init(&c->drain, 2);
     c->abort = 0;
     fence_mbar_init();
   }
@@ -214,73 +216,63 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
           mbar_wait(&c->fullV[j % NV], (j / NV) & 1, &none, p.status);
       }
     }
-  } else if (warp == 9) {
+  } else if (warp < 11) {
     // ------------------------------------------------------------ products
-    // The whole warp runs the loop and one lane issues: addresses that are known to be the same in
-    // all lanes live in uniform registers, where the products' descriptors are wanted (issued by a
-    // lone thread each product took 80 to 150 cycles to issue for 53 of work).
+    // A warp for each softmax warpgroup: one for both waits for one's P while the other's lies ready
+    // (7 heads: 104 us).  The whole warp runs the loop and one lane issues: addresses that are known
+    // to be the same in all lanes live in uniform registers, where the products' descriptors are wanted
+    // (issued by a lone thread each product took 80 to 150 cycles to issue for 53 of work).
       constexpr uint32_t idS = idesc_bf16(128, PX_KEYS);
       constexpr uint32_t idO = idesc_bf16(128, D) | IDESC_B_MN;
-      const uint32_t tm = __shfl_sync(FULL, tmem, 0);
+      const int w = __shfl_sync(FULL, warp - 9, 0);
+      const int i0 = MT == 1 ? w : 0, di = MT == 1 ? 2 : 1;
+      const uint32_t ts = __shfl_sync(FULL, tmem, 0) + w * 128, to = ts + 256;
       const uint32_t q0 = __shfl_sync(FULL, smem_u32(Qs), 0), k0 = q0 + MT * TILE, v0 = k0 + NK * TILE;
-      uint32_t tc = 0, nseg = 0, pv[2] = {0, 0};   // tiles, pieces and P V products so far
+      const uint64_t dq = sw128_desc_at(q0 + (MT == 2 ? w : 0) * TILE, 16);
+      uint32_t tc = 0, nseg = 0, pv = 0;        // tiles, pieces, and P V products so far
       bool ok = true;
       while (ok && run.next(p, c->cum, sg)) {
-        ok = mbar_wait(&c->q_ready, nseg & 1, abort, p.status);
-        ok = __all_sync(FULL, ok);
+        ok = __all_sync(FULL, mbar_wait(&c->q_ready, nseg & 1, abort, p.status));
         ++nseg;
-        const int n = __shfl_sync(FULL, sg.n, 0), U = MT * n;   // steps: (tile, warpgroup)
-        auto issue_s = [&](int u, auto wc) {
-          constexpr int w = decltype(wc)::value;
-          const uint32_t t = tc + (MT == 2 ? u >> 1 : u), ks = t % NK;
-          if (MT == 1 || w == 0) {
-            if (!__all_sync(FULL, mbar_wait(&c->fullK[ks], (t / NK) & 1, abort, p.status))) return false;
-          }
+        const int n = __shfl_sync(FULL, sg.n, 0);
+        auto issue_s = [&](int i) {
+          const uint32_t t = tc + i, ks = t % NK;
+          if (!__all_sync(FULL, mbar_wait(&c->fullK[ks], (t / NK) & 1, abort, p.status))) return false;
           fence_after();
-          const uint64_t da = sw128_desc_at(q0 + (MT == 2 ? w : 0) * TILE, 16);
-          const uint64_t db = sw128_desc_at(k0 + ks * TILE, 16);
+          const uint64_t dk = sw128_desc_at(k0 + ks * TILE, 16);
           if (elect_one()) {
-            if constexpr (D == 128) mma_bf16_k128(tm + w * 128, da, db, PX_ATOM >> 4, PX_ATOM >> 4, idS);
-            else mma_bf16_k64(tm + w * 128, da, db, idS);
+            if constexpr (D == 128) mma_bf16_k128(ts, dq, dk, PX_ATOM >> 4, PX_ATOM >> 4, idS);
+            else mma_bf16_k64(ts, dq, dk, idS);
             mma_commit(&c->s_ready[w]);
-            if (MT == 1 || w == 1) mma_commit(&c->emptyK[ks]);
+            mma_commit(&c->emptyK[ks]);
           }
           __syncwarp();
           return true;
         };
-        auto step = [&](int u, auto wc) {
-          constexpr int w = decltype(wc)::value;
-          const uint32_t t = tc + (MT == 2 ? u >> 1 : u), vs = t % NV;
-          if (!__all_sync(FULL, mbar_wait(&c->fullV[vs], (t / NV) & 1, abort, p.status) &&
-                                    mbar_wait(&c->p_ready[w], pv[w] & 1, abort, p.status)))
-            return false;
-          fence_after();
+        if (ok && i0 < n) ok = issue_s(i0);
+        for (int i = i0; i < n && ok; i += di, ++pv) {
+          const uint32_t t = tc + i, vs = t % NV;
+          ok = __all_sync(FULL, mbar_wait(&c->fullV[vs], (t / NV) & 1, abort, p.status));
           const uint64_t dv = sw128_desc_at(v0 + vs * TILE, PX_ATOM);
-          const uint32_t ta = tm + w * 128, to = tm + 256 + w * 128;
-          if (elect_one()) {
-            // P lo first: the tensor core truncates its fp32 accumulator at every product, and the lo
-            // parts leave it small, so 8 roundings a tile count, not 16 (see the head of the file)
-            mma_bf16_ts_k128(to, ta + 8, dv, idO, 0);
-            mma_bf16_ts_k128(to, ta, dv, idO, 1);
-            mma_commit(&c->o_ready[w]);
-            if (MT == 1 || w == 1) mma_commit(&c->emptyV[vs]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {         // the keys' halves: the first, while P of the second is formed
+            ok = ok && __all_sync(FULL, mbar_wait(&c->p_ready[w][h], pv & 1, abort, p.status));
+            if (!ok) break;
+            fence_after();
+            if (elect_one()) {
+              // P lo first: the tensor core truncates its fp32 accumulator at every product, and the lo
+              // parts of the first half leave it small: 12 roundings a tile count, not 16 (see the head of the file)
+              mma_bf16_ts_k64(to, ts + h * 64 + 8, dv + h * 512, idO, h);
+              mma_bf16_ts_k64(to, ts + h * 64, dv + h * 512, idO, 1);
+              if (h == 1) {
+                mma_commit(&c->o_ready[w]);
+                mma_commit(&c->emptyV[vs]);
+              }
+            }
+            __syncwarp();
           }
-          __syncwarp();
-          bool good = true;
-          if (u + 2 < U) {
-            // the next S of this warpgroup overwrites the P that these products read
-            good = __all_sync(FULL, mbar_wait(&c->o_ready[w], pv[w] & 1, abort, p.status)) && issue_s(u + 2, wc);
-          }
-          ++pv[w];
-          return good;
-        };
-        constexpr std::integral_constant<int, 0> W0{};
-        constexpr std::integral_constant<int, 1> W1{};
-        if (ok) ok = issue_s(0, W0);
-        if (ok && U > 1) ok = issue_s(1, W1);
-        for (int u = 0; u < U && ok; u += 2) {
-          ok = step(u, W0);
-          if (ok && u + 1 < U) ok = step(u + 1, W1);
+          // the next S overwrites the P that these products read
+          if (ok && i + di < n) ok = __all_sync(FULL, mbar_wait(&c->o_ready[w], pv & 1, abort, p.status)) && issue_s(i + di);
         }
         tc += n;
       }
@@ -373,8 +365,9 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
           break;
         }
         fence_after();
-        if (nk < PX_KEYS && (MT == 1 || w == 0)) {
-          // rows past the length may hold anything and 0 * NaN is NaN: zero them in V
+        if (nk < PX_KEYS) {
+          // rows past the length may hold anything and 0 * NaN is NaN: zero them in V, each warpgroup
+          // before its own products
           const uint32_t t = tc + i, vs = t % NV;
           ok = mbar_wait(&c->fullV[vs], (t / NV) & 1, abort, p.status);
           if (!__all_sync(FULL, ok)) {
@@ -441,7 +434,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
           auto chunk = [&](int q, uint32_t (&x)[16], uint32_t (&xn)[16], uint32_t (&u)[16], uint32_t (&un)[16]) {
             tmem_wait_ld16(x);
             if (q + 1 < PX_KEYS / 16) tmem_ld16_raw(tS + q * 16 + 16, xn);
-            if (q > 0) tmem_st16(tS + q * 16 - 16, un);
+            if (q > 0 && q != PX_KEYS / 32) tmem_st16(tS + q * 16 - 16, un);
 #pragma unroll
             for (int k = 0; k < 16; k += 2) {
               uint64_t off = nm2;
@@ -463,15 +456,24 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
           for (int q = 0; q < PX_KEYS / 16; q += 2) {
             chunk(q, xa, xb, ua, ub);
             chunk(q + 1, xb, xa, ub, ua);
+            if (q + 2 == PX_KEYS / 32) {        // the first half is there
+              tmem_st16(tS + PX_KEYS / 2 - 16, ub);
+              tmem_wait_st();
+              fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&c->p_ready[w][0]);
+            }
           }
           tmem_st16(tS + PX_KEYS - 16, ub);
           const float2 s2 = upk2(sum2);
           lsum += s2.x + s2.y;
           tmem_wait_st();
+        } else if (lane == 0) {
+          mbar_arrive(&c->p_ready[w][0]);
         }
         fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&c->p_ready[w]);
+        if (lane == 0) mbar_arrive(&c->p_ready[w][1]);
         ++steps;
       }
       if (!ok) break;
@@ -479,6 +481,14 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
       // the piece's record of this warpgroup
       const int64_t group = 2 * (int64_t)(sg.item + blockIdx.x) + w;
       const int64_t rec = group * 128 + row;
+      // its rows go to memory through the Q area: all S products of the piece are done first
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c->s_done);
+      ok = mbar_wait(&c->s_done, (nseg - 1) & 1, abort, p.status);
+      if (!__all_sync(FULL, ok)) {
+        ok = false;
+        break;
+      }
       if (mine > 0) {
         ok = mbar_wait(&c->o_ready[w], (steps - 1) & 1, abort, p.status);
         if (!__all_sync(FULL, ok)) {
@@ -489,8 +499,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
         if (live) {
           p.pp.ml[rec] = make_float2(m, lsum);
           px_add_o<D>(tO, acc);
-          // rows to memory through the Q area, whose products are all done (this warpgroup's last o_ready
-          // came behind them): a lane that stores its own row, 16 bytes here and there, cost one layer 1.8 of 12.3 us
+          // (a lane that stores its own row, 16 bytes here and there, cost one layer 1.8 of 12.3 us)
           constexpr int CC = D / 4;              // dimensions at a time
           uint8_t* stage = Qs + warp * (32 * CC * 4);
           float* dst = p.pp.o + group * 128 * D + (int64_t)((warp & 3) * 32) * D;

@@ -213,26 +213,20 @@ __device__ __forceinline__ void mma_bf16_k64(uint32_t d_tmem, uint64_t a0, uint6
       "l"(a0), "l"(b0), "r"(idesc)
       : "memory");
 }
-// D[tmem] (+)= A[tmem] * B[smem]^T over K = 128 (eight K = 16 steps) in one asm block.  A's rows are
+// D[tmem] (+)= A[tmem] * B[smem]^T over K = 64 (four K = 16 steps) in one asm block.  A's rows are
 // TMEM lanes, two bf16 of the K dimension in a 32-bit column; step k's 8 columns start at
 // a0 + 16 k.  B is M/N-major: a step is 16 rows of 128 bytes.  first 0: the first step overwrites D.
-__device__ __forceinline__ void mma_bf16_ts_k128(uint32_t d_tmem, uint32_t a0, uint64_t b0, uint32_t idesc,
-                                                 uint32_t first) {
+__device__ __forceinline__ void mma_bf16_ts_k64(uint32_t d_tmem, uint32_t a0, uint64_t b0, uint32_t idesc,
+                                                uint32_t first) {
   asm volatile(
-      "{\n .reg .pred p0, p1;\n .reg .b64 b1, b2, b3, b4, b5, b6, b7;\n .reg .b32 a1, a2, a3, a4, a5, a6, a7;\n"
+      "{\n .reg .pred p0, p1;\n .reg .b64 b1, b2, b3;\n .reg .b32 a1, a2, a3;\n"
       " setp.ne.b32 p0, %4, 0;\n setp.eq.b32 p1, %3, %3;\n"
-      " add.u32 a1, %1, 16;\n add.u32 a2, %1, 32;\n add.u32 a3, %1, 48;\n add.u32 a4, %1, 64;\n"
-      " add.u32 a5, %1, 80;\n add.u32 a6, %1, 96;\n add.u32 a7, %1, 112;\n"
-      " add.s64 b1, %2, 128;\n add.s64 b2, %2, 256;\n add.s64 b3, %2, 384;\n add.s64 b4, %2, 512;\n"
-      " add.s64 b5, %2, 640;\n add.s64 b6, %2, 768;\n add.s64 b7, %2, 896;\n"
+      " add.u32 a1, %1, 16;\n add.u32 a2, %1, 32;\n add.u32 a3, %1, 48;\n"
+      " add.s64 b1, %2, 128;\n add.s64 b2, %2, 256;\n add.s64 b3, %2, 384;\n"
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p0;\n"
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, p1;\n"
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, p1;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, p1;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [a4], b4, %3, p1;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [a5], b5, %3, p1;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [a6], b6, %3, p1;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [a7], b7, %3, p1;\n}\n" ::"r"(d_tmem),
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, p1;\n}\n" ::"r"(d_tmem),
       "r"(a0), "l"(b0), "r"(idesc), "r"(first)
       : "memory");
 }
