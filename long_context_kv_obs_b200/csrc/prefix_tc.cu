@@ -17,7 +17,10 @@
 // one item and the start of the next).  A partial record (m, sum, O) leaves for every item a
 // run touches; the item's runs are consecutive, so the combine kernel finds them by arithmetic.
 // MT = 1 (B * G <= 128): the two softmax warpgroups take the even and the odd tiles of a run, each
-// with its own running state.  MT = 2: both take every tile, with 128 query rows each, so K and V
+// with its own running state.  A warp can read the TMEM lanes of its own quarter only, and the
+// quarters are the SM's schedulers: for up to 64 rows the M = 128 tile holds them twice, the first
+// warpgroup works on the lower copy and the second on the upper, so that all schedulers have a part
+// (56 rows with R: 96 us with half of them idle, 92 so).  MT = 2: both take every tile, with 128 query rows each, so K and V
 // are fetched once for 256 rows.
 //
 // Roles: warps 0-3 and 4-7 are the softmax warpgroups (a thread owns a query row, its TMEM lane),
@@ -285,10 +288,12 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     // ------------------------------------------------------------ softmax
-    const int w = warp >> 2, row = (warp & 3) * 32 + lane;   // row = TMEM lane
+    const int w = warp >> 2;
     const uint32_t tS = tmem + w * 128 + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t tO = tS + 256;
     const int rows = p.B * p.G;
+    const bool twice = MT == 1 && rows <= 64;    // see the head of the file
+    const int row0 = (warp & 3) * 32 - (twice ? w * 64 : 0);   // the warp's first row of a record
     const int wt = threadIdx.x & 127;
     uint32_t steps = 0, tc = 0, nseg = 0;
     bool ok = true;
@@ -308,7 +313,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
         constexpr int CH = D / 8, WR = 16 * MT;  // 16-byte chunks a row, rows a warp
 #pragma unroll
         for (int x = lane; x < WR * CH; x += 32) {
-          const int qr = warp * WR + x / CH, ch = x % CH, R = r0 + qr;
+          const int qr = warp * WR + x / CH, ch = x % CH, R = r0 + (twice ? qr & 63 : qr);
           const int b = R / p.G, gg = R - b * p.G;
           const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(p.q) +
                                    (((int64_t)b * p.L + sg.l) * p.Hq + sg.g * p.G + gg) * D;
@@ -320,8 +325,8 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
         __syncwarp();
         if (lane == 0) mbar_arrive(&c->q_ready);
       }
-      const int Rw = r0 + (MT == 2 ? w * 128 : 0) + (warp & 3) * 32;   // the warp's first query row
-      const bool live = Rw < rows;
+      const int Rw = r0 + (MT == 2 ? w * 128 : 0) + row0;   // the warp's first query row
+      const bool live = Rw < rows && (!twice || ((warp & 3) >> 1) == w);
       float m = -INFINITY, lsum = 0.f;
       const float* Rr = HAS_R ? p.R + sg.l * p.Rsl + sg.g * p.Rsh : nullptr;
       const int i0 = MT == 1 ? w : 0, di = MT == 1 ? 2 : 1;
@@ -480,7 +485,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
       tc += sg.n;
       // the piece's record of this warpgroup
       const int64_t group = 2 * (int64_t)(sg.item + blockIdx.x) + w;
-      const int64_t rec = group * 128 + row;
+      const int64_t rec = group * 128 + row0 + lane;
       // its rows go to memory through the Q area: all S products of the piece are done first
       __syncwarp();
       if (lane == 0) mbar_arrive(&c->s_done);
@@ -502,7 +507,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
           // (a lane that stores its own row, 16 bytes here and there, cost one layer 1.8 of 12.3 us)
           constexpr int CC = D / 4;              // dimensions at a time
           uint8_t* stage = Qs + warp * (32 * CC * 4);
-          float* dst = p.pp.o + group * 128 * D + (int64_t)((warp & 3) * 32) * D;
+          float* dst = p.pp.o + group * 128 * D + (int64_t)row0 * D;
 #pragma unroll
           for (int d0 = 0; d0 < D; d0 += CC) {
 #pragma unroll
