@@ -240,3 +240,50 @@ def test_calls_on_another_stream_and_wrong_arguments():
     with pytest.raises(TypeError):
         B.kvc_page_append(m, k=k, v=v, K=K, V=V, slots=torch.zeros(4, dtype=torch.int64, device=DEV))
     assert B.kvc_launch_count() == before
+
+
+@pytest.mark.parametrize("rows,skip", [(40001, 0), (9001, 1)])
+def test_page_tables_many_rows_one_long_among_short_and_unaligned_lengths(rows, skip):
+    """Many rows to a thread, one row as long as a thousand others, lengths at any alignment."""
+    rng = np.random.default_rng(rows)
+    page = 64
+
+    def new_of(r, a):
+        new_of.n += 1
+        return 30000 if new_of.n == rows // 3 else int(r.integers(0, 60))
+
+    new_of.n = 0
+    lens, new, table, ring, head, count = make(rng, rows, page, 50, new_of)
+    total = sum(max(0, z - a) for a, z in zip(lens, new))
+    ok, et, er, es, el, esl, est = serving.page_tables(lens, new, table, ring, head, count, page, total + 70)
+    assert ok
+    off = lambda x: i32(np.concatenate([np.full(skip, -9), x]).astype(np.int64))[skip:]
+    t_table, t_ring = i32(table), i32(ring)
+    lens_out, state_out = torch.full((rows,), -7, dtype=torch.int32, device=DEV), i32([0, 0])
+    slots, start = i32(np.full(total + 70, -5)), i32(np.full(rows + 1, -5))
+    B.kvc_page_tables(lens=off(lens), lens_new=off(new), table=t_table, ring=t_ring, state=i32([head, count]), page=page,
+                      state_out=state_out, lens_out=lens_out, slots=slots, slot_start=start)
+    assert B.kvc_check_status() == 0
+    for got, want in ((t_table, et), (t_ring, er), (state_out, es), (lens_out, el), (slots, esl), (start, est)):
+        np.testing.assert_array_equal(got.cpu().numpy(), np.asarray(want))
+
+
+def test_page_tables_without_slots_and_pools_on_two_streams():
+    """Tables alone (no slot map, no starts), two pools resized at once on streams of their own."""
+    rng = np.random.default_rng(77)
+    runs = []
+    for k in range(2):
+        lens, new, table, ring, head, count = make(rng, 700 + k, 32, 400, GROW["mixed"])
+        ok, et, er, es, el, _, _ = serving.page_tables(lens, new, table, ring, head, count, 32)
+        assert ok
+        runs.append(dict(lens=i32(lens), lens_new=i32(new), table=i32(table), ring=i32(ring), state=i32([head, count]),
+                         state_out=i32([0, 0]), lens_out=i32(np.zeros(len(lens))), want=(et, er, es, el)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for r, s in zip(runs, streams):
+        B.kvc_page_tables(page=32, stream=s, **{k: v for k, v in r.items() if k != "want"})
+    torch.cuda.synchronize()
+    assert B.kvc_check_status() == 0
+    for r in runs:
+        for got, want in zip((r["table"], r["ring"], r["state_out"], r["lens_out"]), r["want"]):
+            np.testing.assert_array_equal(got.cpu().numpy(), np.asarray(want))

@@ -320,3 +320,56 @@ def test_refusals_launch_nothing():
                                  o=torch.zeros(2, 1, 18, 128, device=DEV), K_prefix=c.Kp, V_prefix=c.Vp,
                                  lens_prefix=i32([64]), max_len_prefix=64)
     assert B.kvc_launch_count() == before
+
+
+@pytest.mark.parametrize("merged", [False, True])
+@pytest.mark.parametrize("B_,G,d", [(13, 5, 128), (32, 4, 128), (16, 4, 64), (43, 3, 64), (32, 8, 128), (37, 7, 128)])
+def test_row_counts_at_the_tiles_borders(B_, G, d, merged):
+    """64, 65, 128, 129, 256 and 259 query rows a KV head."""
+    c = Case(B_, 2, 2, G, d, 400, 30, 16, merged=merged, seed=B_)
+    c.run()
+    assert B.kvc_check_status() == 0
+    c.check()
+
+
+@pytest.mark.parametrize("B_", [3, 40])
+def test_prompts_that_end_at_and_beside_half_tiles(B_):
+    ends = [0, 1, 63, 64, 65, 127, 128, 129, 191, 192, 193, 255, 256, 257]
+    c = Case(B_, len(ends), 1, 4, 128, 257, 20, 16, seed=40, lens_p=ends, merged=B_ == 3)
+    c.run()
+    assert B.kvc_check_status() == 0
+    c.check()
+
+
+def test_more_layers_than_the_tensor_core_kernel_takes():
+    c = Case(2, 130, 1, 2, 64, 40, 20, 16, seed=41, merged=True)
+    c.run()
+    assert B.kvc_check_status() == 0
+    c.check()
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
+def test_calls_on_two_streams_at_once_and_back_to_back(dt):
+    """Every call's kernels overlap at their ends: neither another stream's call nor the next on the same
+    stream, on the same workspace, may see half a result."""
+    cases = [Case(9, 2, 2, 4, 128, 900, 300, 16, seed=s, dt=dt, merged=s % 2 == 1) for s in (42, 43, 44)]
+    want = []
+    for c in cases:
+        c.run()
+        want.append(c.o.clone())
+    assert B.kvc_check_status() == 0
+    kws = [c.kw() for c in cases]
+    ws = [B.kvc_prefix_decode_attn(c.m, **kw) for c, kw in zip(cases[:2], kws[:2])]
+    torch.cuda.synchronize()
+    outs = [[torch.full_like(c.o, float("nan")) for _ in range(8)] for c in cases]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for i in range(8):
+        for k, s in enumerate(streams):
+            # the second stream's calls alternate between two inputs on one workspace
+            j = k if k == 0 or i % 2 == 0 else 2
+            B.kvc_prefix_decode_attn(cases[j].m, workspace=ws[k], stream=s, **{**kws[j], "o": outs[j][i]})
+    torch.cuda.synchronize()
+    assert B.kvc_check_status() == 0
+    for i in range(8):
+        assert torch.equal(outs[0][i], want[0])
+        assert torch.equal(outs[1 if i % 2 == 0 else 2][i], want[1 if i % 2 == 0 else 2])

@@ -236,3 +236,37 @@ def test_bf16_border_parameters():
     zi = z.clone()
     zi[:, 7] = INF
     check(zi, 0.7, temperature=[1.0, 0.5, 2.0, INF, 1e-40, 30.0, 1.0, 1.0], top_p=0.9, min_p=0.1)
+
+
+def test_calls_on_two_streams_and_captured_twice():
+    z = [rows(20, 30011, BF, 30), rows(20, 30011, FP, 31)]
+    u = torch.rand(20, device=DEV)
+    par = dict(temperature=torch.full((20,), 0.8, device=DEV), top_p=torch.full((20,), 0.9, device=DEV))
+    want = []
+    for x in z:
+        tok = torch.empty(20, dtype=torch.int32, device=DEV)
+        B.kvc_sample(logits=x, u=u, token=tok, **par)
+        want.append(tok)
+    toks = [torch.full((20,), -9, dtype=torch.int32, device=DEV) for _ in z]
+    graphs = []
+    torch.cuda.synchronize()
+    for x, tok in zip(z, toks):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            B.kvc_sample(logits=x, u=u, token=tok, **par)
+        graphs.append(g)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(toks, want))
+    for s, x, tok in zip(streams, z, toks):
+        tok.fill_(-9)
+        torch.cuda.synchronize()
+        B.kvc_sample(logits=x, u=u, token=tok, stream=s, **par)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(toks, want))
+    assert B.kvc_check_status() == 0
