@@ -23,10 +23,9 @@
 //      index order for the token
 //   C  else the cut is searched: counts or masses by bins below the maximum (shared-memory integer
 //      atomics: order does not matter), summed over the cluster through distributed shared memory.
-//      Every CTA reads all histograms of the cluster, which is why there are no more bins.
 //      bf16: 2048 bins hold one value each (those nearest zero share one), so counts give masses to
 //      fp64, the border's bin is the cut's value, and of its ties the lowest indices stay.  4096 bins
-//      leave fewer rows in doubt (below), but took a row over 16 CTAs from 33 to 62 us.
+//      leave fewer rows in doubt (below), but take too long to sum (a row over 16 CTAs: 33 -> 62 us).
 //      fp32: 512 bins of the distance below the maximum.  A quarter of the row is summed first, in
 //      fp32: a lower bound S of the mass.  Tokens below (1 - top_p) S / V together hold less than the
 //      1 - top_p that is cut: they stay out, and the bins spread over what is left (atomics that meet in
@@ -60,14 +59,15 @@ constexpr float SP_ONE = 8388608.f;             // 2^23: adding it leaves the ro
 struct alignas(16) SpShared {                   // the slice follows: its vectors are 16-byte aligned
   union {
     struct {
-      unsigned hist[2][2 * SP_BINS];            // two searches deep: counts or masses; two 16-bit limbs of a mass
-      unsigned wide[2][SP_WIDE];                // two searches deep: counts by key
-      unsigned total[SP_WIDE];                  // the cluster's, of the last such search
+      unsigned hist[2 * SP_BINS];               // counts or masses; two 16-bit limbs of a mass
+      unsigned sum[2 * SP_BINS];                // the cluster's
+      unsigned wide[SP_WIDE];                   // counts by value
+      unsigned total[SP_WIDE];                  // the cluster's
     };
     unsigned long long list[SP_LIST];
   };
   uint2 table[256];                             // 2^(j / 256): in 2^-30 units, and as an fp32
-  double part[2];                               // beside a histogram: the mass of the slice, to fp32
+  double part;                                  // beside a histogram: the mass of the slice, to fp32
   unsigned long long xch[2][SP_MAXC][2];        // values of every CTA of the cluster, two steps deep
   double red[SP_WARPS];
   double found[4];
@@ -243,34 +243,50 @@ __device__ __noinline__ double sp_weight(float z, float zmax, float zlow, double
   return __hiloint2double(__double2hiint(w) + (e << 20), __double2loint(w));
 }
 
+// The sums over the cluster of `words` words at src, in every CTA's `sum` (both at one place in all
+// of them; words a multiple of 4 C).  Each CTA adds up its share of the words, 16 bytes from a CTA a thread, and
+// hands the result to all: a load and a store a thread, where reading all histograms by all CTAs
+// took 19k cycles for 2048 bins on 16 of them.  After the call src may be written again.
+__device__ __noinline__ void sp_cluster_add(unsigned* src, unsigned* sum, int words, int C, int rank) {
+  cg::cluster_group cl = cg::this_cluster();
+  const int quads = words / (4 * C);            // of a CTA's share
+  for (int j = threadIdx.x; j < quads; j += SP_THREADS)
+    reinterpret_cast<uint4*>(sum)[rank * quads + j] = make_uint4(0, 0, 0, 0);
+  cl.sync();
+  for (int j = threadIdx.x; j < quads * C; j += SP_THREADS) {
+    const int r = j / quads, w = 4 * (rank * quads + j - r * quads);
+    const uint4 x = *reinterpret_cast<const uint4*>(cl.map_shared_rank(src + w, (rank + r) & (C - 1)));
+    if (x.x) atomicAdd(sum + w, x.x);
+    if (x.y) atomicAdd(sum + w + 1, x.y);
+    if (x.z) atomicAdd(sum + w + 2, x.z);
+    if (x.w) atomicAdd(sum + w + 3, x.w);
+  }
+  __syncthreads();
+  for (int j = threadIdx.x + quads; j < quads * C; j += SP_THREADS) {   // (the first share: its own)
+    const int r = j / quads, w = 4 * (rank * quads + j - r * quads);
+    *reinterpret_cast<uint4*>(cl.map_shared_rank(sum + w, (rank + r) & (C - 1))) = *reinterpret_cast<const uint4*>(sum + w);
+  }
+  cl.sync();
+}
+
 enum { SP_COUNT, SP_SHARE, SP_LIMBS, SP_KEYS };
 // The first bin at which the sum over the cluster's histograms reaches `target` (SHARE: that share of
 // the cluster's `part`), or the last that holds something: returned, with the sum before it in
 // found[0] and the bin's own value in found[1].  What a word of bin i stands for: COUNT, 1; SHARE, 2^-15
 // of the weight at the bin's middle (bins `octaves` wide); LIMBS, 1, and a word of the histogram's second half 2^16; KEYS,
-// the weight of key first - i in 2^-(31 + e) units.  Every CTA reads all histograms (a thread one bin,
-// its loads all in flight) and scans them for itself: one cluster barrier a search.  The next search
-// uses the other buffer, so a slow reader is not overtaken.
+// the weight of key first - i in 2^-(31 + e) units.  A thread has one bin.
 template <int KS>
-__device__ __noinline__ int sp_border(int kind, double target, int C, int rank, int buf, uint32_t first, int e, float zmax,
+__device__ __noinline__ int sp_border(int kind, double target, int C, int rank, uint32_t first, int e, float zmax,
                                       float zlow, double c, float octaves) {
   static_assert(SP_BINS == SP_THREADS, "a bin a thread");
   cg::cluster_group cl = cg::this_cluster();
   SpShared& sh = sp_sh();
-  cl.sync();
+  sp_cluster_add(sh.hist, sh.sum, kind == SP_LIMBS ? 2 * SP_BINS : SP_BINS, C, rank);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  unsigned long long h = 0;
-  if (kind == SP_LIMBS) {
-#pragma unroll
-    for (int r = 0; r < SP_MAXC; ++r)
-      if (r < C)
-        h += (unsigned long long)cl.map_shared_rank(&sh.hist[buf][SP_BINS], (rank + r) & (C - 1))[threadIdx.x] << 16;
-  }
-#pragma unroll
-  for (int r = 0; r < SP_MAXC; ++r)             // each CTA begins with its own: no one is asked by all at once
-    if (r < C) h += cl.map_shared_rank(&sh.hist[buf][0], (rank + r) & (C - 1))[threadIdx.x];
+  unsigned long long h = sh.sum[threadIdx.x];
+  if (kind == SP_LIMBS) h += (unsigned long long)sh.sum[SP_BINS + threadIdx.x] << 16;
   if (kind == SP_SHARE && warp == 0) {
-    double m = lane < C ? *cl.map_shared_rank(&sh.part[buf], lane) : 0.0;
+    double m = lane < C ? *cl.map_shared_rank(&sh.part, lane) : 0.0;
     m = warp_sum_d(m);
     if (lane == 0) sh.found[3] = target * m;
   }
@@ -336,26 +352,14 @@ struct SpWide {
 // values, taken at its middle) reach `target`, a share of their sum for masses, or the last that holds
 // something: returned, with the sum before it in found[0] and all of them in found[1].  For masses found[2] and
 // found[3] bound the mass of the row, of at most V tokens.  A thread has four bins.
-__device__ __noinline__ int sp_wide_border(bool mass, double target, int C, int rank, int buf, SpWide wd, float zmax,
+__device__ __noinline__ int sp_wide_border(bool mass, double target, int C, int rank, SpWide wd, float zmax,
                                            float zlow, double c, int V) {
   static_assert(SP_WIDE == 4 * SP_THREADS, "four bins a thread");
-  cg::cluster_group cl = cg::this_cluster();
   SpShared& sh = sp_sh();
-  cl.sync();
+  sp_cluster_add(sh.wide, sh.total, (wd.n + 4 * C - 1) / (4 * C) * (4 * C), C, rank);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b0 = 4 * threadIdx.x;
   uint4 h = make_uint4(0, 0, 0, 0);
-  if (b0 < wd.n) {
-#pragma unroll
-    for (int r = 0; r < SP_MAXC; ++r)
-      if (r < C) {
-        const uint4 x = *reinterpret_cast<const uint4*>(cl.map_shared_rank(&sh.wide[buf][b0], (rank + r) & (C - 1)));
-        h.x += x.x;
-        h.y += x.y;
-        h.z += x.z;
-        h.w += x.w;
-      }
-    *reinterpret_cast<uint4*>(sh.total + b0) = h;
-  }
+  if (b0 < wd.n) h = *reinterpret_cast<const uint4*>(sh.total + b0);
   double v[4], sum = 0.0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -415,7 +419,7 @@ template <typename T>
 struct SpRow {
   static constexpr int N = SpVec<T>::N, KS = SpVec<T>::KSHIFT;
   int C, rank, nvec, i0;                        // cluster size, rank, vectors of the slice, its first index
-  int step, search;
+  int step;
   float zmax, ybin;                             // bins below the maximum: (zmax - z) * ybin
   float zlow;                                   // weights below this one's, 2^-64 of the largest, are nothing
   double c;                                     // log2(e) / T
@@ -445,9 +449,7 @@ struct SpRow {
     return all;
   }
   __device__ __forceinline__ int border(int kind, double target, uint32_t first, int e) {
-    const int b = sp_border<KS>(kind, target, C, rank, search & 1, first, e, zmax, zlow, c, octaves());
-    ++search;
-    return b;
+    return sp_border<KS>(kind, target, C, rank, first, e, zmax, zlow, c, octaves());
   }
   __device__ __forceinline__ float octaves() const { return ybin > 0.f ? (float)(c / (double)ybin) : 0.f; }   // a bin's width
   __device__ __forceinline__ double weight(float z, int e = 0) const { return sp_weight(z, zmax, zlow, c, e); }
@@ -489,9 +491,9 @@ struct SpRow {
     return fminf(zmax, key2f(f2key(zmax - ((float)b - 0.501f) / ybin) + 1u));
   }
 
-  // The histogram of this search, cleared for use (its words are used again two searches on).
+  // The histogram, cleared for use.
   __device__ __forceinline__ unsigned* clear_hist(int words) {
-    unsigned* h = sp_sh().hist[search & 1];
+    unsigned* h = sp_sh().hist;
 #pragma unroll 1
     for (int j = threadIdx.x; j < words / 4; j += SP_THREADS) reinterpret_cast<uint4*>(h)[j] = make_uint4(0, 0, 0, 0);
     __syncthreads();
@@ -513,7 +515,7 @@ struct SpRow {
 
   // Counts of the tokens left, by bins of one bf16 value each (of zero's neighbours, see SpWide).
   __device__ __forceinline__ void wide_hist(const SpWide& wd) const {
-    unsigned* h = sp_sh().wide[search & 1];
+    unsigned* h = sp_sh().wide;
     *reinterpret_cast<uint4*>(h + 4 * threadIdx.x) = make_uint4(0, 0, 0, 0);
     __syncthreads();
     if (cut) {
@@ -545,9 +547,7 @@ struct SpRow {
     }
   }
   __device__ __forceinline__ int wide_border(bool mass, double target, const SpWide& wd, int V) {
-    const int b = sp_wide_border(mass, target, C, rank, search & 1, wd, zmax, zlow, c, V);
-    ++search;
-    return b;
+    return sp_wide_border(mass, target, C, rank, wd, zmax, zlow, c, V);
   }
 
   // The index of tie `want` (from 1) of zt in this slice, by the ties of every stretch: ifound[1], set by one thread.
@@ -631,10 +631,10 @@ struct SpRow {
     if (take < 1.0) take = 1.0;
     tidx = INT_MAX;
     if (take >= ties) return true;
-    // ties of every 32-vector stretch, in the histogram words of the next search
+    // ties of every 32-vector stretch, in the histogram's words
     const int lane = threadIdx.x & 31;
     const float zt = sp_value<KS>(tkey);
-    unsigned* count = sh.hist[search & 1];
+    unsigned* count = sh.hist;
     double mine = 0.0;
     const typename SpVec<T>::Range range(zt, zt);
 #pragma unroll 1
@@ -692,7 +692,7 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
   const int row = blockIdx.x / s.C, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   s.i0 = s.rank * per_cta;
   s.nvec = max(0, min(per_cta, p.V - s.i0) + N - 1) / N;
-  s.step = s.search = 0;
+  s.step = 0;
   s.cut = false;
   const T* z0 = reinterpret_cast<const T*>(p.logits) + row * p.row_stride;
 
@@ -970,7 +970,7 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
       if (run) atomicAdd(hist + rb, run);
     }
     const double whole = sp_block_sum((double)part);
-    if (tid == 0) sh.part[s.search & 1] = whole;
+    if (tid == 0) sh.part = whole;
     b = s.border(SP_SHARE, top_p, 0, 0);
   } else if (use_p) {
     b = 0;                                      // top_p <= 0: one token
@@ -987,7 +987,7 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
     const double w = use_p ? s.weight(high) : 0.0, share = fmax(top_p, 0.0);
     const double least = sh.found[2] * (1.0 - 1e-12), most = sh.found[3] * (1.0 + 1e-12);   // beside fp64's own errors
     if (use_p && wd.single(b) && w > 0.0 && (most - least) * share <= 0.25 * w) {
-      unsigned* count = sh.hist[s.search & 1];
+      unsigned* count = sh.hist;
       double before_b = 0.0, same = 0.0;
       const typename SpVec<T>::Range front(high, INFINITY);
 #pragma unroll 1
