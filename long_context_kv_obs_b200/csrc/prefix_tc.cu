@@ -42,8 +42,11 @@ constexpr int PX_KEYS = 128;                    // keys a tile
 constexpr int PX_THREADS = 384;                 // warp 11 only completes the third warpgroup
 constexpr int PX_ATOM = PX_KEYS * 128;          // 128 rows x 64 bf16, 128B-swizzled (16 KB)
 template <int D> constexpr int px_tile() { return (D / 64) * PX_ATOM; }
-template <int D, int MT> constexpr int px_nk() { return D == 64 ? 4 : (MT == 1 ? 3 : 2); }
-template <int D, int MT> constexpr int px_nv() { return D == 64 ? 4 : 3; }
+// Slots of the K and V rings.  MT = 1: even, and tile t goes to warpgroup t & 1, so that a slot is always the
+// same warpgroup's: who waits by parity must see every phase of a barrier (with three slots a warpgroup saw
+// every other one, and took a phase long past for the one it wanted when loads were late).
+template <int D, int MT> constexpr int px_nk() { return D == 64 ? 4 : 2; }
+template <int D, int MT> constexpr int px_nv() { return D == 64 || MT == 1 ? 4 : 3; }
 struct PxCtl {
   uint64_t fullK[4], emptyK[4], fullV[4], emptyV[4];
   uint64_t s_ready[2], p_ready[2][2], o_ready[2], b_ready[2], q_ready, q_free, s_done, drain;
@@ -130,6 +133,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1)
 prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
                  const __grid_constant__ PrefixParams p) {
   constexpr int TILE = px_tile<D>(), NK = px_nk<D, MT>(), NV = px_nv<D, MT>(), NA = D / 64;
+  static_assert(MT == 2 || (NK % 2 == 0 && NV % 2 == 0), "a slot belongs to one warpgroup");
   extern __shared__ __align__(1024) uint8_t px_raw[];
   uint8_t* Qs = px_raw;
   uint8_t* Ks = Qs + MT * TILE;
@@ -153,7 +157,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
       mbar_init(&c->b_ready[w], 4);
     }
     mbar_init(&c->q_ready, 8);
-    mbar_init(&c->q_free, 8);
+    mbar_init(&c->q_free, 10);                  // the softmax warps, and the product warps, which have seen q_ready
     mbar_init(&c->s_done, 8);
     mbar_init(&c->drain, 2);
     c->abort = 0;
@@ -228,7 +232,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
       constexpr uint32_t idS = idesc_bf16(128, PX_KEYS);
       constexpr uint32_t idO = idesc_bf16(128, D) | IDESC_B_MN;
       const int w = __shfl_sync(FULL, warp - 9, 0);
-      const int i0 = MT == 1 ? w : 0, di = MT == 1 ? 2 : 1;
+      constexpr int di = MT == 1 ? 2 : 1;
       const uint32_t ts = __shfl_sync(FULL, tmem, 0) + w * 128, to = ts + 256;
       const uint32_t q0 = __shfl_sync(FULL, smem_u32(Qs), 0), k0 = q0 + MT * TILE, v0 = k0 + NK * TILE;
       const uint64_t dq = sw128_desc_at(q0 + (MT == 2 ? w : 0) * TILE, 16);
@@ -237,7 +241,9 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
       while (ok && run.next(p, c->cum, sg)) {
         ok = __all_sync(FULL, mbar_wait(&c->q_ready, nseg & 1, abort, p.status));
         ++nseg;
-        const int n = __shfl_sync(FULL, sg.n, 0);
+        if (lane == 0) mbar_arrive(&c->q_free);
+        __syncwarp();
+        const int n = __shfl_sync(FULL, sg.n, 0), i0 = MT == 1 ? (int)((w ^ tc) & 1) : 0;
         auto issue_s = [&](int i) {
           const uint32_t t = tc + i, ks = t % NK;
           if (!__all_sync(FULL, mbar_wait(&c->fullK[ks], (t / NK) & 1, abort, p.status))) return false;
@@ -329,7 +335,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
       const bool live = Rw < rows && (!twice || ((warp & 3) >> 1) == w);
       float m = -INFINITY, lsum = 0.f;
       const float* Rr = HAS_R ? p.R + sg.l * p.Rsl + sg.g * p.Rsh : nullptr;
-      const int i0 = MT == 1 ? w : 0, di = MT == 1 ? 2 : 1;
+      const int i0 = MT == 1 ? (int)((w ^ tc) & 1) : 0, di = MT == 1 ? 2 : 1;
       float rnext = 1.f;
       if (HAS_R && i0 < sg.n) {
         const int k = (sg.t0 + i0) * PX_KEYS + wt;

@@ -373,3 +373,17 @@ def test_calls_on_two_streams_at_once_and_back_to_back(dt):
     for i in range(8):
         assert torch.equal(outs[0][i], want[0])
         assert torch.equal(outs[1 if i % 2 == 0 else 2][i], want[1 if i % 2 == 0 else 2])
+
+
+@pytest.mark.parametrize("G,merged", [(3, False), (1, True), (8, False)])
+def test_few_rows_on_a_long_prompt_wait_for_late_loads(G, merged):
+    """Bound by HBM, loads come microseconds late and out of order: equal calls give equal bits, right ones."""
+    c = Case(3, 4, 6, G, 128, 20011, 28, 128, merged=merged, seed=50 + G)
+    ws = c.run()
+    assert B.kvc_check_status() == 0
+    first = (c.o.clone(), c.lse.clone())
+    for _ in range(30):
+        c.run(workspace=ws)
+    assert B.kvc_check_status() == 0
+    assert torch.equal(c.o, first[0]) and torch.equal(c.lse, first[1])
+    c.check()
