@@ -659,8 +659,29 @@ struct SpRow {
   }
 };
 
-// a[0, n) sorted downwards, n a power of two (bitonic merges).
-__device__ __noinline__ void sp_sort(unsigned long long* a, int n) {
+// a[0, m) sorted downwards, all different.  Few: each finds its place by counting what is above it, two
+// to a read that all lanes share (256 rows, top-k 50: 84 us with the merges below, 76 so).  More: bitonic
+// merges over n >= m, a power of two, the rest zeros.
+constexpr int SP_COUNTED = 256;
+__device__ __noinline__ void sp_sort(unsigned long long* a, int m, int n) {
+  if (m <= SP_COUNTED) {
+    __syncthreads();
+    const unsigned long long x = (int)threadIdx.x < m ? a[threadIdx.x] : ~0ull;
+    int place = 0;
+    if ((int)(threadIdx.x & ~31u) < m) {
+#pragma unroll 4
+      for (int j = 0; j + 1 < m; j += 2) {
+        const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(a + j);
+        place += (y.x > x) + (y.y > x);
+      }
+      if (m & 1) place += a[m - 1] > x;
+    }
+    __syncthreads();
+    if ((int)threadIdx.x < m) a[place] = x;
+    __syncthreads();
+    return;
+  }
+  for (int i = m + threadIdx.x; i < n; i += SP_THREADS) a[i] = 0ull;
   for (int k = 2; k <= n; k <<= 1)
     for (int j = k >> 1; j > 0; j >>= 1) {
       __syncthreads();
@@ -798,9 +819,7 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
         if (s.rank != 0) return;                // the rest is the first CTA's own
         int np = 2;
         while (np < m) np <<= 1;
-#pragma unroll 1
-        for (int i = m + tid; i < np; i += SP_THREADS) sh.list[i] = 0ull;
-        sp_sort(sh.list, np);
+        sp_sort(sh.list, m, np);
         const int kk = min(k, m);
         // weights in the order, a stretch a thread, and their running sum
         const int Q = (np + SP_THREADS - 1) / SP_THREADS;
@@ -821,12 +840,11 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
         int nk = 2;
         while (nk < keep) nk <<= 1;
 #pragma unroll 1
-        for (int i = tid; i < nk; i += SP_THREADS) {
+        for (int i = tid; i < keep; i += SP_THREADS) {
           const unsigned long long x = sh.list[i];
-          // sorted downwards: index up is ~index down; what is cut sinks
-          sh.list[i] = i < keep ? (x << 32) | (x >> 32) : 0ull;
+          sh.list[i] = (x << 32) | (x >> 32);   // sorted downwards: index up is ~index down
         }
-        sp_sort(sh.list, nk);
+        sp_sort(sh.list, keep, nk);
         sum = 0.0;
         const int Qk = (nk + SP_THREADS - 1) / SP_THREADS;
 #pragma unroll 1
