@@ -30,11 +30,13 @@ __device__ __forceinline__ void ld4(const char* p, int bf16, float (&f)[4]) {
 }
 
 // General form: one CTA a (group of up to 8 query rows, stretch of keys).  D / 4 lanes share a key,
-// four dimensions each; the logits are summed over them by shuffles, the softmax runs online
-// per key group, and the CTA's groups are merged in shared memory.  The lanes of a key hold all
-// of its logits, so no wider exchange is needed.  OWN: the group is the G heads of a
-// (sequence, layer, KV head) row over its own keys; else 8 of the B * G rows of (layer, KV head)
-// over the prompt's.
+// four dimensions each.  Their parts of the 8 logits are summed by halves: at every step a lane keeps half of
+// its rows and gives the other half away, so that it ends with one row's logit (9 shuffles at D = 128, where
+// 8 sums over all lanes took 40) and has that row's maximum, sum and weight to itself; 8 shuffles bring the
+// weights back to all.  Two keys at a time, and the next two are loaded meanwhile.  Bound by issue (7
+// sequences x 4 heads x 8, d = 64, 4013 keys, 3 layers, fp32: 90 us a call before, 61 so).  The key groups are merged
+// in shared memory.  OWN: the group is the G heads of a (sequence, layer, KV head) row over its own keys;
+// else 8 of the B * G rows of (layer, KV head) over the prompt's.
 template <int D, bool OWN>
 __global__ void __launch_bounds__(PG_THREADS) prefix_generic_kernel(const __grid_constant__ PrefixParams p) {
   constexpr int LPK = D / 4, KPW = 32 / LPK, NG = (PG_THREADS / 32) * KPW;   // lanes a key, keys a warp, key groups
@@ -84,11 +86,9 @@ __global__ void __launch_bounds__(PG_THREADS) prefix_generic_kernel(const __grid
     if (OWN) tc::pdl_wait();
     return;
   }
-  float q[PG_ROWS][4], acc[PG_ROWS][4], m[PG_ROWS], ls[PG_ROWS];
+  float q[PG_ROWS][4], acc[PG_ROWS][4];
 #pragma unroll
   for (int r = 0; r < PG_ROWS; ++r) {
-    m[r] = -INFINITY;
-    ls[r] = 0.f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) q[r][e] = acc[r][e] = 0.f;
     if (r < nr) {
@@ -100,62 +100,94 @@ __global__ void __launch_bounds__(PG_THREADS) prefix_generic_kernel(const __grid
     }
   }
   const int esz = p.kbf16 ? 2 : 4;
-  for (int i0 = s0; i0 < s1; i0 += NG) {
-    const int i = i0 + grp;
-    bool valid = i < s1;
-    float kf[4] = {0.f, 0.f, 0.f, 0.f}, vf[4] = {0.f, 0.f, 0.f, 0.f};
-    if (valid) {
-      const char *ka, *va;
-      bool in = true;
-      if (OWN && trow) {
-        const int pg = __ldg(trow + (i >> p.shift)), off = i & ((1 << p.shift) - 1);
-        in = (unsigned)pg < (unsigned)p.n_pages;
-        if (!in) flag(p.status, ST_BOUNDS);
-        ka = Kb + (int64_t)pg * p.Ksb + off * kst;
-        va = Vb + (int64_t)pg * p.Vsb + off * vst;
-      } else {
-        ka = Kb + (int64_t)i * kst;
-        va = Vb + (int64_t)i * vst;
+  constexpr int UK = 2;                         // keys of a lane group at a time
+  struct Key {
+    float k[4], v[4], bias;
+  };
+  auto fetch = [&](int i, Key& x) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x.k[e] = x.v[e] = 0.f;
+    x.bias = -INFINITY;                         // behind the stretch: no weight
+    if (i >= s1) return;
+    x.bias = Rr ? p.alpha_c * log2f(__ldg(Rr + i)) : 0.f;
+    const char *ka, *va;
+    if (OWN && trow) {
+      const int pg = __ldg(trow + (i >> p.shift)), off = i & ((1 << p.shift) - 1);
+      if ((unsigned)pg >= (unsigned)p.n_pages) {
+        flag(p.status, ST_BOUNDS);
+        return;
       }
-      if (in) {
-        ld4(ka + part * 4 * esz, p.kbf16, kf);
-        ld4(va + part * 4 * esz, p.kbf16, vf);
+      ka = Kb + (int64_t)pg * p.Ksb + off * kst;
+      va = Vb + (int64_t)pg * p.Vsb + off * vst;
+    } else {
+      ka = Kb + (int64_t)i * kst;
+      va = Vb + (int64_t)i * vst;
+    }
+    ld4(ka + part * 4 * esz, p.kbf16, x.k);
+    ld4(va + part * 4 * esz, p.kbf16, x.v);
+  };
+  float m = -INFINITY, ls = 0.f;                // of row part / (LPK / 8)
+  Key cur[UK], nxt[UK];
+#pragma unroll
+  for (int u = 0; u < UK; ++u) fetch(s0 + u * NG + grp, cur[u]);
+  for (int i0 = s0; i0 < s1; i0 += UK * NG) {
+#pragma unroll
+    for (int u = 0; u < UK; ++u) fetch(i0 + (UK + u) * NG + grp, nxt[u]);
+    float x[UK];
+#pragma unroll
+    for (int u = 0; u < UK; ++u) {
+      float z[PG_ROWS];
+#pragma unroll
+      for (int r = 0; r < PG_ROWS; ++r) {
+        z[r] = q[r][0] * cur[u].k[0];
+#pragma unroll
+        for (int e = 1; e < 4; ++e) z[r] = fmaf(q[r][e], cur[u].k[e], z[r]);
+      }
+#pragma unroll
+      for (int h = PG_ROWS / 2, o = LPK / 2; h > 0; h >>= 1, o >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int r = 0; r < h; ++r) {
+          const float mine = up ? z[r + h] : z[r], theirs = up ? z[r] : z[r + h];
+          z[r] = mine + __shfl_xor_sync(FULL, theirs, o);
+        }
+      }
+#pragma unroll
+      for (int o = LPK / 16; o > 0; o >>= 1) z[0] += __shfl_xor_sync(FULL, z[0], o);
+      x[u] = z[0] + cur[u].bias;
+    }
+    const float top = fmaxf(x[0], x[1]);
+    const bool grow = top > m + 8.f;
+    if (__any_sync(FULL, grow)) {
+      const float corr = grow ? exp2f(m - top) : 1.f;   // 0 while nothing was seen
+      if (grow) m = top;
+      ls *= corr;
+#pragma unroll
+      for (int r = 0; r < PG_ROWS; ++r) {
+        const float cr = __shfl_sync(FULL, corr, r * (LPK / 8), LPK);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[r][e] *= cr;
       }
     }
-    float z[PG_ROWS];
 #pragma unroll
-    for (int r = 0; r < PG_ROWS; ++r) {
-      z[r] = q[r][0] * kf[0];
+    for (int u = 0; u < UK; ++u) {
+      const float w = x[u] == -INFINITY ? 0.f : exp2f(x[u] - m);
+      ls += w;
 #pragma unroll
-      for (int e = 1; e < 4; ++e) z[r] = fmaf(q[r][e], kf[e], z[r]);
-    }
+      for (int r = 0; r < PG_ROWS; ++r) {
+        const float wr = __shfl_sync(FULL, w, r * (LPK / 8), LPK);
 #pragma unroll
-    for (int o = LPK / 2; o > 0; o >>= 1)
-#pragma unroll
-      for (int r = 0; r < PG_ROWS; ++r) z[r] += __shfl_xor_sync(FULL, z[r], o);
-    const float bias = Rr && valid ? p.alpha_c * log2f(__ldg(Rr + i)) : 0.f;
-#pragma unroll
-    for (int r = 0; r < PG_ROWS; ++r) {
-      const float x = valid ? z[r] + bias : -INFINITY;
-      if (x > m[r] + 8.f) {
-        const float corr = exp2f(m[r] - x);
-        m[r] = x;
-        ls[r] *= corr;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[r][e] *= corr;
+        for (int e = 0; e < 4; ++e) acc[r][e] = fmaf(wr, cur[u].v[e], acc[r][e]);
       }
-      const float w = x == -INFINITY ? 0.f : exp2f(x - m[r]);
-      ls[r] += w;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[r][e] = fmaf(w, vf[e], acc[r][e]);
+      cur[u] = nxt[u];
     }
   }
   // merge the CTA's key groups
   __shared__ float sm_o[NG][PG_ROWS][D];
   __shared__ float2 sm_ml[NG][PG_ROWS];
+  if (part % (LPK / 8) == 0) sm_ml[grp][part / (LPK / 8)] = make_float2(m, ls);
 #pragma unroll
   for (int r = 0; r < PG_ROWS; ++r) {
-    if (part == 0) sm_ml[grp][r] = make_float2(m[r], ls[r]);
     *reinterpret_cast<float4*>(&sm_o[grp][r][part * 4]) = make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]);
   }
   __syncthreads();
