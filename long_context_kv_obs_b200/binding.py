@@ -729,16 +729,12 @@ def _cache(t: torch.Tensor, lead: tuple, d: int, name: str) -> KV:
     """KV descriptor of a cache whose leading sizes must be `lead` (None: any), then tokens, then rows of
     d contiguous elements.  A dimension of one element gets the stride its inner neighbour implies."""
     sh, st = t.shape, t.stride()
-    n = len(lead)
-    ok = len(sh) == n + 2 and sh[n + 1] == d and st[n + 1] == 1
-    if ok:
-        for i in range(n):
-            if lead[i] is not None and sh[i] != lead[i]:
-                ok = False
-    if not ok:
+    n, first = len(lead), lead[0]             # n: 2 or 3
+    if len(sh) != n + 2 or sh[-1] != d or st[-1] != 1 or sh[-3] != lead[-1] or (first is not None and sh[0] != first) \
+            or (n == 3 and sh[1] != lead[1]):
         raise ValueError(f"{name} must be {''.join('[any]' if x is None else f'[{x}]' for x in lead)}[tokens][{d}] with "
                          "contiguous rows")
-    if 1 in sh[:n + 1]:
+    if 1 in sh:
         st = list(st)
         for i in range(n, -1, -1):
             if sh[i] == 1:
@@ -748,7 +744,7 @@ def _cache(t: torch.Tensor, lead: tuple, d: int, name: str) -> KV:
         raise TypeError(f"unsupported dtype {t.dtype}")
     if n == 3:                                # [B][L][Hkv]
         return KV(t.data_ptr(), code, st[0], st[1], st[2], st[3])
-    if lead[0] is None:                       # [pages][Hkv]
+    if first is None:                         # [pages][Hkv]
         return KV(t.data_ptr(), code, st[0], 0, st[1], st[2])
     return KV(t.data_ptr(), code, 0, st[0], st[1], st[2])   # [L][Hkv]
 
