@@ -807,21 +807,20 @@ def kvc_page_append(m: Model, *, k, v, K, V, slots, stream=None):
     of the pools K, V [n_pages][Hkv][page][d]; negative slots are skipped."""
     _one_device(k, v, K, V, slots)
     H, d = m.n_kv_heads, m.head_dim
-    a = PageAppendArgs()
-    if k.dim() != 3 or k.shape != v.shape or k.shape[1] != H or k.shape[2] != d or k.stride(2) != 1 or v.stride(2) != 1:
+    ks, kt, vt, pool = k.shape, k.stride(), v.stride(), K.shape
+    if len(ks) != 3 or v.shape != ks or ks[1] != H or ks[2] != d or kt[2] != 1 or vt[2] != 1:
         raise ValueError(f"k and v must be [T][{H}][{d}] with contiguous rows")
-    if K.shape != V.shape:
+    if V.shape != pool:
         raise ValueError("K and V must have one shape")
-    T = k.shape[0]
-    a.T, a.page, a.n_pages = T, K.shape[2], K.shape[0]
-
-    def src(t):
-        return KV(t.data_ptr(), _dt(t), 0, 0, t.stride(1) if H > 1 else d, t.stride(0) if T > 1 else H * d)
-
+    T = ks[0]
     if T == 0:
         return
-    a.k, a.v, a.K, a.V = src(k), src(v), _cache(K, (None, H), d, "K"), _cache(V, (None, H), d, "V")
-    a.slots = _flat(slots, "slots", torch.int32, T)
+
+    def src(t, st):
+        return KV(t.data_ptr(), _dt(t), 0, 0, st[1] if H > 1 else d, st[0] if T > 1 else H * d)
+
+    pools = _cache(K, (None, H), d, "K"), _cache(V, (None, H), d, "V")
+    a = PageAppendArgs(T, pool[2], pool[0], src(k, kt), src(v, vt), *pools, _flat(slots, "slots", torch.int32, T))
     _check(lib().kvc_page_append(C.byref(m), C.byref(a), _raw_stream(stream)))
 
 
