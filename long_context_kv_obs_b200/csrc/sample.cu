@@ -275,16 +275,32 @@ enum { SP_COUNT, SP_SHARE, SP_LIMBS, SP_KEYS };
 // found[0] and the bin's own value in found[1].  What a word of bin i stands for: COUNT, 1; SHARE, 2^-15
 // of the weight at the bin's middle (bins `octaves` wide); LIMBS, 1, and a word of the histogram's second half 2^16; KEYS,
 // the weight of key first - i in 2^-(31 + e) units.  A thread has one bin.
+// A CTA's words hold what its slice (40960 elements at most) can bring: 65535 or 2^(15 + 1/16) each, below
+// 2^32.  A row's need not: SHARE gives up its last e bits before the cluster's sum, and a CTA's limbs
+// (below 2^48 together) are cut anew at bit 28, so that 16 CTAs' lower halves stay below 2^32.
 template <int KS>
 __device__ __noinline__ int sp_border(int kind, double target, int C, int rank, uint32_t first, int e, float zmax,
                                       float zlow, double c, float octaves) {
   static_assert(SP_BINS == SP_THREADS, "a bin a thread");
   cg::cluster_group cl = cg::this_cluster();
   SpShared& sh = sp_sh();
+  if (kind == SP_LIMBS || (kind == SP_SHARE && e > 0)) {
+    __syncthreads();
+    unsigned& lo = sh.hist[threadIdx.x];
+    if (kind == SP_LIMBS) {
+      unsigned& hi = sh.hist[SP_BINS + threadIdx.x];
+      const unsigned long long v = ((unsigned long long)hi << 16) + lo;
+      lo = (unsigned)v & 0xfffffffu;
+      hi = (unsigned)(v >> 28);
+    } else {
+      lo = (lo + (1u << (e - 1))) >> e;
+    }
+  }
   sp_cluster_add(sh.hist, sh.sum, kind == SP_LIMBS ? 2 * SP_BINS : SP_BINS, C, rank);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   unsigned long long h = sh.sum[threadIdx.x];
-  if (kind == SP_LIMBS) h += (unsigned long long)sh.sum[SP_BINS + threadIdx.x] << 16;
+  if (kind == SP_LIMBS) h += (unsigned long long)sh.sum[SP_BINS + threadIdx.x] << 28;
+  if (kind == SP_SHARE) h <<= e;
   if (kind == SP_SHARE && warp == 0) {
     double m = lane < C ? *cl.map_shared_rank(&sh.part, lane) : 0.0;
     m = warp_sum_d(m);
@@ -989,7 +1005,7 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
     }
     const double whole = sp_block_sum((double)part);
     if (tid == 0) sh.part = whole;
-    b = s.border(SP_SHARE, top_p, 0, 0);
+    b = s.border(SP_SHARE, top_p, 0, p.V > 125000 ? 2 : 0);   // 125000 2^(15 + 1/16) < 2^32
   } else if (use_p) {
     b = 0;                                      // top_p <= 0: one token
   }

@@ -270,3 +270,44 @@ def test_calls_on_two_streams_and_captured_twice():
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(toks, want))
     assert B.kvc_check_status() == 0
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
+@pytest.mark.parametrize("V", [125515, 131072, 152064, 262144])
+def test_large_flat_rows(V, dt):
+    """Nearly all tokens of a large vocabulary within one bin of the search: its sums over the row pass 2^32."""
+    r = np.random.default_rng(V)
+    g = torch.Generator(device=DEV).manual_seed(V)
+    z = torch.zeros(9, V, device=DEV)
+    z[1] = 1.5
+    z[2, 12345] = 0.01                                               # in the search's first bin, beside the others' value
+    z[3] = INF
+    z[4] = torch.where(torch.rand(V, device=DEV, generator=g) < 0.5, 0.0, -0.0005)
+    z[5] = torch.randn(V, device=DEV, generator=g) * 1e-4
+    z[6] = torch.randn(V, device=DEV, generator=g) * 1e-2
+    z[7] = torch.where(torch.rand(V, device=DEV, generator=g) < 0.9, 0.0, -0.5)
+    z[8] = torch.randn(V, device=DEV, generator=g)
+    z = z.to(dt)
+    for p in (0.05, 0.5, 0.95, 0.9999):
+        check(z, r.random(9), top_p=p)
+    check(z, r.random(9), top_p=r.uniform(0.1, 0.999, 9), temperature=[1, 0.3, 1, 1, 0.7, 1e-3, 1, 50, 100], top_k=V - 1000)
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
+def test_large_flat_rows_in_a_large_batch(dt):
+    """The same where rows are cut into fewer, longer slices."""
+    V, n = 262144, 76
+    g = torch.Generator(device=DEV).manual_seed(7)
+    z = torch.zeros(4, V, device=DEV)
+    z[1] = torch.randn(V, device=DEV, generator=g) * 1e-4
+    z[2] = torch.where(torch.rand(V, device=DEV, generator=g) < 0.8, 2.0, 1.9995)
+    z[3] = torch.randn(V, device=DEV, generator=g) * 0.1
+    z = z.to(dt)
+    u = np.array([0.2, 0.55, 0.8, 0.999], np.float32)
+    token, logprob, kept, kw = call(z.repeat(n // 4, 1), np.tile(u, n // 4), top_p=0.9)
+    zn, p = np64(z), float(kw["top_p"][0])
+    for i in range(4):
+        et, el, ek = serving.sample(zn[i], float(u[i]), top_p=p)
+        assert kept[i::4].tolist() == [ek] * (n // 4) and token[i::4].tolist() == [et] * (n // 4)
+        assert np.abs(np64(logprob[i::4]) - el).max() <= 2.0 ** -24 * abs(el) + 1e-9
+    assert B.kvc_check_status() == 0
