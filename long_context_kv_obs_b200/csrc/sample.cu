@@ -277,7 +277,9 @@ enum { SP_COUNT, SP_SHARE, SP_LIMBS, SP_KEYS };
 // the weight of key first - i in 2^-(31 + e) units.  A thread has one bin.
 // A CTA's words hold what its slice (40960 elements at most) can bring: 65535 or 2^(15 + 1/16) each, below
 // 2^32.  A row's need not: SHARE gives up its last e bits before the cluster's sum, and a CTA's limbs
-// (below 2^48 together) are cut anew at bit 28, so that 16 CTAs' lower halves stay below 2^32.
+// (below 2^48 together) are cut anew at bit 28, so that 16 CTAs' lower halves stay below 2^32.  (Below a
+// temperature of 2^-124 bins are wider than 1/8 octave and SHARE's words may wrap: pass D then moves on from
+// a border that is wrong.)
 template <int KS>
 __device__ __noinline__ int sp_border(int kind, double target, int C, int rank, uint32_t first, int e, float zmax,
                                       float zlow, double c, float octaves) {
@@ -976,7 +978,7 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
     // what is lighter than `mean` stays out; the bins before the last cover the rest, with a bin to spare
     const float mean = (float)fmin(0.99 * (1.0 - top_p) * bound / p.V, 0.99);
     const float range = mean > 0x1p-63f ? -log2f(mean) : 63.f;   // octaves
-    s.ybin = fminf((float)((SP_BINS - 3) * s.c) / range, 3e38f);
+    s.ybin = (float)fmin((SP_BINS - 3) * s.c / (double)range, 3e38);   // (clamped, the bins reach farther)
     const int far = SP_BINS - 2;
     const float low = s.edge_low(far), oct = s.octaves();
     unsigned* hist = s.clear_hist(SP_BINS);
@@ -1163,10 +1165,9 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
       moved = -1;
       continue;
     }
-    // weights of the bin scaled by 2^e are at most 2^(1/16): they lie within 2^-(b - 1/2) octaves of the
-    // maximum's (bf16: at or below that of the bin's largest value)
-    const int e = N == 8 ? (int)(((double)s.zmax - (double)high) * s.c) : (int)((float)b * s.octaves());
+    // weights of the bin scaled by 2^e are at most 1: none is above that of `top`
     const float zl = N == 8 ? wd.low(b) : s.edge_low(b), top = N == 8 ? high : s.edge_high(b);
+    const int e = (int)(((double)s.zmax - (double)top) * s.c);
     const int known = N == 8 && wd.single(b) ? (int)sh.total[b] : -1;
     uint32_t tk;
     int ti;

@@ -311,3 +311,16 @@ def test_large_flat_rows_in_a_large_batch(dt):
         assert kept[i::4].tolist() == [ek] * (n // 4) and token[i::4].tolist() == [et] * (n // 4)
         assert np.abs(np64(logprob[i::4]) - el).max() <= 2.0 ** -24 * abs(el) + 1e-9
     assert B.kvc_check_status() == 0
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
+def test_temperatures_at_the_lower_end(dt):
+    """Temperatures down to the least of fp32, over logits whose differences are of their size."""
+    r = np.random.default_rng(40)
+    p = [0.1, 0.3, 0.5, 0.9, 0.99, 0.9999]
+    for V in (5003, 40000):
+        base = r.standard_normal((6, V))
+        for T in (1e-45, 1e-40, 1e-38, 1e-37, 1e-36, 1e-35, 1e-30):
+            for s in (0.3, 1.0, 30.0, 1000.0):
+                z = torch.as_tensor((base * (T * s)).astype(np.float32), device=DEV).to(dt)
+                check(z, r.random(6), top_p=p, temperature=T)
