@@ -63,6 +63,35 @@ int num_sms() {
   return cache[dev];
 }
 
+// The limit is the kernel's, not a launch's, and host threads share it: a call that set it to its own size
+// could lower it between another call's setting and its launch.  So it is set once a device, to the most.
+// (Nothing here throws or locks: two threads at once set the same value.)
+cudaError_t allow_smem_of(const void* kern) {
+  struct Seen {
+    std::atomic<const void*> kern;
+    std::atomic<uint64_t> devices;              // a bit each
+  };
+  constexpr unsigned N = 256;                   // a power of two above the library's kernels; more are set at every call
+  static Seen table[N];
+  int dev = 0, most = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  Seen* seen = nullptr;
+  for (unsigned i = 0, at = (unsigned)((uintptr_t)kern >> 4); i < N && !seen; ++i, ++at) {
+    const void* k = nullptr;
+    Seen& x = table[at % N];
+    if (x.kern.compare_exchange_strong(k, kern) || k == kern) seen = &x;
+  }
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (seen && (seen->devices.load() & bit)) return cudaSuccess;
+  cudaFuncAttributes fa;
+  if ((e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess) return e;
+  if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most - (int)fa.sharedSizeBytes);
+  if (e == cudaSuccess && seen) seen->devices.fetch_or(bit);
+  return e;
+}
+
 // ----------------------------------------------------------------- helpers
 static inline size_t esize(kvc_dtype t) { return t == KVC_BF16 ? 2 : 4; }
 static inline bool dtype_ok(kvc_dtype t) { return t == KVC_F32 || t == KVC_BF16; }

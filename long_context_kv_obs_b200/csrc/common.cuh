@@ -151,4 +151,8 @@ __device__ __forceinline__ float key2f(uint32_t k) {
 namespace kvc {
 unsigned* status_ptr();           // device address of this device's status word
 int num_sms();                    // SM count of the current device
+// Lets launches of `kern` take all the dynamic shared memory that its static part leaves.
+cudaError_t allow_smem_of(const void* kern);
+template <typename... P>
+inline cudaError_t allow_smem(void (*kern)(P...)) { return allow_smem_of(reinterpret_cast<const void*>(kern)); }
 }  // namespace kvc

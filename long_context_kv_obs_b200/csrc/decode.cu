@@ -529,7 +529,7 @@ bool decode_tma_supported(const DecodeParams& p, bool bf16, bool probe) {
 template <int GM>
 static void launch_decode_tma_t(const DecodeParams& p, int grid, int nitems, cudaStream_t st) {
   auto kern = decode_tma_kernel<GM>;
-  cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dt_smem<GM>());
+  allow_smem(kern);
   kern<<<grid, DT_THREADS, dt_smem<GM>(), st>>>(p, nitems);
   count_launch();
 }
@@ -633,7 +633,7 @@ static cudaError_t launch_split_t(const DecodeParams& p, cudaStream_t st) {
   {                                                                                             \
     const size_t sm = (size_t)(DC_THREADS / 32) * GMV * rec * sizeof(float);                    \
     auto kern = decode_split_kernel<T, EPL, GMV, PROBE>;                                        \
-    cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);           \
+    allow_smem(kern);                                                                           \
     kern<<<grid, DC_THREADS, sm, st>>>(p);                                                      \
     count_launch();                                                                             \
     return cudaGetLastError();                                                                  \

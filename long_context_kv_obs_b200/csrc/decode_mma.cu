@@ -409,7 +409,7 @@ static cudaError_t launch_decode_mma_t(const DecodeParams& p, const CUtensorMap&
   if (a.nst < 2) return cudaErrorInvalidConfiguration;
   const size_t smem = fixed + (size_t)a.nst * (DM_STAGE + 16);
   auto kern = decode_mma_kernel<PROBE>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_smem(kern);
   if (e != cudaSuccess) return e;
   int grid = per_sm * num_sms();
   if (grid > a.nitems) grid = a.nitems;

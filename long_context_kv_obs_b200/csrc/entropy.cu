@@ -685,13 +685,13 @@ cudaError_t launch_entropy(const void* logits, kvc_dtype dt, int64_t rows, int64
   const int grid = (int)(want < maxb ? want : maxb);
   if (dt == KVC_BF16) {
     auto kern = entropy_twopass_kernel<__nv_bfloat16>;
-    cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    allow_smem(kern);
     kern<<<grid, nwarps * 32, smem, st>>>((const __nv_bfloat16*)logits, rows, V, row_stride, kk, cap,
                                            vec_ok, nwarps, gcap, warp_bytes, H);
     count_launch();
   } else {
     auto kern = entropy_twopass_kernel<float>;
-    cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    allow_smem(kern);
     kern<<<grid, nwarps * 32, smem, st>>>((const float*)logits, rows, V, row_stride, kk, cap, vec_ok,
                                            nwarps, gcap, warp_bytes, H);
     count_launch();

@@ -515,7 +515,7 @@ cudaError_t launch_lmhead_entropy(const LmheadParams& q, void* ws, cudaStream_t 
   a.counts = reinterpret_cast<int32_t*>(w + al(p.scratch_bytes) + al(p.lists_bytes));
   a.status = status_ptr();
   const size_t smem = lm_smem();
-  cudaError_t e = cudaFuncSetAttribute(lmh_topk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_smem(lmh_topk_kernel);
   if (e != cudaSuccess) return e;
   lmh_topk_kernel<<<p.grid, LM_THREADS, smem, st>>>(mX, mW, a);
   if ((e = cudaGetLastError())) return e;

@@ -447,7 +447,7 @@ static cudaError_t launch_po(const PrefixParams& p, const CUtensorMap& mk, const
   if (a.nst < 2) return cudaErrorInvalidConfiguration;
   const size_t smem = fixed + (size_t)a.nst * po_stage<D>();
   auto kern = prefix_own_kernel<D>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_smem(kern);
   if (e != cudaSuccess) return e;
   int grid = PO_PER_SM * num_sms();
   if (!p.counter_zeroed && (e = cudaMemsetAsync(p.counter, 0, sizeof(int), st)) != cudaSuccess) return e;

@@ -593,7 +593,7 @@ bool prefix_tc_supported(const PrefixParams& p) {
 template <int D, int MT, bool HAS_R>
 static cudaError_t launch_px(const PrefixParams& p, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t st) {
   auto kern = prefix_tc_kernel<D, MT, HAS_R>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)px_smem<D, MT>());
+  cudaError_t e = allow_smem(kern);
   if (e != cudaSuccess) return e;
   kern<<<p.grid, PX_THREADS, px_smem<D, MT>(), st>>>(mk, mv, p);
   e = cudaGetLastError();

@@ -229,8 +229,7 @@ __global__ void __launch_bounds__(RC_THREADS) recas_control_kernel(RecasCtlParam
 
 cudaError_t launch_recas_control(const RecasCtlParams& p, cudaStream_t st) {
   const size_t smem = (size_t)p.np2 * sizeof(uint64_t);
-  cudaError_t e = cudaFuncSetAttribute(recas_control_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
+  cudaError_t e = allow_smem(recas_control_kernel);
   if (e != cudaSuccess) return e;
   recas_control_kernel<<<p.rows, RC_THREADS, smem, st>>>(p);
   e = cudaGetLastError();

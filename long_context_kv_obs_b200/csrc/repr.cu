@@ -177,11 +177,11 @@ cudaError_t launch_repr(const void* hidden, kvc_dtype dt, int L, int64_t n, int 
   int64_t maxb = (int64_t)(sms > 0 ? sms : num_sms()) * 8;
   const int grid = (int)(want < maxb ? want : maxb);
   if (dt == KVC_BF16) {
-    cudaFuncSetAttribute(repr_kernel<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    allow_smem(repr_kernel<__nv_bfloat16>);
     repr_kernel<__nv_bfloat16><<<grid, REPR_WARPS * 32, smem, st>>>((const __nv_bfloat16*)hidden, L, n, Dh, vpl,
                                                                     tau, D);
   } else {
-    cudaFuncSetAttribute(repr_kernel<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    allow_smem(repr_kernel<float>);
     repr_kernel<float><<<grid, REPR_WARPS * 32, smem, st>>>((const float*)hidden, L, n, Dh, vpl, tau, D);
   }
   count_launch();

@@ -1318,7 +1318,7 @@ cudaError_t launch_sample(const SampleParams& p, cudaStream_t st) {
   cfg.attrs = &at;
   cfg.numAttrs = 1;
   auto go = [&](auto kern) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem(kern);
     if (e == cudaSuccess && C > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kern, p, per);
     if (e == cudaSuccess) count_launch();

@@ -473,7 +473,7 @@ static cudaError_t launch_sparse_row(const SparseParams& p, int rows, cudaStream
   const size_t smem = (size_t)p.max_len * sizeof(uint32_t);
   auto kern = sparse_row_kernel<G>;
   if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = allow_smem(kern);
     if (e) return e;
   }
   kern<<<rows, SPR_THREADS, smem, st>>>(p);

@@ -158,8 +158,8 @@ cudaError_t launch_window_ffma(const WinParams& p, kvc_dtype dt, cudaStream_t st
   const size_t s2 = ((size_t)p.R * p.d + (size_t)WF2_THREADS * (p.d + 1) + 3 * (size_t)p.R) * sizeof(float);
   dim3 g1(p.L * p.Hkv, p.nchunk), g2(p.L * p.Hkv, (p.n + WF2_THREADS - 1) / WF2_THREADS);
   if (dt == KVC_BF16) {
-    cudaFuncSetAttribute(win_pass1_ffma<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s1);
-    cudaFuncSetAttribute(win_pass2_ffma<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s2);
+    allow_smem(win_pass1_ffma<__nv_bfloat16>);
+    allow_smem(win_pass2_ffma<__nv_bfloat16>);
     if (!p.wlse) {
       win_pass1_ffma<__nv_bfloat16><<<g1, WF1_THREADS, s1, st>>>(p);
       count_launch();
@@ -168,8 +168,8 @@ cudaError_t launch_window_ffma(const WinParams& p, kvc_dtype dt, cudaStream_t st
     win_pass2_ffma<__nv_bfloat16><<<g2, WF2_THREADS, s2, st>>>(p);
     count_launch();
   } else {
-    cudaFuncSetAttribute(win_pass1_ffma<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s1);
-    cudaFuncSetAttribute(win_pass2_ffma<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s2);
+    allow_smem(win_pass1_ffma<float>);
+    allow_smem(win_pass2_ffma<float>);
     if (!p.wlse) {
       win_pass1_ffma<float><<<g1, WF1_THREADS, s1, st>>>(p);
       count_launch();

@@ -573,7 +573,7 @@ cudaError_t launch_window_fused(const WinParams& p, cudaStream_t st, int grid_ct
   }
   const size_t smem = fu_smem();
   auto kern = win_fused_kernel;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  e = allow_smem(kern);
   if (e != cudaSuccess) return e;
   int grid = grid_ctas > 0 && grid_ctas < num_sms() ? grid_ctas : num_sms();
   if ((int64_t)grid > a.total) grid = (int)a.total;

@@ -561,13 +561,13 @@ cudaError_t launch_window_tc(const WinParams& p, cudaStream_t st) {
   } else if (a.MT == 1) {
     a.tmem_cols = 512;                       // three 128-column accumulators
     auto k1 = win_tc_kernel<1, 1, 3, 1>;
-    cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    allow_smem(k1);
     k1<<<grid, 64 + 3 * 128, smem, st>>>(mK, mQ, a);
     count_launch();
   } else {
     a.tmem_cols = 512;                       // two 256-column accumulators, a warpgroup per M tile
     auto k1 = win_tc_kernel<1, 2, 2, 2>;
-    cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    allow_smem(k1);
     k1<<<grid, 64 + 4 * 128, smem, st>>>(mK, mQ, a);
     count_launch();
   }
@@ -579,12 +579,12 @@ cudaError_t launch_window_tc(const WinParams& p, cudaStream_t st) {
   a.tmem_cols = 512;
   if (3 * a.NC <= 512) {
     auto k2 = win_tc_kernel<2, 1, 3, 1>;
-    cudaFuncSetAttribute(k2, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    allow_smem(k2);
     k2<<<grid, 64 + 3 * 128, smem, st>>>(mK, mQ, a);
     count_launch();
   } else {
     auto k2 = win_tc_kernel<2, 1, 2, 2>;     // two warpgroups split each buffer's columns
-    cudaFuncSetAttribute(k2, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    allow_smem(k2);
     k2<<<grid, 64 + 4 * 128, smem, st>>>(mK, mQ, a);
     count_launch();
   }
