@@ -27,8 +27,6 @@
 // a (row, split) item the warps are merged in shared memory and the item's
 // partial goes to the split combine.  Persistent CTAs, two per SM, take items
 // c, c + grid, ...; the producer runs ahead across items.
-#include <cudaTypedefs.h>
-
 #include "kernels.cuh"
 #include "mma_sync.cuh"
 #include "tc_sm100.cuh"
@@ -350,24 +348,10 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
 }
 
 // ---------------------------------------------------------------- host side
-static PFN_cuTensorMapEncodeTiled_v12000 dm_encode() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  }
-  return fn;
-}
-
 // 5-D map (dim, token, KV head, layer, batch) with 64 x 32-token boxes, 128B swizzle.
 // A dimension of extent 1 gets the stride its inner neighbour implies (any legal value works).
 static bool dm_map(CUtensorMap* m, const char* base, int64_t sb, int64_t sl, int64_t sh, int64_t st,
                    const DecodeParams& p) {
-  auto enc = dm_encode();
-  if (!enc) return false;
   cuuint64_t dims[5] = {128, (cuuint64_t)p.max_len, (cuuint64_t)p.Hkv, (cuuint64_t)p.L, (cuuint64_t)p.B};
   int64_t s[4] = {st, sh, sl, sb};
   for (int i = 1; i < 4; ++i)
@@ -376,10 +360,7 @@ static bool dm_map(CUtensorMap* m, const char* base, int64_t sb, int64_t sl, int
     if (s[i] <= 0 || s[i] % 16) return false;
   cuuint64_t strides[4] = {(cuuint64_t)s[0], (cuuint64_t)s[1], (cuuint64_t)s[2], (cuuint64_t)s[3]};
   cuuint32_t box[5] = {64, DM_KEYS, 1, 1, 1};
-  cuuint32_t el[5] = {1, 1, 1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<char*>(base), dims, strides, box, el,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return tc::bf16_map(m, base, 5, dims, strides, box);
 }
 
 bool decode_mma_supported(const DecodeParams& p, bool bf16, bool probe) {

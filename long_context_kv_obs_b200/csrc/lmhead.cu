@@ -35,8 +35,6 @@
 // The segment count bounds the x tiles live in L2 at once: with S segments about SMs / S
 // row tiles run together, each re-reading its 256 x Dh slice of x for every N tile,
 // while the CTAs sweeping one segment read the same W tiles at about the same time.
-#include <cudaTypedefs.h>
-
 #include "kernels.cuh"
 #include "tc_sm100.cuh"
 
@@ -439,30 +437,13 @@ lmh_entropy_kernel(const float* __restrict__ lists, const int32_t* __restrict__ 
 }
 
 // ---------------------------------------------------------------- host side
-static PFN_cuTensorMapEncodeTiled_v12000 lm_encode() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  }
-  return fn;
-}
-
 // [rows][Dh] bf16, rows `stride` elements apart, boxes of 64 x box_rows, 128B swizzle;
 // rows and columns past the ends read as zero.
 static bool lm_map(CUtensorMap* map, const void* base, int64_t rows, int Dh, int64_t stride, int box_rows) {
-  auto enc = lm_encode();
-  if (!enc) return false;
   cuuint64_t dims[2] = {(cuuint64_t)Dh, (cuuint64_t)rows};
   cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
   cuuint32_t box[2] = {(cuuint32_t)LM_BK, (cuuint32_t)box_rows};
-  cuuint32_t es[2] = {1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return tc::bf16_map(map, base, 2, dims, strides, box);
 }
 
 LmPlan plan_lmhead(int n, int Dh, int V, int k, int sms) {

@@ -22,8 +22,6 @@
 // table entry says.  The producer's lanes hold 32 entries of the row's table at a time and each
 // issues one box.  A page id outside the pool becomes a coordinate past the map, whose box reads
 // as zeros.  Boxes wholly behind the row's end are not loaded.
-#include <cudaTypedefs.h>
-
 #include "kernels.cuh"
 #include "mma_sync.cuh"
 #include "tc_sm100.cuh"
@@ -379,18 +377,6 @@ prefix_own_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
 }
 
 // ---------------------------------------------------------------- host side
-static PFN_cuTensorMapEncodeTiled_v12000 po_encode() {
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      ptr = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  }();
-  return fn;
-}
-
 static int po_box(const PrefixParams&) { return 16; }
 
 // Byte strides of the 5-D map below; a dimension of extent 1 gets its inner neighbour's.
@@ -408,18 +394,14 @@ static bool po_strides(int64_t (&s)[4], int64_t sb, int64_t sl, int64_t sh, int6
 // 5-D map: (dim, token, KV head, layer, sequence), or (dim, token of the page, KV head, page, 1).
 static bool po_map(CUtensorMap* m, const char* base, int64_t sb, int64_t sl, int64_t sh, int64_t st,
                    const PrefixParams& p) {
-  auto enc = po_encode();
   int64_t s[4];
-  if (!enc || !po_strides(s, sb, sl, sh, st, p)) return false;
+  if (!po_strides(s, sb, sl, sh, st, p)) return false;
   const bool paged = p.table != nullptr;
   cuuint64_t dims[5] = {(cuuint64_t)p.d, (cuuint64_t)(paged ? 1 << p.shift : p.max_len), (cuuint64_t)p.Hkv,
                         (cuuint64_t)(paged ? p.n_pages : p.L), (cuuint64_t)(paged ? 1 : p.B)};
   cuuint64_t strides[4] = {(cuuint64_t)s[0], (cuuint64_t)s[1], (cuuint64_t)s[2], (cuuint64_t)s[3]};
   cuuint32_t box[5] = {64, (cuuint32_t)po_box(p), 1, 1, 1};
-  cuuint32_t el[5] = {1, 1, 1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<char*>(base), dims, strides, box, el,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return bf16_map(m, base, 5, dims, strides, box);
 }
 
 bool prefix_own_mma_supported(const PrefixParams& p) {

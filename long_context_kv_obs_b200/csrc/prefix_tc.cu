@@ -30,8 +30,6 @@
 // works on its S the tensor cores run the other's products.
 // Measured: 64 sequences (256 rows, 32 layers x 8 heads, 13107 keys) 513 us, 0.58 TFLOP with both parts of
 // P: 1.13 PFLOP/s, held by the power limit; 56 rows, 28 x 4 heads, 8200 keys with R 94 us, 4.3 TB/s.
-#include <cudaTypedefs.h>
-
 #include "kernels.cuh"
 #include "tc_sm100.cuh"
 
@@ -544,18 +542,6 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
 }
 
 // ---------------------------------------------------------------- host side
-static PFN_cuTensorMapEncodeTiled_v12000 px_encode() {
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      ptr = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  }();
-  return fn;
-}
-
 // Byte strides (token, head, layer) of the 4-D map below.  A dimension of extent 1 gets the stride its
 // inner neighbour implies (any legal value works).
 static bool px_strides(int64_t (&s)[3], int64_t sl, int64_t sh, int64_t st, const PrefixParams& p) {
@@ -570,16 +556,12 @@ static bool px_strides(int64_t (&s)[3], int64_t sl, int64_t sh, int64_t st, cons
 
 // 4-D map (dim, token, KV head, layer) with 64 x 128-token boxes, 128B swizzle.
 static bool px_map(CUtensorMap* m, const char* base, int64_t sl, int64_t sh, int64_t st, const PrefixParams& p) {
-  auto enc = px_encode();
   int64_t s[3];
-  if (!enc || !px_strides(s, sl, sh, st, p)) return false;
+  if (!px_strides(s, sl, sh, st, p)) return false;
   cuuint64_t dims[4] = {(cuuint64_t)p.d, (cuuint64_t)p.max_p, (cuuint64_t)p.Hkv, (cuuint64_t)p.L};
   cuuint64_t strides[3] = {(cuuint64_t)s[0], (cuuint64_t)s[1], (cuuint64_t)s[2]};
   cuuint32_t box[4] = {64, PX_KEYS, 1, 1};
-  cuuint32_t el[4] = {1, 1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<char*>(base), dims, strides, box, el,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return bf16_map(m, base, 4, dims, strides, box);
 }
 
 // bf16 queries and keys, at most 128 layers, and cache layouts a TMA map can describe.

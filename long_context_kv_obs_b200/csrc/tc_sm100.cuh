@@ -9,6 +9,11 @@
 namespace kvc {
 namespace tc {
 
+// A map of a bf16 tensor (dims, and strides in bytes of all but the innermost) for boxes of box[0] elements
+// in 128B-swizzled rows; what lies outside reads as zeros.  False if the driver refuses it.
+bool bf16_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+              const cuuint32_t* box);
+
 constexpr uint64_t WAIT_NS = 2000000000ull;   // 2 s: far beyond any legitimate wait
 
 // Programmatic dependent launch: the next kernel may start; the kernel before is done and its writes seen.

@@ -34,8 +34,6 @@
 // ring), warp 1 TMEM owner and tcgen05.mma issuer, warp 2 helper (partials,
 // counts, merges), warps 3.. four epilogue warpgroups (WIN_FUSED_NB) that take tiles
 // round-robin, each owning one 128-column TMEM accumulator.
-#include <cudaTypedefs.h>
-
 #include <cstddef>
 
 #include "exp2_poly.cuh"

@@ -23,8 +23,6 @@
 // Pass 2 computes S2 = K Q^T (M = 128 keys, N = G*W rows): every thread owns
 // one key and sums its normalised probabilities over the rows, so A needs no
 // cross-thread reduction; the S epilogue is fused.
-#include <cudaTypedefs.h>
-
 #include <cstddef>
 
 #include "kernels.cuh"
@@ -478,21 +476,7 @@ __global__ void __launch_bounds__(256) vnorm_kernel(const __nv_bfloat16* __restr
 }
 
 // ---------------------------------------------------------------- host side
-static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  }
-  return fn;
-}
-
 bool make_window_maps(const WinParams& p, int QR, CUtensorMap* mK, CUtensorMap* mQ) {
-  auto enc = encode_fn();
-  if (!enc) return false;
   const uint64_t es = 2;
   int64_t sl = p.Ksl, sh = p.Ksh, st = p.Kst;
   if (p.Hkv == 1) sh = st * p.n;          // unused coordinate: any legal stride
@@ -500,18 +484,11 @@ bool make_window_maps(const WinParams& p, int QR, CUtensorMap* mK, CUtensorMap* 
   cuuint64_t dK[4] = {128, (cuuint64_t)p.n, (cuuint64_t)p.Hkv, (cuuint64_t)p.L};
   cuuint64_t sK[3] = {(cuuint64_t)(st * es), (cuuint64_t)(sh * es), (cuuint64_t)(sl * es)};
   cuuint32_t bK[4] = {64, TC_KT, 1, 1};
-  cuuint32_t e4[4] = {1, 1, 1, 1};
-  CUresult r = enc(mK, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(p.K), dK, sK, bK, e4,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return false;
+  if (!tc::bf16_map(mK, p.K, 4, dK, sK, bK)) return false;
   cuuint64_t dQ[2] = {128, (cuuint64_t)p.L * p.Hq * p.W};
   cuuint64_t sQ[1] = {128 * es};
   cuuint32_t bQ[2] = {64, (cuuint32_t)QR};
-  r = enc(mQ, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p.Qw), dQ, sQ, bQ, e4,
-          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
+  return tc::bf16_map(mQ, p.Qw, 2, dQ, sQ, bQ);
 }
 
 cudaError_t launch_vnorm(const WinParams& p, cudaStream_t st) {

@@ -48,3 +48,53 @@ def test_samples_of_different_vocabularies():
     assert together(jobs) == {0}
     assert all(torch.equal(a, b) for a, b in zip(want, got))
     assert B.kvc_check_status() == 0
+
+
+def test_attention_of_different_groups_in_new_threads():
+    """Calls of threads that made no CUDA call before: their tensor maps want a context."""
+    lib, jobs, want, got, keep = B.lib(), [], [], [], []
+    for G in (1, 8, 4):
+        Bn, L, H, d, n, P = 3, 1, 2, 128, 100, 200
+        m = B.model(L, H * G, H, d)
+        q, K, V, Kp, Vp = [torch.randn(*s, device=DEV).to(torch.bfloat16)
+                           for s in ((Bn, L, H * G, d), (Bn, L, H, n, d), (Bn, L, H, n, d), (L, H, P, d), (L, H, P, d))]
+        o = torch.empty(Bn, L, H * G, d, device=DEV)
+        kw = dict(q=q, o=o, K=K, V=V, lens=torch.full((Bn, L), n, dtype=torch.int32, device=DEV), max_len=n)
+        if G > 1:
+            kw.update(K_prefix=Kp, V_prefix=Vp, lens_prefix=torch.full((L,), P, dtype=torch.int32, device=DEV), max_len_prefix=P)
+        ws = B.kvc_prefix_decode_attn(m, **kw)
+        want.append(o.clone())
+        got.append(o)
+        a = B.prefix_decode_args(m, **kw)
+        keep.append((m, a, kw, ws))
+        jobs.append(lambda s, m=m, a=a, ws=ws: lib.kvc_prefix_decode_attn(C.byref(m), C.byref(a), ws.data_ptr(), ws.numel(), s))
+    assert together(jobs) == {0}
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    assert B.kvc_check_status() == 0
+
+
+def test_decode_in_a_new_thread():
+    Bn, L, Hq, H, d, n = 2, 2, 8, 2, 128, 300
+    m = B.model(L, Hq, H, d)
+    q, K, V = [torch.randn(*s, device=DEV).to(torch.bfloat16) for s in ((Bn, L, Hq, d), (Bn, L, H, n, d), (Bn, L, H, n, d))]
+    first, o = torch.empty(Bn, L, Hq, d, device=DEV), torch.empty(Bn, L, Hq, d, device=DEV)
+    kw = dict(q=q, K=K, V=V, lens=torch.full((Bn, L), n, dtype=torch.int32, device=DEV), max_len=n)
+    before = B.kvc_launch_count()
+    ws = B.kvc_decode_attn(m, o=first, **kw)
+    launches = B.kvc_launch_count() - before
+    raised, stream = [], torch.cuda.current_stream()
+
+    def work():
+        try:
+            B.kvc_decode_attn(m, o=o, workspace=ws, stream=stream, **kw)
+        except Exception as e:                                       # noqa: BLE001
+            raised.append(e)
+
+    torch.cuda.synchronize()
+    t = threading.Thread(target=work)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert raised == [] and torch.equal(o, first)
+    assert B.kvc_launch_count() - before == 2 * launches            # by the same kernels
+    assert B.kvc_check_status() == 0
