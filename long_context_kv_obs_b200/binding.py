@@ -317,10 +317,19 @@ def workspace_size(op: int, m: Optional[Model], args) -> int:
     return n.value
 
 
-def _ws(op, m, args, workspace: Optional[torch.Tensor], device):
+def _alloc_ws(nbytes: int, device, stream) -> torch.Tensor:
+    """Memory for work on `stream` (None: the current one), from that stream's own pool: a block of another's may
+    still be in use there, and would be handed out there again while `stream` works on it."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _ws(op, m, args, workspace: Optional[torch.Tensor], device, stream):
     need = workspace_size(op, m, args)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+        workspace = _alloc_ws(max(need, 1), device, stream)
     elif workspace.numel() < need:
         raise ValueError(f"workspace of {workspace.numel()} bytes < {need}")
     return workspace, need
@@ -359,7 +368,7 @@ def kvc_score(m: Model, *, mode: int, n: int, W: int, Qw: torch.Tensor, K: torch
     a.S, a.A = _f32(S, "S"), _f32(A, "A")
     a.H_out, a.D_out, a.Ebar = _f32(H_out, "H_out"), _f32(D_out, "D_out"), _f32(Ebar, "Ebar")
     a.window_sms, a.wait_limit_ns = window_sms, wait_limit_ns
-    ws, need = _ws(OP_SCORE, m, a, workspace, K.device)
+    ws, need = _ws(OP_SCORE, m, a, workspace, K.device, stream)
     _check(lib().kvc_score(C.byref(m), C.byref(a), _p(ws), ws.numel(), _stream(stream)))
     return ws
 
@@ -376,7 +385,7 @@ def kvc_select(m: Model, *, n: int, w: int, S: torch.Tensor, k_out: torch.Tensor
     a.budget_mode, a.rho, a.k_in, a.B_total = budget_mode, rho, _i32(k_in, "k_in"), B_total
     a.Ebar = _f32(Ebar, "Ebar")
     a.k_out, a.idx, a.k_cap = _i32(k_out, "k_out"), _i32(idx, "idx"), idx.shape[-1]
-    ws, need = _ws(OP_SELECT, m, a, workspace, S.device)
+    ws, need = _ws(OP_SELECT, m, a, workspace, S.device, stream)
     _check(lib().kvc_select(C.byref(m), C.byref(a), _p(ws), ws.numel(), _stream(stream)))
     return ws
 
@@ -484,7 +493,7 @@ def decode_args(m: Model, *, q: torch.Tensor, K: torch.Tensor, V: torch.Tensor,
 def kvc_decode_attn(m: Model, *, workspace=None, stream=None, **kw):
     """Decode attention over K, V [B][L][Hkv][cap][d] for q [B][L][Hq][d] -> o (fp32)."""
     a = decode_args(m, **kw)
-    ws, need = _ws(OP_DECODE, m, a, workspace, kw["q"].device)
+    ws, need = _ws(OP_DECODE, m, a, workspace, kw["q"].device, stream)
     _check(lib().kvc_decode_attn(C.byref(m), C.byref(a), _p(ws), ws.numel(), _stream(stream)))
     return ws
 
@@ -550,7 +559,7 @@ def kvc_recompress(m: Model, *, workspace=None, stream=None, **kw):
     a = recompress_args(m, **kw)
     kept = C.c_int(-2)
     a.host_kept = C.addressof(kept)
-    ws, need = _ws(OP_RECOMPRESS, m, a, workspace, kw["K"].device)
+    ws, need = _ws(OP_RECOMPRESS, m, a, workspace, kw["K"].device, stream)
     _check(lib().kvc_recompress(C.byref(m), C.byref(a), _p(ws), ws.numel(), _stream(stream)))
     return ws, kept.value
 
@@ -577,7 +586,7 @@ def sparse_decode_args(m: Model, *, q, K, V, lens, max_len: int, pos, acc, t_cur
 def kvc_sparse_decode(m: Model, *, workspace=None, stream=None, **kw):
     """RECAS dynamic sparse decode over the retained caches (see kvc.h); returns the workspace."""
     a = sparse_decode_args(m, **kw)
-    ws, need = _ws(OP_SPARSE_DECODE, m, a, workspace, kw["q"].device)
+    ws, need = _ws(OP_SPARSE_DECODE, m, a, workspace, kw["q"].device, stream)
     _check(lib().kvc_sparse_decode(C.byref(m), C.byref(a), _p(ws), ws.numel(), _stream(stream)))
     return ws
 
@@ -600,7 +609,7 @@ def kvc_lmhead_entropy(*, x: torch.Tensor, W: torch.Tensor, H: torch.Tensor, k: 
                        stream=None):
     """Top-k entropy H [n] of softmax(W x_i) without writing the logits (see kvc.h); returns the workspace."""
     a = lmhead_entropy_args(x=x, W=W, H=H, k=k)
-    ws, need = _ws(OP_LMHEAD_ENTROPY, None, a, workspace, x.device)
+    ws, need = _ws(OP_LMHEAD_ENTROPY, None, a, workspace, x.device, stream)
     _check(lib().kvc_lmhead_entropy(C.byref(a), _p(ws), ws.numel(), _stream(stream)))
     return ws
 
@@ -751,7 +760,7 @@ def _cache(t: torch.Tensor, lead: tuple, d: int, name: str) -> KV:
 
 def _own_ws(op, m, args, workspace, device, stream):
     """(workspace, its bytes).  A workspace given is checked by the library; without one, the bytes
-    it wants are allocated here (None where none are) and held for `stream`."""
+    it wants are allocated here, for `stream` (None where none are)."""
     if workspace is not None:
         if workspace.get_device() != torch.cuda.current_device() or not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous memory of the current device")
@@ -759,10 +768,7 @@ def _own_ws(op, m, args, workspace, device, stream):
     need = workspace_size(op, m, args)
     if need == 0:
         return None, 0
-    workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    if stream is not None:
-        workspace.record_stream(stream)
-    return workspace, need
+    return _alloc_ws(need, device, stream), need
 
 
 def page_tables_args(*, lens, lens_new, table, ring, state, page: int, state_out=None, lens_out=None, slots=None,
