@@ -368,8 +368,9 @@ class SharedPromptBatch:
         """One generated token per sequence, k and v [batch][L][Hkv][d], into every layer's pages."""
         with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
             torch.add(self.lens, 1, out=self.lens_next)
+            k, v = k.flatten(0, 1), v.flatten(0, 1)                 # a copy where they cannot be viewed so
         self.resize(self.lens_next, self.slots, self.slot_start, stream)
-        B.kvc_page_append(self.m, k=k.flatten(0, 1), v=v.flatten(0, 1), K=self.K, V=self.V, slots=self.slots, stream=stream)
+        B.kvc_page_append(self.m, k=k, v=v, K=self.K, V=self.V, slots=self.slots, stream=stream)
 
     def attend(self, q, stream=None):
         """o [batch][L][Hq][d] (and self.lse) of q over the prompt and the sequences' own rows."""

@@ -3,6 +3,7 @@ import pytest
 import torch
 
 from long_context_kv_obs_b200 import binding as B
+from long_context_kv_obs_b200.pipeline import SharedPromptBatch
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -63,4 +64,30 @@ def test_a_workspace_made_by_a_call_is_its_streams_own(make):
     with torch.cuda.stream(s):
         there = [torch.empty(n, dtype=torch.uint8, device=DEV) for _ in range(200)]
     assert any(x.data_ptr() == at for x in there)
+    assert B.kvc_check_status() == 0
+
+
+def test_a_step_copies_strided_rows_on_its_own_stream():
+    """k and v as [L][B][H][d] memory cannot be viewed as rows: their copies are made, and kept, on the step's stream."""
+    Bn, L, Hq, H, d = 3, 4, 8, 2, 128
+    m = B.model(L, Hq, H, d)
+    Kp, Vp = [torch.randn(L, H, 100, d, device=DEV).to(BF) for _ in range(2)]
+    sb = SharedPromptBatch(m, Kp, Vp, i32(100, L), batch=Bn, n_pages=Bn * L, max_len=16)
+    k, v = [torch.randn(L, Bn, H, d, device=DEV).to(BF).transpose(0, 1) for _ in range(2)]
+    q = torch.randn(Bn, L, Hq, d, device=DEV).to(BF)
+    s, done = torch.cuda.Stream(), torch.cuda.Event()
+    torch.cuda.synchronize()
+    sb.step(q, v, k, stream=s)                                       # what a first step sets up
+    torch.cuda.synchronize()
+    torch.cuda._sleep(2 ** 30)                                       # half a second: the current stream is busy
+    done.record()
+    sb.step(q, k, v, stream=s)
+    s.synchronize()
+    assert not done.query()
+    torch.cuda.synchronize()
+    at = sb.slots.view(Bn, L).tolist()
+    for b in range(Bn):
+        for l in range(L):
+            page, i = divmod(at[b][l], 16)
+            assert i == 1 and torch.equal(sb.K[page, :, 1], k[b, l]) and torch.equal(sb.V[page, :, 1], v[b, l])
     assert B.kvc_check_status() == 0
