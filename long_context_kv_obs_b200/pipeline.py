@@ -331,6 +331,11 @@ class SharedPromptBatch:
     kvc_page_tables -> kvc_page_append -> kvc_prefix_decode_attn, and kvc_sample takes the next token
     from the step's logits.  Every buffer is allocated here, so a step only enqueues kernels and can be
     captured into a graph (after one step outside of it).
+
+    A row (sequence, layer) holds up to max_len tokens, max_len rounded up to whole pages, and n_pages =
+    batch * L * ceil(max_len / page) suffice for all.  A step that would take a row past that, or more
+    pages than are free, stores no sequence's token, and its attention is over what is there already:
+    kvc_check_status raises.
     """
 
     def __init__(self, m, K_prompt, V_prompt, k, *, batch: int, n_pages: int, max_len: int, page: int = 16,
@@ -338,12 +343,13 @@ class SharedPromptBatch:
         dev, dt = K_prompt.device, K_prompt.dtype
         L, Hq, Hkv, d = m.n_layers, m.n_q_heads, m.n_kv_heads, m.head_dim
         i32, f32 = torch.int32, torch.float32
-        self.m, self.batch, self.page, self.max_len = m, batch, page, max_len
+        pages = -(-max_len // page)             # a row's; what they hold is its limit
+        self.m, self.batch, self.page, self.max_len = m, batch, page, pages * page
         self.Kp, self.Vp, self.k, self.R, self.alpha_c, self.scale = K_prompt, V_prompt, k, R, alpha_c, scale
         self.max_len_prompt = K_prompt.shape[2] if max_len_prompt is None else max_len_prompt
         self.K = torch.zeros(n_pages, Hkv, page, d, dtype=dt, device=dev)
         self.V = torch.zeros(n_pages, Hkv, page, d, dtype=dt, device=dev)
-        self.table = torch.full((batch, L, -(-max_len // page)), -1, dtype=i32, device=dev)
+        self.table = torch.full((batch, L, pages), -1, dtype=i32, device=dev)
         self.lens = torch.zeros(batch, L, dtype=i32, device=dev)
         self.lens_next = torch.zeros_like(self.lens)
         self.ring = torch.arange(n_pages, dtype=i32, device=dev)

@@ -131,3 +131,74 @@ def test_the_decode_call_and_the_shared_prompt_call_agree():
     B.kvc_prefix_decode_attn(m, q=q, K_prefix=Kp, V_prefix=Vp, lens_prefix=i32(P, L), max_len_prefix=P, K=Ko, V=Vo,
                              lens=i32(n, Bn, L), max_len=n, o=o2)
     assert float((o1 - o2).abs().max()) < 2e-5
+
+
+def small_batch(Bn, L, max_len, n_pages, page=16, seed=6):
+    """A batch on a prompt of 90 and 100 rows, fp32, and a function that runs a step and checks it."""
+    Hq, H, d, P = 4, 2, 64, 100
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    draw = lambda *s: torch.randn(*s, device=DEV, generator=g)
+    m = B.model(L, Hq, H, d)
+    Kp, Vp, R = draw(L, H, P, d), draw(L, H, P, d), 1 + 3 * torch.rand(L, H, P, device=DEV, generator=g)
+    k = torch.tensor(([90, 100] * L)[:L], dtype=torch.int32, device=DEV)
+    sb = SharedPromptBatch(m, Kp, Vp, k, batch=Bn, n_pages=n_pages, max_len=max_len, page=page, R=R)
+    own = [[] for _ in range(Bn)]
+
+    def step(live=None, stored=True, **kw):
+        """One step; the rows that the sequences then hold, and how far its results are from the oracle's."""
+        q, kk, vv = draw(Bn, L, Hq, d), draw(Bn, L, H, d), draw(Bn, L, H, d)
+        o = np64(sb.step(q, kk, vv, **({} if live is None else dict(live=live)), **kw))
+        for b in range(Bn):
+            if stored and (live is None or bool(live[b])):
+                own[b].append((np64(kk[b]), np64(vv[b])))
+        worst = 0.0
+        for b in range(Bn):
+            for l in range(L):
+                for h in range(H):
+                    n, G = int(k[l]), Hq // H
+                    ko, vo = [np.array([x[i][l, h] for x in own[b]]).reshape(-1, d) for i in (0, 1)]
+                    want, lse, _ = serving.prefix_attention(np64(q[b, l, h * G:(h + 1) * G]), np64(Kp[l, h, :n]), np64(Vp[l, h, :n]),
+                                                            ko, vo, np64(R[l, h, :n]))
+                    worst = max(worst, np.abs(o[b, l, h * G:(h + 1) * G] - want).max(),
+                                np.abs(np64(sb.lse)[b, l, h * G:(h + 1) * G] - lse).max())
+        return worst
+
+    return sb, own, step
+
+
+# fp32, d = 64: a logit is off by at most gamma_64 (of 2^-23) of sum |q k| / 8 < 10, 7.6e-5; an output by twice that
+# times the values' spread of about 1, and 150 sums and weights of 2^-23.  A key left out moves a row by some 1e-2.
+STEP_ATOL = 2e-4
+
+
+def test_every_token_that_is_stored_is_attended_and_a_full_row_refuses_the_step_as_a_whole():
+    sb, own, step = small_batch(3, 2, max_len=40, n_pages=3 * 2 * 3)
+    for t in range(48):                                              # 40 tokens want three pages, which hold 48
+        assert step() < STEP_ATOL, t
+        assert B.kvc_check_status() == 0
+    assert sb.max_len == 48 and sb.lens.tolist() == [[48, 48]] * 3
+    K, table = sb.K.clone(), sb.table.clone()
+    assert step(stored=False) < STEP_ATOL                            # over what is there
+    with pytest.raises(B.KvcError):
+        B.kvc_check_status()
+    assert sb.lens.tolist() == [[48, 48]] * 3 and torch.equal(sb.K, K) and torch.equal(sb.table, table)
+    sb.resize(sb.lens * torch.tensor([[0], [1], [1]], dtype=torch.int32, device=DEV))   # one ends; the others are full
+    own[0].clear()
+    assert step(stored=False) < STEP_ATOL
+    with pytest.raises(B.KvcError):
+        B.kvc_check_status()
+
+
+def test_a_pool_one_page_short_refuses_the_step_as_a_whole():
+    sb, own, step = small_batch(3, 2, max_len=40, n_pages=3 * 2 + 5)
+    for t in range(16):
+        assert step() < STEP_ATOL
+    assert B.kvc_check_status() == 0
+    assert step(stored=False) < STEP_ATOL                            # six rows want a page, five are free
+    with pytest.raises(B.KvcError):
+        B.kvc_check_status()
+    assert sb.lens.tolist() == [[16, 16]] * 3 and int(sb.state[1]) == 5
+    sb.resize(sb.lens * torch.tensor([[1], [0], [1]], dtype=torch.int32, device=DEV))
+    own[1].clear()
+    assert step() < STEP_ATOL
+    assert B.kvc_check_status() == 0 and sb.lens.tolist() == [[17, 17], [1, 1], [17, 17]]
