@@ -335,7 +335,7 @@ class SharedPromptBatch:
     A row (sequence, layer) holds up to max_len tokens, max_len rounded up to whole pages, and n_pages =
     batch * L * ceil(max_len / page) suffice for all.  A step that would take a row past that, or more
     pages than are free, stores no sequence's token, and its attention is over what is there already:
-    kvc_check_status raises.
+    kvc_check_status raises.  Sequences that have ended, or wait, are left out of a step by `live`.
     """
 
     def __init__(self, m, K_prompt, V_prompt, k, *, batch: int, n_pages: int, max_len: int, page: int = 16,
@@ -370,13 +370,24 @@ class SharedPromptBatch:
                           page=self.page, lens_out=self.lens, slots=slots, slot_start=slot_start,
                           workspace=self.ws_tables, stream=stream)
 
-    def append(self, k, v, stream=None):
-        """One generated token per sequence, k and v [batch][L][Hkv][d], into every layer's pages."""
-        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
-            torch.add(self.lens, 1, out=self.lens_next)
+    def append(self, k, v, stream=None, live=None):
+        """One generated token per sequence, k and v [batch][L][Hkv][d], into every layer's pages.  live
+        [batch] (bool, on the device): only these sequences' rows grow; the others rest as they are (one that
+        ended, after a resize to 0, takes no page until it is live again) and their k and v go nowhere."""
+        if live is not None and (live.dtype is not torch.bool or tuple(live.shape) != (self.batch,) or live.device != self.lens.device):
+            raise ValueError(f"live must be bool [{self.batch}] on {self.lens.device}")
+        on_stream = torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+        with on_stream:
+            torch.add(self.lens, 1 if live is None else live[:, None], out=self.lens_next)
             k, v = k.flatten(0, 1), v.flatten(0, 1)                 # a copy where they cannot be viewed so
         self.resize(self.lens_next, self.slots, self.slot_start, stream)
-        B.kvc_page_append(self.m, k=k, v=v, K=self.K, V=self.V, slots=self.slots, stream=stream)
+        slots = self.slots
+        if live is not None:
+            # new slots lie row after row: back to a slot a row (all -1, from 0, where the step is refused)
+            with on_stream:
+                slots = torch.index_select(self.slots, 0, self.slot_start[:-1])
+                slots.view(self.batch, -1).masked_fill_(~live[:, None], -1)
+        B.kvc_page_append(self.m, k=k, v=v, K=self.K, V=self.V, slots=slots, stream=stream)
 
     def attend(self, q, stream=None):
         """o [batch][L][Hq][d] (and self.lse) of q over the prompt and the sequences' own rows."""
@@ -386,9 +397,9 @@ class SharedPromptBatch:
             max_len=self.max_len, o=self.o, lse=self.lse, workspace=self.ws_attn, stream=stream)
         return self.o
 
-    def step(self, q, k, v, stream=None):
-        """append, then attend."""
-        self.append(k, v, stream)
+    def step(self, q, k, v, stream=None, live=None):
+        """append, then attend (a resting sequence's q too, over the prompt and what it holds)."""
+        self.append(k, v, stream, live)
         return self.attend(q, stream)
 
     def sample(self, logits, u, stream=None, **par):

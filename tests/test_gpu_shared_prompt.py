@@ -202,3 +202,64 @@ def test_a_pool_one_page_short_refuses_the_step_as_a_whole():
     own[1].clear()
     assert step() < STEP_ATOL
     assert B.kvc_check_status() == 0 and sb.lens.tolist() == [[17, 17], [1, 1], [17, 17]]
+
+
+def test_sequences_rest_end_and_start_again():
+    L, Bn, n_pages = 2, 5, 5 * 2 * 2
+    sb, own, step = small_batch(Bn, L, max_len=32, n_pages=n_pages)
+    rng = np.random.default_rng(8)
+    mask = lambda m: torch.tensor(m, dtype=torch.bool, device=DEV)
+    for t in range(40):
+        if t % 7 == 6:                                               # one ends: its pages go back, and stay there while it rests
+            b = int(rng.integers(0, Bn))
+            keep = torch.ones(Bn, 1, dtype=torch.int32, device=DEV)
+            keep[b] = 0
+            sb.resize(sb.lens * keep)
+            own[b].clear()
+        live = [bool(x) and len(own[b]) < 32 for b, x in enumerate(rng.random(Bn) < (0.0 if t == 20 else 1.0 if t == 5 else 0.6))]
+        assert step(live=mask(live)) < STEP_ATOL, (t, live)
+        assert sb.lens.tolist() == [[len(x)] * L for x in own]
+        assert int(sb.state[1]) == n_pages - sum(-(-len(x) // 16) * L for x in own)
+    # full ones rest, the others go on
+    while min(map(len, own)) < 32:
+        assert step(live=(sb.lens[:, 0] < 32)) < STEP_ATOL
+    assert B.kvc_check_status() == 0
+    assert step(live=mask([False] * Bn)) < STEP_ATOL
+    assert B.kvc_check_status() == 0
+    assert step(live=mask([True] + [False] * (Bn - 1)), stored=False) < STEP_ATOL      # refused: the row is full
+    with pytest.raises(B.KvcError):
+        B.kvc_check_status()
+    for bad in (torch.ones(Bn, dtype=torch.int32, device=DEV), mask([True] * (Bn + 1)), torch.ones(Bn, dtype=torch.bool)):
+        with pytest.raises(ValueError):
+            step(live=bad)
+
+
+def test_a_captured_step_with_resting_sequences_replays():
+    L, Bn = 2, 6
+    sb, own, step = small_batch(Bn, L, max_len=32, n_pages=Bn * L * 2)
+    live = torch.ones(Bn, dtype=torch.bool, device=DEV)
+    assert step(live=live) < STEP_ATOL
+    q, k, v = torch.randn(Bn, L, 4, 64, device=DEV), torch.randn(Bn, L, 2, 64, device=DEV), torch.randn(Bn, L, 2, 64, device=DEV)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        sb.step(q, k, v, live=live)
+    rng = np.random.default_rng(9)
+    for _ in range(20):
+        m = rng.random(Bn) < 0.6
+        live.copy_(torch.as_tensor(m))
+        for x in (k, v):
+            x.normal_()
+        graph.replay()
+        for b in np.flatnonzero(m):
+            own[b].append((np64(k[b]), np64(v[b])))
+    assert sb.lens.tolist() == [[len(x)] * L for x in own]
+    assert step(live=~live) < STEP_ATOL                              # an eager step on the same rows sees them all
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    some, before = torch.arange(Bn, device=DEV) % 2 == 0, sb.lens.clone()
+    torch.cuda.synchronize()
+    sb.append(k, v, stream=s, live=some)
+    s.synchronize()
+    assert torch.equal(sb.lens, before + some[:, None].int())
+    assert B.kvc_check_status() == 0
