@@ -617,7 +617,7 @@ typedef struct {
  * The prompt's keys and values are read once for the batch, not once a sequence.  The own
  * cache is paged (table != NULL: K and V are pools, table row (b, l) as kvc_page_tables
  * fills it) or contiguous ([B][L][Hkv][>= max_len][d], as kvc_append fills it).  A row with
- * no key at all gets o = 0 and lse = -infinity.  A length outside its bound is clamped to it,
+ * no key at all gets o = 0 and lse = -infinity, one with a NaN logit NaN.  A length outside its bound is clamped to it,
  * a page id outside the pool reads as rows of zeros (keys and values); both are recorded in
  * the status word.  Rows behind a length may hold anything. */
 typedef struct {

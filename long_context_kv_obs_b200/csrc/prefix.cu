@@ -325,12 +325,12 @@ __global__ void __launch_bounds__(PC_THREADS) prefix_combine_kernel(const __grid
     if (grp > 0) return;
   }
   if (!live) return;
-  const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
+  const float inv = lsum == 0.f ? 0.f : 1.f / lsum;   // (a NaN among the logits makes lsum NaN, and with it the row)
   const int64_t out = (int64_t)bl * p.Hq + h;
   float4* o = reinterpret_cast<float4*>(p.o + out * D);
 #pragma unroll
   for (int q = 0; q < Q; ++q) o[q * 8 + sub] = make_float4(acc[q].x * inv, acc[q].y * inv, acc[q].z * inv, acc[q].w * inv);
-  if (p.lse && sub == 0) p.lse[out * p.lse_stride] = lsum > 0.f ? (M + log2f(lsum)) * PF_LN2 : -INFINITY;
+  if (p.lse && sub == 0) p.lse[out * p.lse_stride] = lsum == 0.f ? -INFINITY : (M + log2f(lsum)) * PF_LN2;
 }
 
 static size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }

@@ -387,3 +387,42 @@ def test_few_rows_on_a_long_prompt_wait_for_late_loads(G, merged):
     assert B.kvc_check_status() == 0
     assert torch.equal(c.o, first[0]) and torch.equal(c.lse, first[1])
     c.check()
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
+@pytest.mark.parametrize("d", [64, 128])
+def test_nan_in_a_query_or_a_key_is_seen_and_stays_in_its_rows(dt, d):
+    """By the formula: a NaN query makes its row NaN; a NaN key the rows that face it; no other row changes."""
+    nan = float("nan")
+    kw = dict(dt=dt, lens=[[40, 3], [0, 70], [5, 5]], seed=60)
+    ref = Case(3, 2, 2, 4, d, 300, 70, 16, **kw)
+    ref.run()
+    want = (ref.o.clone(), ref.lse.clone())
+
+    def check(c, bad):
+        c.run()
+        assert B.kvc_check_status() == 0
+        assert bool(torch.isnan(c.o[bad]).all()) and bool(torch.isnan(c.lse[bad]).all())
+        assert torch.equal(c.o[~bad], want[0][~bad]) and torch.equal(c.lse[~bad], want[1][~bad])
+
+    bad = lambda: torch.zeros(3, 2, 8, dtype=torch.bool, device=DEV)
+    c, b = Case(3, 2, 2, 4, d, 300, 70, 16, **kw), bad()
+    c.q[1, 0, 5, 7] = nan                                            # (over the prompt alone)
+    c.q[2, 1, 0, :] = nan
+    b[1, 0, 5] = b[2, 1, 0] = True
+    check(c, b)
+    c, b = Case(3, 2, 2, 4, d, 300, 70, 16, **kw), bad()
+    c.Kp[0, 1, 17, 3] = nan
+    b[:, 0, 4:] = True
+    check(c, b)
+    c, b = Case(3, 2, 2, 4, d, 300, 70, 16, **kw), bad()
+    c.K[int(c.table[0, 0, 1]), 0, 2, 3] = nan                        # own token 18 of sequence 0
+    b[0, 0, :4] = True
+    check(c, b)
+    c, b = Case(3, 2, 2, 4, d, 300, 70, 16, prompt=False, **kw), bad()
+    ref = Case(3, 2, 2, 4, d, 300, 70, 16, prompt=False, **kw)
+    ref.run()
+    want = (ref.o.clone(), ref.lse.clone())
+    c.q[0, 1, 2, 0] = nan
+    b[0, 1, 2] = True
+    check(c, b)
