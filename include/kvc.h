@@ -621,19 +621,19 @@ typedef struct {
  * a page id outside the pool reads as rows of zeros (keys and values); both are recorded in
  * the status word.  Rows behind a length may hold anything. */
 typedef struct {
-  int batch;
+  int batch;               /* batch * L * Hq <= 2^26, and times max_len_prefix <= 2^44 */
   const void* q;           /* [B][L][Hq][d] contiguous */
   kvc_dtype q_dtype;
   kvc_kv K_prefix, V_prefix; /* [L][Hkv][>= max_len_prefix][d] (s_batch unused); ptr NULL: no prompt */
   const int32_t* len_prefix; /* [L] device (kvc_select's k_out) */
-  int max_len_prefix;      /* host upper bound on every len_prefix[l] */
+  int max_len_prefix;      /* host upper bound on every len_prefix[l], <= 2^30 */
   const float* R;          /* NULL: no bias; else R(l,g,i) = R[l*R_s_layer + g*R_s_head + i] */
   int64_t R_s_layer, R_s_head;
   float alpha_c;
   float scale;             /* 0 selects 1/sqrt(head_dim) */
   kvc_kv K, V;             /* the sequences' own rows; ptr NULL: none */
   const int32_t* len;      /* [B][L] device */
-  int max_len;             /* host upper bound on every len[b][l] */
+  int max_len;             /* host upper bound on every len[b][l], <= 2^30 */
   const int32_t* table;    /* NULL: contiguous; else entry j of row (b, l) at
                               table[b*table_s_batch + l*table_s_layer + j], j < ceil(max_len / page) */
   int64_t table_s_batch, table_s_layer;

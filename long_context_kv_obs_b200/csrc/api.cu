@@ -1199,6 +1199,8 @@ static kvc_status run_page_append(const kvc_model* m, const kvc_page_append_args
 }
 
 // ----------------------------------------------------------------- shared-prompt decode
+static const int PREFIX_MAX_LEN = 1 << 30;      // lengths are rounded up and split in 32 bits
+
 static kvc_status check_prefix(const kvc_model* m, const kvc_prefix_decode_args* a) {
   kvc_status s = check_model(m);
   if (s) return s;
@@ -1221,6 +1223,11 @@ static kvc_status check_prefix(const kvc_model* m, const kvc_prefix_decode_args*
     if (k.dtype != v.dtype) return fail(KVC_ERR_ARG, "K_prefix and V_prefix dtypes differ");
     if (!a->len_prefix) return fail(KVC_ERR_ARG, "len_prefix is required with a prompt");
     if (a->max_len_prefix < 1) return fail(KVC_ERR_ARG, "max_len_prefix must be >= 1");
+    if (a->max_len_prefix > PREFIX_MAX_LEN) return fail(KVC_ERR_UNSUPPORTED, "max_len_prefix above 2^30");
+    // 128-key tiles of all rows, counted in 32 bits
+    const int64_t blocks = ((int64_t)a->batch * (m->n_q_heads / m->n_kv_heads) + 127) / 128;
+    if (((int64_t)a->max_len_prefix + 127) / 128 * blocks > INT_MAX / 2 / ((int64_t)m->n_layers * m->n_kv_heads))
+      return fail(KVC_ERR_UNSUPPORTED, "max_len_prefix * batch * layers * query heads above 2^44");
     if (a->R && !std::isfinite(a->alpha_c)) return fail(KVC_ERR_ARG, "alpha_c must be finite");
   } else if (a->R) {
     return fail(KVC_ERR_ARG, "R belongs to a prompt");
@@ -1233,6 +1240,7 @@ static kvc_status check_prefix(const kvc_model* m, const kvc_prefix_decode_args*
     if (a->K_prefix.ptr && k.dtype != a->K_prefix.dtype) return fail(KVC_ERR_ARG, "K and K_prefix dtypes differ");
     if (!a->len) return fail(KVC_ERR_ARG, "len is required with own rows");
     if (a->max_len < 1) return fail(KVC_ERR_ARG, "max_len must be >= 1");
+    if (a->max_len > PREFIX_MAX_LEN) return fail(KVC_ERR_UNSUPPORTED, "max_len above 2^30");
     if (a->table) {
       if ((s = check_pool(a->page, a->n_pages))) return s;
       if (a->table_s_batch < 0 || a->table_s_layer < 0) return fail(KVC_ERR_ARG, "table strides must be >= 0");

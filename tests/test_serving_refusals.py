@@ -120,6 +120,29 @@ def test_binding_refuses_host_tensors():
         B.kvc_page_tables(lens=i, lens_new=i, table=torch.zeros(4, 2, dtype=torch.int32), ring=i, state=i[:2], page=16)
 
 
+def test_prefix_decode_refuses_bounds_whose_sums_pass_32_bits():
+    lib = B.lib()
+    m = B.model(2, 8, 2, 128)
+    cache = lambda p: B.KV(p, B.KVC_BF16, 2 * 2 * 64 * 128, 2 * 64 * 128, 64 * 128, 128)
+    a = B.PrefixDecodeArgs()
+    a.batch, a.q, a.q_dtype, a.o = 3, 0x1000, B.KVC_BF16, 0x2000
+    a.K_prefix, a.V_prefix, a.len_prefix, a.max_len_prefix = cache(0x10000), cache(0x20000), 0x3000, 64
+    a.K, a.V, a.len, a.max_len = cache(0x30000), cache(0x40000), 0x4000, 64
+    n = C.c_size_t(0)
+    size = lambda: lib.kvc_workspace_size(B.OP_PREFIX_DECODE, C.byref(m), C.byref(a), C.byref(n))
+    for table in (None, 0x5000):
+        a.table, a.table_s_batch, a.table_s_layer, a.page, a.n_pages = table, 8, 4, 16, 50
+        each(a, size, [("max_len", 2 ** 30 + 1, UNSUPPORTED), ("max_len", 2 ** 31 - 1, UNSUPPORTED),
+                       ("max_len_prefix", 2 ** 30 + 1, UNSUPPORTED), ("max_len_prefix", 2 ** 31 - 1, UNSUPPORTED)])
+        a.max_len = a.max_len_prefix = 2 ** 30                       # the most: a workspace of records that fit
+        assert size() == 0 and 0 < n.value < 2 ** 34
+        a.max_len = a.max_len_prefix = 64
+    a.batch, a.max_len_prefix = 2 ** 21, 2 ** 20                      # 2^17 row blocks of 2^13 tiles
+    assert size() == UNSUPPORTED
+    a.max_len_prefix = 2 ** 10
+    assert size() == 0
+
+
 # ----------------------------------------------------------------------------- the oracle by hand
 
 def test_oracle_page_tables_by_hand():
