@@ -187,6 +187,7 @@ prefix_own_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
   uint32_t chunk = 0, merges = 0;
   for (uint32_t nq = 0;; ++nq) {
     const int q = nq % PO_Q;
+    if (nq == 1) pdl_wait();                    // as the producer does: the time limits are for what runs here, not the prompt
     bool fine = mbar_wait(&c->q_full[q], (nq / PO_Q) & 1, abort, p.status);
     if (!__all_sync(FULL, fine)) break;
     const int item = c->item[q], n = c->len[q];

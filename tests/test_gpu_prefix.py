@@ -426,3 +426,26 @@ def test_nan_in_a_query_or_a_key_is_seen_and_stays_in_its_rows(dt, d):
     c.q[0, 1, 2, 0] = nan
     b[0, 1, 2] = True
     check(c, b)
+
+
+def test_a_prompt_that_takes_seconds():
+    """Waits inside a kernel have a limit of two seconds each.  The own rows' kernel is under way while the prompt's ends: what it
+    waits for then is not its own, and the limit must not count (4 M keys times 2^20 query rows, some 3 s)."""
+    Bn, G, d, P, own = 2 ** 17, 8, 128, 4_000_000, 3
+    m = B.model(1, G, 1, d)
+    g = torch.Generator(device=DEV).manual_seed(70)
+    draw = lambda *s: torch.randn(*s, device=DEV, dtype=BF, generator=g)
+    q, Kp, Vp, K, V = draw(Bn, 1, G, d), draw(1, 1, P, d), draw(1, 1, P, d), draw(Bn, 1, 1, own, d), draw(Bn, 1, 1, own, d)
+    Kp[0, 0, -5:] *= 3                                               # keys at the end that weigh
+    K *= 3
+    o, lse = torch.empty(Bn, 1, G, d, device=DEV), torch.empty(Bn, 1, G, device=DEV)
+    B.kvc_prefix_decode_attn(m, q=q, o=o, lse=lse, K_prefix=Kp, V_prefix=Vp, lens_prefix=i32([P]), max_len_prefix=P, K=K, V=V,
+                             lens=i32(np.full((Bn, 1), own)), max_len=own)
+    assert B.kvc_check_status() == 0
+    for b in (0, 1, 777, 40000, 99999, Bn - 1):
+        z = q[b, 0].double() @ torch.cat([Kp[0, 0], K[b, 0, 0]]).double().t() / d ** 0.5
+        w, want = torch.softmax(z, -1), torch.logsumexp(z, -1)
+        # logits (below 80) to 2^-17 of them, weights to 2^-16, sums of tiles in fp32: 31250 tiles, 2^-24 of the sum each
+        assert float((lse[b, 0] - want).abs().max()) < 80 * 2 ** -17 + 31250 * 2 ** -24 + 2 ** -16
+        lim = (2 * (80 * 2 ** -17 + 2 ** -16) + 31250 * 2 ** -23) * (w @ torch.cat([Vp[0, 0], V[b, 0, 0]]).double().abs())
+        assert bool(((o[b, 0] - w @ torch.cat([Vp[0, 0], V[b, 0, 0]]).double()).abs() <= lim + 1e-6).all())
