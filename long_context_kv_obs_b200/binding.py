@@ -834,6 +834,10 @@ def prefix_decode_args(m: Model, *, q, o, K_prefix=None, V_prefix=None, lens_pre
                        R=None, alpha_c: float = 1.0, scale: float = 0.0, K=None, V=None, lens=None, max_len: int = 0,
                        table=None, lse=None) -> PrefixDecodeArgs:
     """Argument struct of kvc_prefix_decode_attn."""
+    if (K_prefix is None) != (V_prefix is None) or (K is None) != (V is None):
+        raise ValueError("keys and values belong together: K_prefix with V_prefix, K with V")
+    if table is not None and K is None:
+        raise ValueError("table belongs to K and V")
     _one_device(q, o, K_prefix, V_prefix, lens_prefix, R, K, V, lens, table, lse)
     L, Hq, H, d = m.n_layers, m.n_q_heads, m.n_kv_heads, m.head_dim
     qs = q.shape

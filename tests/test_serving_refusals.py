@@ -143,6 +143,20 @@ def test_prefix_decode_refuses_bounds_whose_sums_pass_32_bits():
     assert size() == 0
 
 
+def test_binding_refuses_halves_of_a_cache():
+    import torch
+    m = B.model(2, 8, 2, 64)
+    q, o = torch.zeros(3, 2, 8, 64), torch.zeros(3, 2, 8, 64)
+    cache, own = torch.zeros(2, 2, 10, 64), torch.zeros(3, 2, 2, 10, 64)
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    prompt = dict(K_prefix=cache, V_prefix=cache, lens_prefix=i(2), max_len_prefix=10)
+    for half in (dict(K_prefix=cache), dict(V_prefix=cache), dict(prompt, K=own), dict(prompt, V=own), dict(prompt, V_prefix=None)):
+        with pytest.raises(ValueError, match="belong together"):
+            B.kvc_prefix_decode_attn(m, q=q, o=o, lens=i(3, 2), max_len=10, **half)
+    with pytest.raises(ValueError, match="table belongs"):
+        B.kvc_prefix_decode_attn(m, q=q, o=o, table=i(3, 2, 1), lens=i(3, 2), max_len=10, **prompt)
+
+
 # ----------------------------------------------------------------------------- the oracle by hand
 
 def test_oracle_page_tables_by_hand():
