@@ -84,22 +84,6 @@ __device__ __forceinline__ void lm_drain_wait(uint64_t* bar, uint32_t parity, un
   }
 }
 
-// D[tmem] (+)= A B^T over one 64-wide K slice: four K = 16 steps, 32 bytes apart inside
-// the swizzle atom (2 in the descriptor's 16-byte address units).  `acc` = 0 makes the
-// first step overwrite D.
-__device__ __forceinline__ void mma_bf16_k64(uint32_t d_tmem, uint64_t a0, uint64_t b0, uint32_t idesc,
-                                             uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p0, p1;\n setp.ne.b32 p0, %9, 0;\n setp.eq.b32 p1, %8, %8;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %5, %8, p0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %2, %6, %8, p1;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %3, %7, %8, p1;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %4, %10, %8, p1;\n}\n" ::"r"(d_tmem),
-      "l"(a0), "l"(a0 + 2), "l"(a0 + 4), "l"(a0 + 6), "l"(b0), "l"(b0 + 2), "l"(b0 + 4), "r"(idesc),
-      "r"(acc), "l"(b0 + 6)
-      : "memory");
-}
-
 // The k largest of the c values src[0, c) (k < c <= LM_CAP), written in index order to
 // dst[0, k): the values above the k-th largest, then copies of it.  Returns the k-th
 // largest.  Warp-wide; src and dst may be the same list.  The k-th largest key t is found

@@ -367,8 +367,8 @@ size_t plan_prefix(PrefixParams& p, void* ws) {
     }
   }
   if (p.K) {
-    // items of at least 128 keys, about 12 a persistent CTA (two an SM), so that their round robin
-    // leaves little imbalance
+    // items of at least 128 keys, about 12 a persistent CTA (two an SM): drawn one by one, the last ones leave
+    // little imbalance.  The cut goes by the bound: one far above the rows' lengths makes their items few and long
     const int64_t rows = (int64_t)p.B * p.L * p.Hkv;
     int64_t ns = ((int64_t)sms * 2 * 12 + rows - 1) / rows;
     const int most = (p.max_len + 127) / 128;

@@ -18,9 +18,9 @@
 // elsewhere.  Merging the prompt's records here too, in place of a kernel of its own, doubled the
 // time: the consumers wait for those loads while the ring is full.  Every wait is an mbarrier with a
 // time limit.  Measured: 16384 rows of 175 keys on average, 1.47 GB in 260 us (5.7 TB/s); 896 rows, 270 MB, 57 us.
-// Pages: a stage is 64 / page boxes of `page` tokens (or a part of one page), each at the place its
-// table entry says.  The producer's lanes hold 32 entries of the row's table at a time and each
-// issues one box.  A page id outside the pool becomes a coordinate past the map, whose box reads
+// Pages: a stage is four boxes of 16 tokens, the smallest page, each at the place its page's table entry
+// says.  The producer's lanes hold 32 entries of the row's table at a time and four of them issue a
+// box each.  A page id outside the pool becomes a coordinate past the map, whose box reads
 // as zeros.  Boxes wholly behind the row's end are not loaded.
 #include "kernels.cuh"
 #include "mma_sync.cuh"
@@ -37,10 +37,12 @@ constexpr int PO_PER_SM = 2;
 template <int D> constexpr int po_stage() { return 2 * (D / 64) * PO_ATOM; }
 
 constexpr int PO_Q = 4;                         // items handed on at a time
+constexpr int PO_BOX = 16;                      // tokens of a box
+constexpr int PO_NB = PO_KEYS / PO_BOX;         // boxes a stage (per K / V atom)
 
 struct PoArgs {
   PrefixParams p;
-  int nitems, nst, bt;                          // bt: tokens of a box
+  int nitems, nst;
 };
 struct PoCtl {
   uint64_t full[6], empty[6];
@@ -93,7 +95,6 @@ prefix_own_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     const bool paged = p.table != nullptr;
-    const int bt = a.bt, nb = PO_KEYS / bt;     // boxes a stage (per K / V atom)
     uint32_t chunk = 0, nq = 0;
     bool ok = true;
     int drawn = blockIdx.x;
@@ -130,8 +131,8 @@ prefix_own_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
       int ent = 0, ent0 = -1;                   // entries ent0 .. ent0 + 31 of the table, one a lane
       for (int i0 = s0; i0 < s1; i0 += PO_KEYS, ++chunk) {
         const int s = chunk % NST;
-        const int tok = i0 + lane * bt;         // this lane's box, lane < nb
-        const bool box = lane < nb && tok < s1;
+        const int tok = i0 + lane * PO_BOX;     // this lane's box, lane < PO_NB
+        const bool box = lane < PO_NB && tok < s1;
         int pg = 0, off = 0;
         if (paged) {
           const int first = i0 >> p.shift;      // the stage's entries: at most 4 from here
@@ -150,12 +151,12 @@ prefix_own_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
         const unsigned boxes = __ballot_sync(FULL, box);
         if (lane == 0) {
           ok = mbar_wait(&empty[s], ((chunk / NST) & 1) ^ 1, abort, p.status);
-          if (ok) mbar_expect_tx(&full[s], (uint32_t)__popc(boxes) * bt * 128 * 2 * NA);
+          if (ok) mbar_expect_tx(&full[s], (uint32_t)__popc(boxes) * PO_BOX * 128 * 2 * NA);
         }
         ok = __shfl_sync(FULL, (int)ok, 0) != 0;
         if (!ok) break;
         if (box) {
-          uint8_t* st = ring + (size_t)s * STAGE + (size_t)lane * bt * 128;
+          uint8_t* st = ring + (size_t)s * STAGE + (size_t)lane * PO_BOX * 128;
           const int c1 = paged ? off : tok, c3 = paged ? pg : l, c4 = paged ? 0 : b;
 #pragma unroll
           for (int x = 0; x < NA; ++x) {
@@ -378,8 +379,6 @@ prefix_own_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
 }
 
 // ---------------------------------------------------------------- host side
-static int po_box(const PrefixParams&) { return 16; }
-
 // Byte strides of the 5-D map below; a dimension of extent 1 gets its inner neighbour's.
 static bool po_strides(int64_t (&s)[4], int64_t sb, int64_t sl, int64_t sh, int64_t st, const PrefixParams& p) {
   const bool paged = p.table != nullptr;
@@ -401,7 +400,7 @@ static bool po_map(CUtensorMap* m, const char* base, int64_t sb, int64_t sl, int
   cuuint64_t dims[5] = {(cuuint64_t)p.d, (cuuint64_t)(paged ? 1 << p.shift : p.max_len), (cuuint64_t)p.Hkv,
                         (cuuint64_t)(paged ? p.n_pages : p.L), (cuuint64_t)(paged ? 1 : p.B)};
   cuuint64_t strides[4] = {(cuuint64_t)s[0], (cuuint64_t)s[1], (cuuint64_t)s[2], (cuuint64_t)s[3]};
-  cuuint32_t box[5] = {64, (cuuint32_t)po_box(p), 1, 1, 1};
+  cuuint32_t box[5] = {64, PO_BOX, 1, 1, 1};
   return bf16_map(m, base, 5, dims, strides, box);
 }
 
@@ -417,7 +416,6 @@ static cudaError_t launch_po(const PrefixParams& p, const CUtensorMap& mk, const
   PoArgs a{};
   a.p = p;
   a.nitems = p.B * p.L * p.Hkv * p.nso;
-  a.bt = po_box(p);
   int dev = 0, smem_sm = 0;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&smem_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev);

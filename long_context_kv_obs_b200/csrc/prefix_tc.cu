@@ -3,8 +3,9 @@
 // For every layer l and KV head g the B * G query rows of the batch face the same len_prefix[l]
 // keys:  S = Q K^T,  P = 2^(S * qscale + alpha_c log2 R - m),  O = P V, with a running maximum m
 // and sum a row.  Every key and value is read once for the whole batch: 512 bytes (bf16,
-// d = 128) serve B * G rows, so the arithmetic per byte grows with the batch, and up to about 128 rows
-// (one M = 128 tile) the pass is bound by HBM, above it by the products.
+// d = 128) serve B * G rows, so the arithmetic per byte grows with the batch.  Up to 128 rows (one M =
+// 128 tile) the floor is HBM, and what bounds the pass is each warpgroup's chain S, maximum, weights,
+// P V (56 rows: 94 us for 62 of HBM); above that the products, under the power limit.
 //
 // P is carried as a bf16 pair hi + lo (two products with V), about 16 bits of it, so that the
 // fp32 output keeps fp32-level accuracy: with hi alone its error would be up to 2^-8 a weight.
@@ -249,7 +250,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
           const uint64_t dk = sw128_desc_at(k0 + ks * TILE, 16);
           if (elect_one()) {
             if constexpr (D == 128) mma_bf16_k128(ts, dq, dk, PX_ATOM >> 4, PX_ATOM >> 4, idS);
-            else mma_bf16_k64(ts, dq, dk, idS);
+            else mma_bf16_k64(ts, dq, dk, idS, 0);
             mma_commit(&c->s_ready[w]);
             mma_commit(&c->emptyK[ks]);
           }

@@ -35,8 +35,8 @@
 //      A bin of several values is searched again by ranges of the key, in 2^-31 units of the bin's
 //      weights, or exactly once a bin is one key.
 //   D  fp64 sums of the kept weights by 32-vector stretches of a warp, in index order.  For top-p the
-//      whole mass is summed beside them, 29 instructions an element, unless the counts bound it well
-//      enough to know the cut: then vectors that hold nothing kept cost two instructions an element
+//      whole mass is summed beside them, a weight an element, unless the counts bound it well enough to
+//      know the cut: then vectors that hold nothing kept cost a packed comparison
 //   E  the stretch, lane and element where u * total falls
 #include <cooperative_groups.h>
 
@@ -1298,16 +1298,17 @@ cudaError_t launch_sample(const SampleParams& p, cudaStream_t st) {
   // the cluster.  Few rows: slices down to 4096, for short passes, up to 16 CTAs a row (more than 8 need
   // the non-portable size) while all rows fit the GPU at once.  Many rows: slices of up to 40960, two
   // CTAs an SM, so that a search's barriers are paid by fewer CTAs
-  const int most = p.n * 8 > 4 * num_sms() ? 40960 : 16384;
+  const int64_t n = p.n;
+  const int most = n * 8 > 4 * num_sms() ? 40960 : 16384;
   int C = 1;
   while (C < 8 && (p.V + C - 1) / C > most) C <<= 1;
-  while (C < SP_MAXC && p.V / C > 4096 && p.n * 2 * C <= num_sms()) C <<= 1;
+  while (C < SP_MAXC && p.V / C > 4096 && n * 2 * C <= num_sms()) C <<= 1;
   const int unit = 32 * vn;
   const int per = ((p.V + C - 1) / C + unit - 1) / unit * unit;
   const size_t smem = sizeof(SpShared) + (size_t)per * es + (size_t)(per / unit) * sizeof(double);
   const bool aligned = (uintptr_t)p.logits % 16 == 0 && (p.n == 1 || p.row_stride * es % 16 == 0);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(p.n * C));
+  cfg.gridDim = dim3((unsigned)(n * C));
   cfg.blockDim = dim3(SP_THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;

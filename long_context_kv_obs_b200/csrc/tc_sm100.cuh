@@ -204,18 +204,19 @@ __device__ __forceinline__ void mma_bf16_k128(uint32_t d_tmem, uint64_t a0, uint
       "l"(b[1]), "l"(b[2]), "l"(b[3]), "l"(b[4]), "l"(b[5]), "l"(b[6]), "l"(b[7]), "r"(idesc)
       : "memory");
 }
-// The same over K = 64 (four steps inside one atom).
-__device__ __forceinline__ void mma_bf16_k64(uint32_t d_tmem, uint64_t a0, uint64_t b0, uint32_t idesc) {
+// D[tmem] (+)= A B^T over one 64-wide K slice: four K = 16 steps, 32 bytes apart inside
+// the swizzle atom (2 in the descriptor's 16-byte address units).  `acc` = 0 makes the
+// first step overwrite D.
+__device__ __forceinline__ void mma_bf16_k64(uint32_t d_tmem, uint64_t a0, uint64_t b0, uint32_t idesc,
+                                             uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p0, p1;\n .reg .b64 a1, a2, a3, b1, b2, b3;\n"
-      " setp.ne.b32 p0, %3, %3;\n setp.eq.b32 p1, %3, %3;\n"
-      " add.s64 a1, %1, 2;\n add.s64 a2, %1, 4;\n add.s64 a3, %1, 6;\n"
-      " add.s64 b1, %2, 2;\n add.s64 b2, %2, 4;\n add.s64 b3, %2, 6;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, p1;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, p1;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, p1;\n}\n" ::"r"(d_tmem),
-      "l"(a0), "l"(b0), "r"(idesc)
+      "{\n .reg .pred p0, p1;\n setp.ne.b32 p0, %9, 0;\n setp.eq.b32 p1, %8, %8;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %5, %8, p0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %2, %6, %8, p1;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %3, %7, %8, p1;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %4, %10, %8, p1;\n}\n" ::"r"(d_tmem),
+      "l"(a0), "l"(a0 + 2), "l"(a0 + 4), "l"(a0 + 6), "l"(b0), "l"(b0 + 2), "l"(b0 + 4), "r"(idesc),
+      "r"(acc), "l"(b0 + 6)
       : "memory");
 }
 // D[tmem] (+)= A[tmem] * B[smem]^T over K = 64 (four K = 16 steps) in one asm block.  A's rows are
