@@ -795,7 +795,21 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
     best = best == INFINITY ? 0.f : -INFINITY;
     s.zmax = 0.f;
   }
-  s.c = 1.4426950408889634 / (double)T_;
+  double temp = (double)T_;
+  if (N == 4 && s.zmax > 1e30f && T_ > 1e36f) {
+    // differences of such logits may pass fp32's range, and count at such a temperature: all are halved, the
+    // temperature too (exactly, but for the last bit of logits below 2^-125)
+#pragma unroll 1
+    for (int v = tid; v < s.nvec; v += SP_THREADS) {
+      float* e = reinterpret_cast<float*>(slice + v);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) e[j] *= 0.5f;
+    }
+    best *= 0.5f;
+    s.zmax *= 0.5f;
+    temp *= 0.5;
+  }
+  s.c = 1.4426950408889634 / temp;
   s.ybin = fminf((float)(8.0 * s.c), 3e38f);
   {
     const double x = (double)s.zmax - 64.0 / s.c;   // (an infinite temperature: -infinity, held above it)
@@ -806,7 +820,7 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
   // p_i >= min_p max p  <=>  z_i >= max z + T ln(min_p); as the least such value of the dtype's keys
   float zcut = -INFINITY;
   if (mf > 0.f) {
-    const double x = (double)s.zmax + (mf < 1.f ? (double)T_ * log((double)mf) : 0.0);
+    const double x = (double)s.zmax + (mf < 1.f ? temp * log((double)mf) : 0.0);
     zcut = x > -3.4028234663852886e38 ? __double2float_ru(x) : -INFINITY;
   }
   float u = p.u[row];

@@ -324,3 +324,22 @@ def test_temperatures_at_the_lower_end(dt):
             for s in (0.3, 1.0, 30.0, 1000.0):
                 z = torch.as_tensor((base * (T * s)).astype(np.float32), device=DEV).to(dt)
                 check(z, r.random(6), top_p=p, temperature=T)
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
+def test_logits_further_apart_than_the_range_of_fp32(dt):
+    """Rows from -3.4e38 to 3.4e38 at temperatures that make that a few octaves, or none."""
+    r = np.random.default_rng(50)
+    p = [0.1, 0.3, 0.5, 0.9, 0.99, 0.9999]
+    for V in (1001, 40000):
+        base = r.uniform(-1, 1, (6, V))
+        base[3] = np.where(r.random(V) < 0.5, -1, 1)
+        base[4] = np.where(r.random(V) < 0.5, -1, 1e-38)
+        for s in (1e30, 1e37, 2e38, 3.38e38):
+            z = torch.as_tensor((base * s).astype(np.float32), device=DEV).to(dt)
+            for T in (1.0, 1e35, 1e36, 1e37, 1e38, 3e38, INF):
+                u = r.random(6)
+                check(z, u, temperature=T, top_p=p)
+                check(z, u, temperature=T, top_p=p, top_k=[700, 1, V // 2, V // 3, V - 1, 900], min_p=0.05)
+        check(z, u, temperature=1e38)
+        check(z, u, temperature=1e38, min_p=0.3)
