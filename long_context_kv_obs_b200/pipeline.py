@@ -356,6 +356,7 @@ class SharedPromptBatch:
         self.state = torch.tensor([0, n_pages], dtype=i32, device=dev)     # head, free pages
         self.slots = torch.empty(batch * L, dtype=i32, device=dev)
         self.slot_start = torch.empty(batch * L + 1, dtype=i32, device=dev)
+        self.row_slots, self.resting = torch.empty_like(self.slots), torch.empty(batch, dtype=torch.bool, device=dev)
         self.o = torch.empty(batch, L, Hq, d, dtype=f32, device=dev)
         self.lse = torch.empty(batch, L, Hq, dtype=f32, device=dev)
         self.token = torch.empty(batch, dtype=i32, device=dev)
@@ -385,8 +386,8 @@ class SharedPromptBatch:
         if live is not None:
             # new slots lie row after row: back to a slot a row (all -1, from 0, where the step is refused)
             with on_stream:
-                slots = torch.index_select(self.slots, 0, self.slot_start[:-1])
-                slots.view(self.batch, -1).masked_fill_(~live[:, None], -1)
+                slots = torch.index_select(self.slots, 0, self.slot_start[:-1], out=self.row_slots)
+                slots.view(self.batch, -1).masked_fill_(torch.logical_not(live, out=self.resting)[:, None], -1)
         B.kvc_page_append(self.m, k=k, v=v, K=self.K, V=self.V, slots=slots, stream=stream)
 
     def attend(self, q, stream=None):
