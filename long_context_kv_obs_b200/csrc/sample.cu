@@ -1179,9 +1179,9 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p, i
       moved = -1;
       continue;
     }
-    // weights of the bin scaled by 2^e are at most 1: none is above that of `top`
+    // weights of the bin scaled by 2^e are at most 1: none is above that of `top` (past 2^-64 all are nothing)
     const float zl = N == 8 ? wd.low(b) : s.edge_low(b), top = N == 8 ? high : s.edge_high(b);
-    const int e = (int)(((double)s.zmax - (double)top) * s.c);
+    const int e = (int)fmin(((double)s.zmax - (double)top) * s.c, 100.0);
     const int known = N == 8 && wd.single(b) ? (int)sh.total[b] : -1;
     uint32_t tk;
     int ti;
